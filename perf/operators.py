@@ -14,7 +14,7 @@ own = False
 DEV = "cuda"
 E4M3_MAX = 448.0
 SCALE_EXP_MIN = -100       # smallest power-of-two scale that a page is given
-DROPPED = -1e30            # what the filtered logits hold for a dropped token
+DROPPED = -1e5             # what the filtered logits hold for a dropped token
 
 
 def listed():
