@@ -75,18 +75,33 @@ extern "C" {
 /* Logit storage types. */
 #define SSD_F32 0
 #define SSD_BF16 1
+/* Half precision: queries, keys and values of the ssd_kv_* calls only (logits are
+ * SSD_F32 or SSD_BF16). */
+#define SSD_F16 2
 
 /* Device status bits. */
 #define SSD_DEV_BAD_TOKEN 1
 #define SSD_DEV_BAD_TEMPERATURE 2
 #define SSD_DEV_NONFINITE 4
 #define SSD_DEV_TIMEOUT 8
+#define SSD_DEV_BAD_PAGE 16   /* a page or slot outside the cache */
+#define SSD_DEV_NO_PAGES 32   /* a request got no pages: too few are free */
+#define SSD_DEV_BAD_LENGTH 64 /* a negative length, or one beyond the table or the token buffers */
+#define SSD_DEV_BAD_PARAM 128 /* a sampling parameter or a uniform that is not a number in its range */
 
 /* Limits. */
 #define SSD_MAX_K 32
 #define SSD_MAX_F 256
 #define SSD_MAX_V_F32 400000
 #define SSD_MAX_V_BF16 800000
+#define SSD_KV_MAX_B 4096
+
+/* What ssd_sample's filtered logits hold for a dropped token (rounded to the
+ * logits' type).  Finite and of moderate size, so that ssd_verify and ssd_round
+ * take rows that hold little else: their running sums start from such a value,
+ * and its rounding has to stay far below the exponent range (temperatures from
+ * 1e-4).  Its weight is 0 next to any larger logit up to temperatures of 900. */
+#define SSD_DROPPED_LOGIT (-1e5f)
 
 /*
  * sigma_{F,C} descriptor of one draft row ([SSD] item 2).  Token t is in the
@@ -420,6 +435,131 @@ int ssd_round_host(const void *tgt, const void *drf, int dtype, int B, int K, in
                    int32_t *cache_tok, uint8_t *hit, int32_t *slot, void *staging,
                    size_t staging_bytes, void *workspace, size_t workspace_bytes,
                    int32_t *dev_status, size_t *h2d_bytes, void *stream);
+
+/*
+ * The loop around a round: a paged 8-bit cache of keys and values, its block
+ * tables, the attention of new tokens over it, and truncated sampling.
+ *
+ * The cache.  k_cache and v_cache are [num_pages, Hkv, page_size, D] e4m3 bytes,
+ * so that one head of one page is contiguous; k_scale and v_scale [num_pages, Hkv]
+ * fp32 hold one scale for each of those blocks, and a byte x8 stands for
+ * x8 * scale.  page_size is 16, 32, 64 or 128, D is 64 or 128, the caches are
+ * 16-byte aligned and num_pages * page_size < 2^31, as is num_pages * Hkv *
+ * page_size.  Token position j of a sequence lies in page block_table[b, j /
+ * page_size], row j % page_size; its slot is page * page_size + row.
+ */
+
+/*
+ * ssd_kv_plan -- commits the lengths that a round accepted, and gives the tokens
+ * of the next forward their pages, slots and positions ([SSD] notes: the
+ * reconciliation and rollback of the page tables after each round).
+ * State of the loop, all device int32, updated in place:
+ *   seq_len [B]      committed tokens of each sequence;
+ *   held [B]         pages that each holds: block_table[b, 0 .. held[b]) are its;
+ *   block_table [B, max_blocks];
+ *   ring [num_pages], ring_state [2] = (head, count): the free pages are
+ *                    ring[(head + i) % num_pages], i < count, first in first out.
+ * Inputs: accept_len [B] (may be NULL): the accepted lengths of the last round,
+ *   which leave accept_len + 1 more tokens committed (the token fed first and the
+ *   accepted drafts; a negative length commits none); new_len [B]: tokens that
+ *   each sequence feeds next.
+ * With keep = seq_len (+ accept_len + 1) and want = ceil((keep + new_len) /
+ * page_size): a sequence that holds fewer pages takes the rest from the ring's
+ * head, one that holds more gives the tail of its row back to the ring's end
+ * (those entries become -1), both in the order of the sequences; pages given back
+ * by a call can be taken by the next one.  A sequence is refused when the pages
+ * wanted up to and including it exceed the free ones: it keeps what it holds and
+ * its tokens get no slots (SSD_DEV_NO_PAGES).  One with a negative length, with
+ * more pages than max_blocks, or whose tokens end beyond the cap is refused too
+ * (SSD_DEV_BAD_LENGTH); a new_len below 0 counts as 0.
+ * Outputs: cu_new [B+1] int32: prefix sums of new_len (at most cap); kv_len [B]
+ *   int32: keep + new_len, or keep when refused; slots [cap], positions [cap]
+ *   int32: token i of sequence b at cu_new[b] + i has position keep + i and the
+ *   slot of that position, -1 when refused; entries from cu_new[B] on are -1 and 0.
+ * seq_len becomes keep.  Requires 1 <= B <= SSD_KV_MAX_B, cap >= 0,
+ * B * max_blocks < 2^31 and num_pages * page_size < 2^31.
+ */
+int ssd_kv_plan(int32_t *seq_len, const int32_t *accept_len, const int32_t *new_len, int32_t *held, int B,
+                int32_t *block_table, int max_blocks, int32_t *ring, int32_t *ring_state, int num_pages,
+                int page_size, int cap, int32_t *cu_new, int32_t *kv_len, int32_t *slots,
+                int32_t *positions, int32_t *dev_status, void *stream);
+
+/*
+ * ssd_kv_append -- stores the keys and values of T new tokens in the cache.
+ * k, v: [T, Hkv, D] of `dtype` (SSD_F32, SSD_BF16 or SSD_F16), heads and
+ *   channels contiguous, tokens k_stride / v_stride elements apart.
+ * slots [T] int32 (ssd_kv_plan): a negative slot is skipped; tokens of one page
+ *   are consecutive and in order, and no page is met twice in a call.
+ * For every page written and head: with amax the largest finite magnitude of the
+ * new tokens there, need = the smallest power of two 2^k, k >= -100, with
+ * amax <= 448 * 2^k.  A page whose first new token has row 0 takes scale = need;
+ * one that holds earlier tokens (the rows before its first new token) takes
+ * scale' = max(scale, need), and when that is larger its earlier rows are stored
+ * again as e4m3(x8 * (scale / scale')) (a former scale that is not a positive
+ * finite number counts as 0).  A new value is stored as e4m3(x / scale'): nearest,
+ * ties to even, beyond 448 the nearest finite; NaN stays NaN.  Infinities and NaN
+ * set SSD_DEV_NONFINITE; slots beyond the cache are skipped (SSD_DEV_BAD_PAGE).
+ */
+int ssd_kv_append(const void *k, const void *v, int dtype, int64_t k_stride, int64_t v_stride,
+                  const int32_t *slots, int T, int Hkv, int D, void *k_cache, void *v_cache, float *k_scale,
+                  float *v_scale, int num_pages, int page_size, int32_t *dev_status, void *stream);
+
+/*
+ * ssd_kv_attend -- attention of T query tokens over the cache, causal from the
+ * end: sequence b has the tokens cu_new[b] .. cu_new[b+1] of q, and token i of its
+ * n attends to the positions j <= kv_len[b] - n + i, and with window > 0 only to
+ * the last `window` of those.
+ *   score = sm_scale * <q, k8> * k_scale,  out = sum softmax(score) * v8 * v_scale
+ * q [T, Hq, D] of `dtype` (SSD_BF16 or SSD_F16), tokens q_stride elements apart,
+ *   16-byte aligned with q_stride a multiple of 8; query head h reads head
+ *   h / (Hq / Hkv) of the cache (Hq a multiple of Hkv).  out [T, Hq, D] dense.
+ * cu_new [B+1], kv_len [B] int32 as from ssd_kv_plan; max_new: a bound on the
+ *   tokens of one sequence (a longer one counts SSD_DEV_BAD_LENGTH, its tokens
+ *   beyond max_new get zeros, as does every token from cu_new[B] on).
+ * A token that attends to nothing gets zeros.  What lies in masked places of the
+ * cache, NaN among them, has no effect.  A page outside the cache counts as not
+ * there (SSD_DEV_BAD_PAGE).
+ * Sums and the softmax are held in fp32.  The 8-bit values enter the products
+ * unchanged; a query enters as the exact sum of two (bf16) or three (fp16) e4m3
+ * digits next to its row's largest, and so does each softmax weight, rounded to
+ * two or three of them (2^-8 and 2^-12 of the weight, as bf16 and fp16 would be).
+ * workspace: ssd_kv_workspace_size() bytes, 256-byte aligned, zero-filled before
+ *   its first use and left ready by each call; calls that share one must not
+ *   overlap on the GPU.
+ */
+size_t ssd_kv_workspace_size(void);
+int ssd_kv_attend(const void *q, int dtype, int64_t q_stride, const void *k_cache, const void *v_cache,
+                  const float *k_scale, const float *v_scale, int num_pages, int page_size, int Hq, int Hkv,
+                  int D, const int32_t *block_table, int max_blocks, const int32_t *cu_new,
+                  const int32_t *kv_len, int B, int T, int max_new, float sm_scale, int window, void *out,
+                  void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * ssd_sample -- one token for each of `rows` logit rows [rows, V] (rows ld >= V
+ * elements apart) under temperature and truncation.  Tokens are ranked by
+ * (logit desc, id asc); with weights w = exp((z - max z) / tau):
+ *   top_k [rows] int32 (<= 0 or >= V: off): the k first ranks;
+ *   top_p [rows] fp32 (>= 1: off): of those, each rank whose ranks above it hold
+ *     less than top_p of their weight;
+ *   min_p [rows] fp32 (0: off): of those, w >= min_p;
+ * the first rank is always kept.  tau == 0 keeps the first rank alone.  The token
+ * is the first one, in ascending id, at which the kept weight passes u times its
+ * total, as in ssd_verify's bonus draw.  top_k, top_p and min_p may each be NULL.
+ * Outputs: tokens [rows] int32; prob [rows] fp32 (may be NULL): the token's weight
+ *   among the kept; filtered (may be NULL): rows of the logits' type, ld elements
+ *   apart, where every dropped token holds SSD_DROPPED_LOGIT: logits for
+ *   ssd_verify / ssd_round that make their p and q the truncated ones.
+ * A row with a NaN or +inf logit or without a finite one (SSD_DEV_NONFINITE), a bad
+ * temperature (SSD_DEV_BAD_TEMPERATURE), a top_p or min_p that is NaN or a uniform
+ * outside [0, 1) (SSD_DEV_BAD_PARAM) gets token -1 and prob NaN; its filtered row
+ * is a copy of the logits.  A -inf logit is a token of weight 0, dropped in `filtered`.
+ * Weights are summed in 64-bit fixed point (2^-43 of the largest weight; each is
+ * exact to about 2^-28 of itself), so the sums do not depend on their order.
+ * Requires rows >= 1, 2 <= V <= SSD_MAX_V_F32 / SSD_MAX_V_BF16.
+ */
+int ssd_sample(const void *logits, int dtype, int rows, int V, int64_t ld, const float *temperature,
+               const int32_t *top_k, const float *top_p, const float *min_p, const float *uniforms,
+               int32_t *tokens, float *prob, void *filtered, int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }

@@ -27,14 +27,21 @@ SSD_ERR_UNSUPPORTED = 5
 
 SSD_F32 = 0
 SSD_BF16 = 1
+SSD_F16 = 2
 
 SSD_DEV_BAD_TOKEN = 1
 SSD_DEV_BAD_TEMPERATURE = 2
 SSD_DEV_NONFINITE = 4
 SSD_DEV_TIMEOUT = 8
+SSD_DEV_BAD_PAGE = 16
+SSD_DEV_NO_PAGES = 32
+SSD_DEV_BAD_LENGTH = 64
+SSD_DEV_BAD_PARAM = 128
 
 SSD_MAX_K = 32
 SSD_MAX_F = 256
+SSD_KV_MAX_B = 4096
+SSD_DROPPED_LOGIT = -1e5
 
 LIB_PATH = _build.LIB
 
@@ -44,7 +51,8 @@ ABI_SYMBOLS = ("ssd_strerror", "ssd_version", "ssd_workspace_size", "ssd_verify"
                "ssd_noalloc_max_scratch", "ssd_round_noalloc", "ssd_fanout_uniform",
                "ssd_backup_fill", "ssd_draft_cache", "ssd_verify_sigma", "ssd_round_sigma",
                "ssd_set_dispatch", "ssd_check_wait_timeout", "ssd_verify_ld", "ssd_round_ld",
-               "ssd_host_staging_size", "ssd_round_host", "ssd_last_kernel", "ssd_workspace_size_v")
+               "ssd_host_staging_size", "ssd_round_host", "ssd_last_kernel", "ssd_workspace_size_v",
+               "ssd_kv_plan", "ssd_kv_append", "ssd_kv_workspace_size", "ssd_kv_attend", "ssd_sample")
 
 
 class SSDError(RuntimeError):
@@ -119,6 +127,18 @@ def lib() -> ctypes.CDLL:
         L.ssd_round_host.argtypes = [P, P, i, i, i, i, P, P, P, P, i, P, P, P, P, P, P, z, P, z, P, P,
                                      P]
         L.ssd_round_host.restype = i
+        n = ctypes.c_int64
+        L.ssd_kv_plan.argtypes = [P, P, P, P, i, P, i, P, P, i, i, i, P, P, P, P, P, P]
+        L.ssd_kv_plan.restype = i
+        L.ssd_kv_append.argtypes = [P, P, i, n, n, P, i, i, i, P, P, P, P, i, i, P, P]
+        L.ssd_kv_append.restype = i
+        L.ssd_kv_workspace_size.argtypes = []
+        L.ssd_kv_workspace_size.restype = z
+        L.ssd_kv_attend.argtypes = [P, i, n, P, P, P, P, i, i, i, i, i, P, i, P, P, i, i, i, f, i, P, P, z,
+                                    P, P]
+        L.ssd_kv_attend.restype = i
+        L.ssd_sample.argtypes = [P, i, i, i, n, P, P, P, P, P, P, P, P, P, P]
+        L.ssd_sample.restype = i
         _lib = L
     return _lib
 
@@ -608,3 +628,216 @@ def ssd_draft_cache(drf, tokens, F, budget, C=1.0, *, cache=True, reshape=False,
 def desc_fields(desc: torch.Tensor):
     """Decodes reshape descriptors: (thr_val fp32, thr_id int32, F int32, C fp32) tensors."""
     return desc[:, 0].view(torch.float32), desc[:, 1], desc[:, 2], desc[:, 3].view(torch.float32)
+
+
+# ---------------------------------------------------------------------------
+# The loop around a round: the paged 8-bit cache and truncated sampling.
+# ---------------------------------------------------------------------------
+
+def _on(stream, *made):
+    """Tensors allocated here for a call on another stream than the current one: the
+    allocator must not hand their memory on before that stream has used it."""
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        for t in made:
+            if t is not None:
+                t.record_stream(s)
+
+
+def _shaped(t, name, dtype, shape):
+    _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def kv_state(B: int, max_blocks: int, num_pages: int, device=None) -> dict:
+    """The state of a loop of B sequences over a cache of num_pages pages, nothing held:
+    dict(seq_len, held, ring_state, ring, block_table), views of one int32 tensor
+    (`buffer`), so that one copy saves or restores it."""
+    head = 2 * B + 2
+    buf = torch.zeros(head + num_pages + B * max_blocks, dtype=torch.int32, device=device or "cuda")
+    buf[2 * B + 1] = num_pages
+    buf[head:head + num_pages] = torch.arange(num_pages, dtype=torch.int32, device=buf.device)
+    buf[head + num_pages:] = -1
+    return {"seq_len": buf[:B], "held": buf[B:2 * B], "ring_state": buf[2 * B:head],
+            "ring": buf[head:head + num_pages], "block_table": buf[head + num_pages:].view(B, max_blocks),
+            "buffer": buf}
+
+
+def ssd_kv_plan(seq_len, new_len, held, block_table, ring, ring_state, page_size: int, cap: int, *,
+                accept_len=None, out=None, dev_status=None, stream=None):
+    """Commits accept_len, and gives each sequence's new_len next tokens their pages and
+    slots: updates seq_len, held, block_table, ring and ring_state in place and returns
+    dict(cu_new [B+1], kv_len [B], slots [cap], positions [cap]), all int32."""
+    i32 = torch.int32
+    _dev(seq_len, "seq_len", i32)
+    if seq_len.dim() != 1:
+        raise ValueError("seq_len must be [B]")
+    B = seq_len.shape[0]
+    _shaped(new_len, "new_len", i32, (B,))
+    _shaped(held, "held", i32, (B,))
+    if accept_len is not None:
+        _shaped(accept_len, "accept_len", i32, (B,))
+    _dev(block_table, "block_table", i32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks]")
+    _dev(ring, "ring", i32)
+    _shaped(ring_state, "ring_state", i32, (2,))
+    if ring.dim() != 1:
+        raise ValueError("ring must be [num_pages]")
+    o = dict(out) if out is not None else {}
+    made = []
+    for name, shape in (("cu_new", (B + 1,)), ("kv_len", (B,)), ("slots", (int(cap),)), ("positions", (int(cap),))):
+        if name not in o:
+            o[name] = torch.empty(shape, dtype=i32, device=seq_len.device)
+            made.append(o[name])
+        _shaped(o[name], name, i32, shape)
+    _check(lib().ssd_kv_plan(
+        _ptr(seq_len), _ptr(accept_len), _ptr(new_len), _ptr(held), B, _ptr(block_table),
+        int(block_table.shape[1]), _ptr(ring), _ptr(ring_state), int(ring.shape[0]), int(page_size), int(cap),
+        _ptr(o["cu_new"]), _ptr(o["kv_len"]), _ptr(o["slots"]), _ptr(o["positions"]),
+        _ptr(_opt(dev_status, "dev_status", i32)), _stream(stream)), "ssd_kv_plan")
+    _on(stream, *made)
+    return o
+
+
+_KV_DTYPES = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16, torch.float16: SSD_F16}
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale):
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _dev(t, name)
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise TypeError(f"{name} must be float8_e4m3fn or uint8, got {t.dtype}")
+        if t.dim() != 4 or t.shape != k_cache.shape:
+            raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, D]")
+    N, H, P, D = k_cache.shape
+    _shaped(k_scale, "k_scale", torch.float32, (N, H))
+    _shaped(v_scale, "v_scale", torch.float32, (N, H))
+    return N, H, P, D
+
+
+def _tokens(t, name, H, D):
+    """Token stride of a [T, H, D] tensor whose heads and channels are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _KV_DTYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != D or (H is not None and t.shape[1] != H):
+        raise ValueError(f"{name} must be [T, {'heads' if H is None else H}, {D}]")
+    T, heads, _ = t.shape
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: heads and channels must be contiguous")
+    ld = t.stride(0) if T > 1 else heads * D
+    if ld < heads * D:
+        raise ValueError(f"{name}: tokens overlap")
+    return int(ld)
+
+
+def ssd_kv_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, *, dev_status=None, stream=None):
+    """Stores keys and values [T, Hkv, D] (views with a longer token stride are fine) at
+    `slots` of the e4m3 cache, growing the touched pages' power-of-two scales in place."""
+    N, H, P, D = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    ks, vs = _tokens(k, "k", H, D), _tokens(v, "v", H, D)
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must match in shape and dtype")
+    T = int(k.shape[0])
+    _shaped(slots, "slots", torch.int32, (T,))
+    _check(lib().ssd_kv_append(
+        _ptr(k), _ptr(v), _KV_DTYPES[k.dtype], ks, vs, _ptr(slots), T, H, D, _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), N, P, _ptr(_opt(dev_status, "dev_status", torch.int32)),
+        _stream(stream)), "ssd_kv_append")
+
+
+def kv_workspace(device=None) -> torch.Tensor:
+    """A zero-filled workspace for ssd_kv_attend (one per stream)."""
+    return torch.zeros(int(lib().ssd_kv_workspace_size()), dtype=torch.uint8, device=device or "cuda")
+
+
+def ssd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, kv_len, max_new: int,
+                  sm_scale: float, *, window: int = 0, out=None, workspace=None, dev_status=None, stream=None):
+    """Causal attention of q [T, Hq, D] (bf16 or fp16) over the paged e4m3 cache: returns
+    out [T, Hq, D].  cu_new and kv_len as from ssd_kv_plan."""
+    N, Hkv, P, D = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    ld = _tokens(q, "q", None, D)
+    T, Hq, _ = q.shape
+    _dev(kv_len, "kv_len", torch.int32)
+    if kv_len.dim() != 1:
+        raise ValueError("kv_len must be [B]")
+    B = int(kv_len.shape[0])
+    _shaped(cu_new, "cu_new", torch.int32, (B + 1,))
+    _dev(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks]")
+    made = []
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        made.append(out)
+    _shaped(out, "out", q.dtype, (T, Hq, D))
+    if workspace is None:
+        workspace = kv_workspace(q.device)
+        made.append(workspace)
+    _dev(workspace, "workspace", torch.uint8)
+    if stream is not None and made:
+        # the fill of a workspace made here runs on the current stream
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        s.wait_stream(torch.cuda.current_stream())
+    _check(lib().ssd_kv_attend(
+        _ptr(q), _KV_DTYPES[q.dtype], ld, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), N, P,
+        int(Hq), Hkv, D, _ptr(block_table), int(block_table.shape[1]), _ptr(cu_new), _ptr(kv_len), B, int(T),
+        int(max_new), float(sm_scale), int(window), _ptr(out), _ptr(workspace), workspace.numel(),
+        _ptr(_opt(dev_status, "dev_status", torch.int32)), _stream(stream)), "ssd_kv_attend")
+    _on(stream, *made)
+    return out
+
+
+def ssd_sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=None, filtered=False, tokens=None,
+               prob=None, dev_status=None, stream=None):
+    """One token per row of logits [rows, V] (rows may be a [..., :V] view of longer ones)
+    under temperature, top-k, top-p and min-p: returns dict(tokens, prob[, filtered]).
+    filtered: True, or a tensor of the logits' shape and strides, for the logits with every
+    dropped token at SSD_DROPPED_LOGIT."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    dt = _logit_dtype(logits)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, V]")
+    R, V = logits.shape
+    ld = logits.stride(0) if R > 1 else V
+    if logits.stride(1) != 1 or ld < V:
+        raise ValueError("logits: rows must be contiguous and must not overlap")
+    _shaped(temperature, "temperature", torch.float32, (R,))
+    _shaped(uniforms, "uniforms", torch.float32, (R,))
+    for t, name, dty in ((top_k, "top_k", torch.int32), (top_p, "top_p", torch.float32),
+                         (min_p, "min_p", torch.float32)):
+        if t is not None:
+            _shaped(t, name, dty, (R,))
+    made = []
+
+    def new(t, name, dty):
+        if t is None:
+            t = torch.empty(R, dtype=dty, device=logits.device)
+            made.append(t)
+        return _shaped(t, name, dty, (R,))
+
+    tokens, prob = new(tokens, "tokens", torch.int32), new(prob, "prob", torch.float32)
+    if filtered is True:
+        filtered = torch.empty((R, ld), dtype=logits.dtype, device=logits.device)[:, :V]
+        made.append(filtered)
+    elif filtered is False:
+        filtered = None
+    if filtered is not None:
+        if not isinstance(filtered, torch.Tensor) or not filtered.is_cuda or filtered.dtype != logits.dtype:
+            raise TypeError("filtered must be a CUDA tensor of the logits' dtype")
+        if filtered.shape != logits.shape or filtered.stride(1) != 1 or (R > 1 and filtered.stride(0) != ld):
+            raise ValueError("filtered must have the logits' shape and strides")
+    _check(lib().ssd_sample(
+        _ptr(logits), dt, int(R), int(V), int(ld), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+        _ptr(uniforms), _ptr(tokens), _ptr(prob), _ptr(filtered), _ptr(_opt(dev_status, "dev_status", torch.int32)),
+        _stream(stream)), "ssd_sample")
+    _on(stream, *made)
+    out = {"tokens": tokens, "prob": prob}
+    if filtered is not None:
+        out["filtered"] = filtered
+    return out

@@ -22,7 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libssd.so")
 
 SOURCES = ["ssd_unit.cu", "ssd_stream.cu", "ssd_stream_wide.cu", "ssd_slice.cu", "ssd_reshape.cu", "ssd_api.cu", "ssd_fanout.cpp", "ssd_backup.cu",
-           "ssd_diag.cu"]
+           "ssd_diag.cu", "ssd_kv_plan.cu", "ssd_kv_append.cu", "ssd_kv_attend.cu", "ssd_sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,282 @@
+// ssd_kv_append.cu -- new keys and values into the paged e4m3 cache (sm_103a).
+//
+// One scale stands for a whole (page, head) block, so a block's new tokens are looked at
+// together: their largest magnitude gives the smallest power of two that brings them into
+// e4m3's range, and where that exceeds the block's scale the tokens already there are
+// stored again under the new one.  A power of two costs e4m3 no precision (the format
+// floats), and makes that second rounding exact but for the smallest values.
+//
+// A warp takes one run (the tokens of one page, found from the slots alone: a run starts
+// where the page differs from the token before), one head, and keys or values.  Its lanes
+// hold 8 channels each, 16 bytes in and 8 bytes out, 256 / D tokens at a time; the first
+// kHold of those steps stay in registers between the search for the largest magnitude and
+// the conversion.  Bytes moved bound a prompt, the three dependent reads (slot, old scale,
+// tokens) a decoded token.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ssd_kv.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr int kHold = 8;  // steps whose values stay in registers
+
+struct AppendParams {
+    const void *x[2];  // keys, values
+    int64_t stride[2];
+    const int32_t *slots;
+    int T, H;
+    uint8_t *cache[2];
+    float *scale[2];
+    int num_pages;
+    int page_shift;
+    int chunk_shift;  // tokens that one warp looks through for starts of runs: 1 << chunk_shift
+    int64_t units;    // chunks * H * 2
+    int32_t *dev_status;
+};
+
+
+template <class E, bool kVec>
+__device__ __forceinline__ void load8(const E *p, float (&v)[8]);
+
+template <>
+__device__ __forceinline__ void load8<float, true>(const float *p, float (&v)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16, true>(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t r[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(r[i] << 16), v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
+}
+template <>
+__device__ __forceinline__ void load8<__half, true>(const __half *p, float (&v)[8]) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t r[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r[i]));
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ float wide(float x) { return x; }
+__device__ __forceinline__ float wide(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float wide(__half x) { return __half2float(x); }
+template <class E, bool kVec>
+__device__ __forceinline__ void load8(const E *p, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = wide(p[i]);
+}
+
+// Largest finite magnitude; `odd` is set when a value is not finite.
+__device__ __forceinline__ void magnitude(const float (&v)[8], float &amax, bool &odd) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float a = fabsf(v[i]);
+        const bool fine = a <= 3.402823466e38f;
+        odd |= !fine;
+        if (fine) amax = fmaxf(amax, a);
+    }
+}
+
+// The smallest power of two 2^k, k >= -100, with amax <= 448 * 2^k.  448 is 1.75 * 2^8: the
+// exponent decides, and the mantissa whether it has to be the next one.
+__device__ __forceinline__ float needed_scale(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    int k = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    k = k < -100 ? -100 : k;
+    return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+
+__device__ __forceinline__ uint2 pack8(const float (&v)[8], float inv) {
+    uint2 r;
+    r.x = e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16);
+    r.y = e4m3x2(v[4] * inv, v[5] * inv) | (e4m3x2(v[6] * inv, v[7] * inv) << 16);
+    return r;
+}
+// A scale that the cache held before need not be a power of two: divide.
+__device__ __forceinline__ uint2 pack8_div(const float (&v)[8], float scale) {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], scale);
+    return pack8(q, 1.f);
+}
+
+template <class E, int D, bool kVec>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams P) {
+    constexpr int kLanes = D / 8;          // lanes of one token
+    constexpr int kStep = 32 / kLanes;     // tokens of one step
+    const int lane = threadIdx.x & 31;
+    const int sub = lane / kLanes, ch = (lane % kLanes) * 8;
+    const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
+    if (unit >= P.units) return;
+    const int what = static_cast<int>(unit & 1);
+    const int64_t rest = unit >> 1;
+    const int h = static_cast<int>(rest % P.H);
+    const int64_t t0 = (rest / P.H) << P.chunk_shift;
+    const int chunk = 1 << P.chunk_shift;
+    const E *x = static_cast<const E *>(P.x[what]);
+    const int64_t stride = P.stride[what];
+    const int64_t cache_rows = static_cast<int64_t>(P.num_pages) << P.page_shift;
+
+    // page of each token of the chunk (one per lane), -1 for a slot that is skipped
+    const int64_t tl = t0 + lane;
+    int page = -1, before = -2;
+    if (lane < chunk && tl < P.T) {
+        const int slot = P.slots[tl];
+        if (slot >= cache_rows) report(P.dev_status, SSD_DEV_BAD_PAGE);
+        page = slot >= 0 && slot < cache_rows ? slot >> P.page_shift : -1;
+        if (tl > 0) {
+            const int s = P.slots[tl - 1];
+            before = s >= 0 && s < cache_rows ? s >> P.page_shift : -1;
+        }
+    }
+    uint32_t starts = __ballot_sync(0xFFFFFFFFu, page >= 0 && page != before);
+    while (starts) {
+        const int leader = __ffs(starts) - 1;
+        starts &= starts - 1;
+        const int64_t t = t0 + leader;
+        const int p = __shfl_sync(0xFFFFFFFFu, page, leader);
+        // length of the run: tokens from t on with the same page
+        int n = 0;
+        for (;;) {
+            const int64_t tt = t + n + lane;
+            int same = 0;
+            if (tt < P.T) {
+                const int s = P.slots[tt];
+                same = s >= 0 && s < cache_rows && (s >> P.page_shift) == p;
+            }
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, same);
+            if (m != 0xFFFFFFFFu) {
+                n += __ffs(~m) - 1;
+                break;
+            }
+            n += 32;
+        }
+        const int page_mask = (1 << P.page_shift) - 1;
+        const int row0 = P.slots[t] & page_mask;
+        const int64_t block = static_cast<int64_t>(p) * P.H + h;
+        float *scale_at = P.scale[what] + block;
+        const float scale_was = *scale_at;
+        uint8_t *rows = P.cache[what] + ((block << P.page_shift) * D);
+        const E *xt = x + t * stride + static_cast<int64_t>(h) * D + ch;
+
+        float hold[kHold][8];
+        float amax = 0.f;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int k = i * kStep + sub;
+            if (k < n) {
+                load8<E, kVec>(xt + k * stride, hold[i]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) hold[i][c] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) magnitude(hold[i], amax, odd);
+        for (int k = kHold * kStep + sub; k < n; k += kStep) {
+            float v[8];
+            load8<E, kVec>(xt + k * stride, v);
+            magnitude(v, amax, odd);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        if (__any_sync(0xFFFFFFFFu, odd) && lane == 0) report(P.dev_status, SSD_DEV_NONFINITE);
+
+        const float need = needed_scale(amax);
+        const bool had = row0 > 0 && scale_was > 0.f && scale_was <= 3.402823466e38f;
+        const float scale = had && scale_was > need ? scale_was : need;
+        if (row0 > 0 && !(had && scale_was == scale)) {
+            const float ratio = had ? __fdiv_rn(scale_was, scale) : 0.f;
+            for (int r = sub; r < row0; r += kStep) {
+                uint2 *at = reinterpret_cast<uint2 *>(rows + static_cast<int64_t>(r) * D + ch);
+                const uint2 w = *at;
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t two = halves_of_e4m3x2(((i < 2 ? w.x : w.y) >> (16 * (i & 1))) & 0xFFFFu);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&two));
+                    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+                }
+                *at = pack8(v, ratio);
+            }
+        }
+        const bool pow2 = (__float_as_uint(scale) & 0x7FFFFFu) == 0 && scale >= 7.8e-31f;
+        const float inv = pow2 ? __frcp_rn(scale) : 0.f;
+        auto store = [&](int k, const float(&v)[8]) {
+            const int s = P.slots[t + k];
+            uint2 *at = reinterpret_cast<uint2 *>(rows + static_cast<int64_t>(s & page_mask) * D + ch);
+            *at = pow2 ? pack8(v, inv) : pack8_div(v, scale);
+        };
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int k = i * kStep + sub;
+            if (k < n) store(k, hold[i]);
+        }
+        for (int k = kHold * kStep + sub; k < n; k += kStep) {
+            float v[8];
+            load8<E, kVec>(xt + k * stride, v);
+            store(k, v);
+        }
+        if (lane == 0 && !(scale_was == scale)) *scale_at = scale;
+    }
+}
+
+template <class E, int D>
+int append_launch(const AppendParams &P, bool vec, cudaStream_t stream) {
+    const int64_t blocks = (P.units * 32 + kAppendThreads - 1) / kAppendThreads;
+    if (blocks > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
+    if (vec)
+        append_kernel<E, D, true><<<static_cast<unsigned>(blocks), kAppendThreads, 0, stream>>>(P);
+    else
+        append_kernel<E, D, false><<<static_cast<unsigned>(blocks), kAppendThreads, 0, stream>>>(P);
+    return launched();
+}
+
+}  // namespace
+}  // namespace ssd
+
+extern "C" int ssd_kv_append(const void *k, const void *v, int dtype, int64_t k_stride, int64_t v_stride,
+                             const int32_t *slots, int T, int Hkv, int D, void *k_cache, void *v_cache, float *k_scale,
+                             float *v_scale, int num_pages, int page_size, int32_t *dev_status, void *stream) {
+    using namespace ssd;
+    if (dtype != SSD_F32 && dtype != SSD_BF16 && dtype != SSD_F16) return SSD_ERR_DTYPE;
+    if (T < 0 || Hkv < 1 || num_pages < 1 || !kv_page_size_ok(page_size) || (D != 64 && D != 128))
+        return SSD_ERR_INVALID_ARG;
+    if (!k_cache || !v_cache || !k_scale || !v_scale || (T > 0 && (!k || !v || !slots))) return SSD_ERR_INVALID_ARG;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return SSD_ERR_INVALID_ARG;
+    if (T > 1 && (k_stride < static_cast<int64_t>(Hkv) * D || v_stride < static_cast<int64_t>(Hkv) * D))
+        return SSD_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(num_pages) * page_size > 0x7FFFFFFF ||
+        static_cast<int64_t>(num_pages) * Hkv > 0x7FFFFFFF / page_size)
+        return SSD_ERR_UNSUPPORTED;
+    if (T == 0) return SSD_OK;
+    AppendParams P{};
+    P.x[0] = k, P.x[1] = v;
+    P.stride[0] = k_stride, P.stride[1] = v_stride;
+    P.slots = slots;
+    P.T = T, P.H = Hkv;
+    P.cache[0] = static_cast<uint8_t *>(k_cache), P.cache[1] = static_cast<uint8_t *>(v_cache);
+    P.scale[0] = k_scale, P.scale[1] = v_scale;
+    P.num_pages = num_pages;
+    P.page_shift = log2_of(page_size);
+    // as many tokens per warp as still leave 64 warps to every SM: a decoded token is a run
+    // of its own, and runs met by one warp follow one another
+    P.chunk_shift = 0;
+    while (P.chunk_shift < 4 && ((static_cast<int64_t>(T) * Hkv * 2) >> (P.chunk_shift + 1)) >= 64 * 152) ++P.chunk_shift;
+    P.units = ((static_cast<int64_t>(T) + (1 << P.chunk_shift) - 1) >> P.chunk_shift) * Hkv * 2;
+    P.dev_status = dev_status;
+    const int es = dtype == SSD_F32 ? 4 : 2;
+    const bool vec = aligned(k, 16) && aligned(v, 16) && k_stride * es % 16 == 0 && v_stride * es % 16 == 0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == SSD_F32) return D == 64 ? append_launch<float, 64>(P, vec, s) : append_launch<float, 128>(P, vec, s);
+    if (dtype == SSD_BF16)
+        return D == 64 ? append_launch<__nv_bfloat16, 64>(P, vec, s) : append_launch<__nv_bfloat16, 128>(P, vec, s);
+    return D == 64 ? append_launch<__half, 64>(P, vec, s) : append_launch<__half, 128>(P, vec, s);
+}

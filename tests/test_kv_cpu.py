@@ -1,0 +1,130 @@
+"""CPU checks of the serving loop's operators: what the library and the binding refuse before anything
+reaches a GPU, and the plain forms that the GPU tests compare with."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import _loop_ref as ref
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    from speculative_decoding_verification_ssd_gb300 import _build
+    _build.build()
+    import speculative_decoding_verification_ssd_gb300 as m
+    return m
+
+
+P = ctypes.c_void_p(0x10000)
+ODD = ctypes.c_void_p(0x10008)
+
+
+def test_plan_refuses(ssd):
+    def call(seq=P, new=P, held=P, B=4, table=P, blocks=8, ring=P, state=P, pages=100, page=16, cap=20, slots=P, pos=P, cu=P):
+        return ssd.lib().ssd_kv_plan(seq, None, new, held, B, table, blocks, ring, state, pages, page, cap, cu, P, slots, pos, None,
+                                     None)
+    bad = ssd.SSD_ERR_INVALID_ARG
+    for kw in (dict(seq=None), dict(new=None), dict(held=None), dict(table=None), dict(ring=None), dict(state=None), dict(cu=None),
+               dict(slots=None), dict(pos=None), dict(B=0), dict(blocks=0), dict(pages=0), dict(cap=-1), dict(page=24),
+               dict(page=256), dict(page=0)):
+        assert call(**kw) == bad, kw
+    for kw in (dict(B=ssd.SSD_KV_MAX_B + 1), dict(pages=2 ** 28, page=16), dict(B=4096, blocks=2 ** 20),
+               dict(B=1, blocks=2 ** 28, page=16)):
+        assert call(**kw) == ssd.SSD_ERR_UNSUPPORTED, kw
+
+
+def test_append_refuses(ssd):
+    def call(k=P, v=P, dtype=ssd.SSD_BF16, ks=1024, vs=1024, slots=P, T=3, H=8, D=128, kc=P, vc=P, sc=P, pages=10, page=16):
+        return ssd.lib().ssd_kv_append(k, v, dtype, ks, vs, slots, T, H, D, kc, vc, sc, P, pages, page, None, None)
+    for kw in (dict(k=None), dict(v=None), dict(slots=None), dict(kc=None), dict(vc=None), dict(sc=None), dict(T=-1), dict(H=0),
+               dict(D=96), dict(pages=0), dict(page=48), dict(ks=1023), dict(vs=8), dict(kc=ODD), dict(vc=ODD)):
+        assert call(**kw) == ssd.SSD_ERR_INVALID_ARG, kw
+    assert call(dtype=3) == ssd.SSD_ERR_DTYPE
+    assert call(pages=2 ** 27) == ssd.SSD_ERR_UNSUPPORTED
+    assert call(pages=2 ** 24, page=128) == ssd.SSD_ERR_UNSUPPORTED
+    assert call(T=0, k=None, v=None, slots=None) == ssd.SSD_OK
+
+
+def test_attend_refuses(ssd):
+    n = ssd.lib().ssd_kv_workspace_size()
+    assert n % 256 == 0
+
+    def call(q=P, dtype=ssd.SSD_BF16, stride=4096, kc=P, vc=P, ks=P, vs=P, pages=10, page=16, Hq=32, Hkv=8, D=128, table=P, blocks=4,
+             cu=P, kv=P, B=2, T=3, max_new=2, scale=0.1, window=0, out=P, ws=P, nbytes=n):
+        return ssd.lib().ssd_kv_attend(q, dtype, stride, kc, vc, ks, vs, pages, page, Hq, Hkv, D, table, blocks, cu, kv, B, T, max_new,
+                                       ctypes.c_float(scale), window, out, ws, nbytes, None, None)
+    for kw in (dict(q=None), dict(kc=None), dict(vc=None), dict(ks=None), dict(vs=None), dict(table=None), dict(cu=None),
+               dict(kv=None), dict(out=None), dict(q=ODD), dict(kc=ODD), dict(vc=ODD), dict(out=ODD), dict(stride=4095),
+               dict(stride=4100), dict(B=0), dict(T=-1), dict(max_new=0), dict(pages=0), dict(blocks=0), dict(Hkv=0), dict(Hq=0),
+               dict(Hq=12), dict(window=-1), dict(page=20), dict(D=32), dict(scale=float("nan")), dict(scale=float("inf"))):
+        assert call(**kw) == ssd.SSD_ERR_INVALID_ARG, kw
+    for dtype in (ssd.SSD_F32, 7):
+        assert call(dtype=dtype) == ssd.SSD_ERR_DTYPE
+    for kw in (dict(ws=None), dict(ws=ODD), dict(nbytes=n - 1)):
+        assert call(**kw) == ssd.SSD_ERR_WORKSPACE, kw
+    for kw in (dict(pages=2 ** 27), dict(pages=2 ** 25), dict(B=2048, blocks=2 ** 20), dict(blocks=2 ** 27), dict(B=5000)):
+        assert call(**kw) == ssd.SSD_ERR_UNSUPPORTED, kw
+    assert call(T=0, q=None, out=None) == ssd.SSD_OK
+
+
+def test_sample_refuses(ssd):
+    def call(z=P, dtype=ssd.SSD_F32, rows=2, V=100, ld=100, tau=P, u=P, tokens=P):
+        return ssd.lib().ssd_sample(z, dtype, rows, V, ld, tau, None, None, None, u, tokens, None, None, None, None)
+    for kw in (dict(z=None), dict(tau=None), dict(u=None), dict(tokens=None), dict(rows=0), dict(V=1), dict(ld=99)):
+        assert call(**kw) == ssd.SSD_ERR_INVALID_ARG, kw
+    assert call(dtype=ssd.SSD_F16) == ssd.SSD_ERR_DTYPE
+    assert call(V=400001, ld=400001) == ssd.SSD_ERR_UNSUPPORTED
+    assert call(dtype=ssd.SSD_BF16, V=800001, ld=800001) == ssd.SSD_ERR_UNSUPPORTED
+
+
+def test_binding_refuses_host_tensors(ssd):
+    i, f = torch.zeros(2, dtype=torch.int32), torch.zeros(2)
+    with pytest.raises(TypeError):
+        ssd.ssd_kv_plan(i, i, i, i.view(2, 1), i, i, 16, 2)
+    c, s = torch.zeros((2, 1, 16, 64), dtype=torch.uint8), torch.zeros((2, 1))
+    x = torch.zeros((2, 1, 64), dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        ssd.ssd_kv_append(x, x, i, c, c, s, s)
+    with pytest.raises(TypeError):
+        ssd.ssd_kv_attend(x, c, c, s, s, i.view(1, 2), i, i[:1], 1, 1.0)
+    with pytest.raises(TypeError):
+        ssd.ssd_sample(torch.zeros((2, 9)), f, f)
+
+
+def test_e4m3_rounding_of_the_plain_form():
+    """Against torch's conversion, over every halfway point and its neighbours."""
+    pos = ref.e4m3_values()[:127]
+    mid = (pos[1:] + pos[:-1]) / 2
+    x = np.concatenate([pos, mid, np.nextafter(mid.astype(np.float32), np.float32(1e9)),
+                        np.nextafter(mid.astype(np.float32), np.float32(0)), [1e-9, 448.0]]).astype(np.float32)
+    x = np.concatenate([x, -x])
+    want = torch.from_numpy(x).to(torch.float8_e4m3fn).to(torch.float64).numpy()
+    np.testing.assert_array_equal(ref.to_e4m3(x), want)
+    np.testing.assert_array_equal(ref.e4m3_values(), torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy())
+
+
+def test_digits_of_a_query_are_exact():
+    """A bf16 value is the sum of two e4m3 digits, an fp16 value of three, while it lies within 2^14 of the row's largest."""
+    for bits, digits in ((8, 2), (11, 3)):
+        m = np.arange(2 ** (bits - 1), 2 ** bits, dtype=np.float64) / 2 ** (bits - 1)
+        for e in range(-6, 8):
+            x = rest = m * 2.0 ** e
+            got = np.zeros_like(x)
+            for d in range(digits):
+                t = ref.to_e4m3(rest * 16.0 ** d) / 16.0 ** d
+                got, rest = got + t, rest - t
+            np.testing.assert_array_equal(got, x)
+
+
+def test_plain_sample_keeps_prefixes():
+    z = np.log(np.array([0.1, 0.4, 0.2, 0.3]))
+    assert ref.sample(z, 1.0, 2, 1.0, 0.0, 0.5)[2].tolist() == [1, 3]
+    assert ref.sample(z, 1.0, 0, 0.75, 0.0, 0.5)[2].tolist() == [1, 2, 3]
+    assert ref.sample(z, 1.0, 0, 1.0, 0.6, 0.5)[2].tolist() == [1, 3]
+    assert ref.sample(z, 1.0, 0, 1.0, 0.0, 0.55)[0] == 2
+    assert ref.sample(z, 0.0, 0, 1.0, 0.0, 0.9)[0] == 1
+    token, prob, _, _ = ref.sample(z, 1.0, 2, 1.0, 0.0, 0.99)
+    assert token == 3 and abs(prob - 3 / 7) < 1e-12
