@@ -40,9 +40,7 @@ namespace ssd {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kAttendWarps = 11;
-constexpr int kAttendThreads = 32 * kAttendWarps;
-constexpr int kMaxCtas = 320;
+constexpr int kMaxCtas = 160;
 constexpr int kMaxRows = 64;
 constexpr int kMaxHead = 128;
 constexpr int kSeqsInside = 512;   // sequences whose prefix sums every CTA makes itself
@@ -62,7 +60,7 @@ struct Workspace {
     float2 ml[2 * kMaxCtas][kMaxRows];
     Join join[kMaxCtas];
     int32_t pairs;              // of the schedule below
-    int32_t sums[kMaxPairs + 1];  // tiles before each pair
+    int32_t sums[kMaxPairs + 1];  // steps before each pair
     int32_t seq[kMaxPairs];
     int32_t row0[kMaxPairs];
     int32_t start[kMaxCtas + 1];  // pair in which each CTA's stretch starts
@@ -81,8 +79,8 @@ struct AttendParams {
     float scale;  // sm_scale * log2(e): scores are held in base 2
     int window;
     int rows_per_item;
+    int step_shift;  // log2 of the keys of one step
     int inside;  // the schedule is made by every CTA in shared memory
-    int slots;   // of the K/V ring
     void *out;
     Workspace *ws;
     int32_t *dev_status;
@@ -101,9 +99,9 @@ __device__ __forceinline__ Seq load_seq(const AttendParams &P, int b) {
     return s;
 }
 
-// The keys of rows [row0, row1) of a sequence: [start, stop), in tiles tile0 .. tile0 + tiles.
+// The keys of rows [row0, row1) of a sequence: [start, stop), in steps step0 .. step0 + steps.
 struct Span {
-    int start, stop, tile0, tiles;
+    int start, stop, step0, steps;
 };
 __device__ __forceinline__ Span key_span(const AttendParams &P, const Seq &s, int row0, int row1) {
     const int low = s.pos0 + row0 / P.G, high = s.pos0 + (row1 - 1) / P.G;
@@ -111,11 +109,11 @@ __device__ __forceinline__ Span key_span(const AttendParams &P, const Seq &s, in
     k.start = P.window > 0 ? max(0, low + 1 - P.window) : 0;
     k.stop = min(high + 1, P.max_blocks << P.page_shift);
     if (k.stop > k.start) {
-        k.tile0 = k.start / kTile;
-        k.tiles = (k.stop + kTile - 1) / kTile - k.tile0;
-    } else {  // nothing to attend to: one tile without keys writes the zeros
-        k.start = k.stop = k.tile0 = 0;
-        k.tiles = 1;
+        k.step0 = k.start >> P.step_shift;
+        k.steps = ((k.stop - 1) >> P.step_shift) + 1 - k.step0;
+    } else {  // nothing to attend to: one step without keys writes the zeros
+        k.start = k.stop = k.step0 = 0;
+        k.steps = 1;
     }
     return k;
 }
@@ -129,9 +127,9 @@ struct Part {
     int b, head, row0, rows;
     int first, pos0;      // of the sequence
     int start, stop;      // keys that any row attends to
-    int tile, tiles;      // this part's tiles
+    int step, steps;      // this part's
     bool from_start, to_end;
-    int last_cta;         // CTA that holds the item's last tile
+    int last_cta;         // CTA that holds the item's last step
 };
 
 struct Walk {
@@ -151,16 +149,16 @@ struct Walk {
         part.rows = min(P.rows_per_item, s.n * P.G - part.row0);
         const Span k = key_span(P, s, part.row0, part.row0 + part.rows);
         part.start = k.start, part.stop = k.stop;
-        const int all = span / P.Hkv;  // == k.tiles
+        const int all = span / P.Hkv;  // == k.steps
         part.head = (unit - base) / all;
         const int done = (unit - base) - part.head * all;
-        part.tile = k.tile0 + done;
-        part.tiles = min(all - done, end - unit);
+        part.step = k.step0 + done;
+        part.steps = min(all - done, end - unit);
         part.from_start = done == 0;
-        part.to_end = done + part.tiles == all;
+        part.to_end = done + part.steps == all;
         const int64_t item_end = static_cast<int64_t>(base) + static_cast<int64_t>(part.head + 1) * all;
         part.last_cta = static_cast<int>((item_end * ctas - 1) / units);
-        unit += part.tiles;
+        unit += part.steps;
         return true;
     }
 };
@@ -227,7 +225,7 @@ __global__ void __launch_bounds__(kScheduleThreads) schedule_kernel(const __grid
             const int b = last_not_above(blocks, P.B, p);
             const int row0 = (p - blocks[b]) * P.rows_per_item;
             const Seq s = load_seq(P, b);
-            v = key_span(P, s, row0, min(row0 + P.rows_per_item, s.n * P.G)).tiles * P.Hkv;
+            v = key_span(P, s, row0, min(row0 + P.rows_per_item, s.n * P.G)).steps * P.Hkv;
             W.seq[p] = b;
             W.row0[p] = row0;
         }
@@ -262,43 +260,61 @@ constexpr int digits_of() {
 template <class E_, int kD_, int kR_>
 struct Form {
     using E = E_;
-    static constexpr int D = kD_, R = kR_;
+    static constexpr int D = kD_, R = kR_;  // channels, most rows of an item
     static constexpr int kDigits = digits_of<E>();
-    static constexpr int N = (R * kDigits + 15) / 16 * 16;              // columns of S and O
-    static constexpr int kPitch = N <= 32 ? 32 : (N <= 64 ? 64 : 128);  // bytes of weights per key
-    static constexpr int kColumns = 4 * N <= 64 ? 64 : (4 * N <= 128 ? 128 : (4 * N <= 256 ? 256 : 512));
-    static constexpr int kCtas = kColumns <= 256 ? 2 : 1;  // per SM
-    static constexpr int kSlot = kTile * D;
-    static constexpr int kQ = (N * D + 1023) / 1024 * 1024;
-    static constexpr int kP = kTile * kPitch;
-    static_assert(N <= 128 && 4 * N <= kColumns);
+    static constexpr int N = R;  // columns set aside for S and O
+    // tiles of 128 keys in one step: two, unless the weights' digits then leave too few slots for K and V
+    static constexpr int kSub = R > 32 && kDigits == 3 && D == 128 ? 1 : 2;
+    static constexpr int kStep = kSub * kTile;
+    static constexpr int kPitch = R;  // bytes of one digit of a key's weights
+    // fp16 outputs: the weights' second and third digits are of 32 times what is left, and summed apart
+    static constexpr int kOut = kDigits == 3 ? 2 : 1;
+    static constexpr float kFine = 32.f;
+    static constexpr int kUsed = (2 * kSub + 2 * kOut) * N;
+    static constexpr int kColumns = kUsed <= 256 ? 256 : 512;
+    static constexpr int kSlot = kStep * D;
+    static constexpr int kQ = N * D;           // one digit of the queries
+    static constexpr int kP = kStep * kPitch;  // one digit of the weights
+    static_assert((R == 32 || R == 64) && kUsed <= kColumns && kQ % 1024 == 0 && kP % 1024 == 0);
 };
 
-// Waits are bounded.  When one runs out, `gave_up` is set and every role goes on through its
-// loop without waiting, loading or multiplying, so that all of them reach the end together.
-constexpr uint64_t kSliceNs = 50000000;
-constexpr int kSlices = 80;  // 4 s
-__device__ __forceinline__ void wait_phase(uint64_t *bar, uint32_t parity, int *gave_up) {
-    if (mbar_test_wait(bar, parity) || *static_cast<volatile int *>(gave_up)) return;
-    for (int i = 0; i < kSlices; ++i) {
-        if (mbar_wait_suspend_for(bar, parity, kSliceNs)) return;
-        if (*static_cast<volatile int *>(gave_up)) return;
-    }
-    *static_cast<volatile int *>(gave_up) = 1;
-}
-
-constexpr int kRowRing = 4;  // items whose row data may be in use at once
+constexpr int kAttendWarps = 16;  // softmax 2 x 4, output 4, TMA, MMA, queries, scout
+constexpr int kAttendThreads = 32 * kAttendWarps;
+constexpr int kSteps = 8;    // steps that the scout may be ahead
+constexpr int kItems = 8;    // items whose row data may be in use at once
 constexpr int kMaxSlots = 12;
+constexpr int kSharedBytes = 227 * 1024;  // of one CTA
+constexpr int kConsumers = 4 + 4 + 3;  // warps that read one step: a softmax group, output, TMA, MMA, queries
+
+// One step of a CTA's stretch: up to kStep keys of one item.
+struct Step {
+    int32_t live;       // 0: the stretch has ended
+    int32_t first, last;  // of its part
+    int32_t plain;      // every row attends to every key, and every page is there
+    int32_t odd;        // a value scale is not finite
+    int32_t key0, subs;  // first key, tiles in use
+    int32_t start, stop;  // keys that some row attends to
+    int32_t common_from, common_to;  // ... and that every row does
+    int32_t there;      // bit p: page p is there
+    int32_t item;       // row data of kItems
+    int32_t from_start, to_end, last_cta;
+    int32_t seq, head, row0, rows, token0, pos0;
+    int32_t part_key0;  // first key of the part
+    float v_unit;       // what the weights' value scales were divided by
+    int32_t page[16];
+    float2 scale[16];   // of the keys, and of the values over v_unit
+};
 
 template <int R>
 struct Shared {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
+    uint64_t step_full[kSteps], step_free[kSteps];
     uint64_t s_full[2], s_free[2], p_full[2], o_full[2], o_free[2], q_full, q_free, drained;
-    float q_factor[kRowRing][R];
-    int2 row_keys[kRowRing][R];  // first and last key of a row
-    float4 tile_max[2][R];       // of the four softmax warps
-    float4 tile_sum[2][R];
-    float v_max[2][4];
+    Step step[kSteps];
+    float q_factor[kItems][R];
+    int2 row_keys[kItems][R];  // first and last key of a row
+    float4 step_max[2][R];     // of the four warps of a softmax group
+    float4 step_sum[2][R];
     float2 joined[2][R];  // factors of the old and the new output
     float final[R];
     int64_t out_at[R];
@@ -308,41 +324,77 @@ struct Shared {
     int red[kAttendWarps];
 };
 
-// Sum over the 32 lanes of each of 8 values; lane l gets the sum of value l / 4.
-__device__ __forceinline__ float sums_of_8(const float (&v)[8], int lane) {
-    float a[4], b[2];
-    const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float give = h16 ? v[i] : v[i + 4], keep = h16 ? v[i + 4] : v[i];
-        a[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 16);
+// Waits are bounded by a number of polls (each may suspend the thread for a while: seconds in all, far
+// more than any step takes).  When one runs out, `gave_up` is set and every role leaves its loop without
+// waiting for the others; barriers that a whole group shares are met by all of it or by none.
+constexpr int kPolls = 1 << 22;
+__device__ __forceinline__ void wait_phase(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
+    int polls = 0;
+    while (!mbar_try_wait(bar, parity)) {
+        if (*gave_up || ++polls == kPolls) {
+            *gave_up = 1;
+            break;
+        }
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float give = h8 ? a[i] : a[i + 2], keep = h8 ? a[i + 2] : a[i];
-        b[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 8);
+}
+// The same for what has to end whether or not a wait ran out.
+__device__ __forceinline__ void drain_phase(uint64_t *bar, uint32_t parity) {
+    for (int i = 0; i < kPolls && !mbar_try_wait(bar, parity); ++i) {
     }
-    float c = (h4 ? b[1] : b[0]) + __shfl_xor_sync(0xFFFFFFFFu, h4 ? b[0] : b[1], 4);
-    c += __shfl_xor_sync(0xFFFFFFFFu, c, 2);
-    return c + __shfl_xor_sync(0xFFFFFFFFu, c, 1);
 }
 
+// Reduces each of kN values over the 32 lanes: kN / 32 results per lane (one where kN < 32), of the
+// values from lane * kN / 32 on.  Each round halves the values by trading halves with a partner lane.
+struct MaxOf {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct SumOf {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+template <int kN, class Op>
+__device__ __forceinline__ void reduce_lanes(float (&v)[kN], int lane, Op op) {
+    int n = kN;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool high = lane & o;
+#pragma unroll
+            for (int i = 0; i < kN / 2; ++i) {
+                if (i >= n) break;
+                const float give = high ? v[i] : v[i + n], keep = high ? v[i + n] : v[i];
+                v[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+            }
+        } else {
+            v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], o));
+        }
+    }
+}
+
+// Shared memory besides the ring of K and V slots, which gets the rest.
 template <class F>
-__global__ void __launch_bounds__(kAttendThreads, F::kCtas)
+constexpr int kFixedBytes = 1024 + F::kDigits * (F::kQ + 2 * F::kP) + static_cast<int>(sizeof(Shared<F::R>)) + (kSeqsInside + 1) * 4;
+template <class F>
+constexpr int kSlots = (kSharedBytes - kFixedBytes<F>) / F::kSlot < kMaxSlots ? (kSharedBytes - kFixedBytes<F>) / F::kSlot : kMaxSlots;
+
+template <class F>
+__global__ void __launch_bounds__(kAttendThreads, 1)
     attend_kernel(const __grid_constant__ AttendParams P, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map) {
     using E = typename F::E;
-    constexpr int D = F::D, R = F::R, N = F::N, kDigits = F::kDigits, kPitch = F::kPitch;
+    constexpr int D = F::D, R = F::R, N = F::N, kDigits = F::kDigits, kPitch = F::kPitch, kSub = F::kSub;
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
     extern __shared__ uint8_t raw[];
     uint8_t *base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     uint8_t *ring = base;
-    uint8_t *q_sh = ring + P.slots * F::kSlot;
-    uint8_t *p_sh = q_sh + F::kQ;
-    Shared<R> &S = *reinterpret_cast<Shared<R> *>(p_sh + 2 * F::kP);
+    uint8_t *q_sh = ring + kSlots<F> * F::kSlot;
+    uint8_t *p_sh = q_sh + kDigits * F::kQ;
+    Shared<R> &S = *reinterpret_cast<Shared<R> *>(p_sh + 2 * kDigits * F::kP);
     int32_t *sums_sh = reinterpret_cast<int32_t *>(&S + 1);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kAll, tid >> 5, 0);
     const int cta = blockIdx.x;
-    const int slots = P.slots;
+    constexpr int slots = kSlots<F>;
 
     // ---- schedule -------------------------------------------------------------------
     Walk walk;
@@ -354,7 +406,7 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
             int v = 0;
             if (b < P.B) {
                 const Seq s = load_seq(P, b);
-                if (s.n > 0) v = key_span(P, s, 0, s.n * P.G).tiles * P.Hkv;
+                if (s.n > 0) v = key_span(P, s, 0, s.n * P.G).steps * P.Hkv;
             }
             const int sum = block_sums<kAttendThreads>(v, carry, S.red);
             if (b < P.B) sums_sh[b + 1] = sum;
@@ -391,6 +443,7 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
 
     if (tid == 0) {
         for (int i = 0; i < slots; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], 1);
+        for (int i = 0; i < kSteps; ++i) mbar_init(&S.step_full[i], 1), mbar_init(&S.step_free[i], kConsumers);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.s_full[i], 1);
             mbar_init(&S.s_free[i], 4);
@@ -406,168 +459,173 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
         fence_mbar_init();
         P.ws->join[cta].last_cta = -1;
     }
-    if (busy && warp == 9) tc::tmem_alloc(&S.tmem, F::kColumns);
+    if (busy && warp == 13) tc::tmem_alloc(&S.tmem, F::kColumns);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     if (!busy) return;
     const uint32_t tmem = S.tmem;
 
-    Part part;
     auto wait = [&](uint64_t *bar, int parity) { wait_phase(bar, static_cast<uint32_t>(parity), &S.gave_up); };
     auto gave_up = [&] { return *static_cast<volatile int *>(&S.gave_up) != 0; };
-    if (warp < 4) {
-        // ---- softmax: one key per thread --------------------------------------------
-        int it = 0, item = 0;
-        while (walk.next(P, part)) {
-            const int ring_row = item % kRowRing;
-            ++item;
-            const int32_t *table = P.table + static_cast<int64_t>(part.b) * P.max_blocks;
-            auto page_of = [&](int j) { return j >= part.start && j < part.stop ? __ldg(table + (j >> P.page_shift)) : -1; };
-            auto page_ok = [&](int page) { return page >= 0 && page < P.num_pages; };
-            // all rows attend to the keys [common_from, common_to]
-            const int low = part.pos0 + part.row0 / P.G, high = part.pos0 + (part.row0 + part.rows - 1) / P.G;
-            const int common_to = low, common_from = P.window > 0 ? max(0, high + 1 - P.window) : 0;
-            int j = part.tile * kTile + tid;
-            int page = page_of(j);
-            int page_next = page_of(j + kTile);
-            bool ok = page_ok(page);
-            float ks = 0.f, vs = 0.f;
-            if (ok) {
-                ks = __ldg(P.ks + static_cast<int64_t>(page) * P.Hkv + part.head);
-                vs = __ldg(P.vs + static_cast<int64_t>(page) * P.Hkv + part.head);
+    auto open_step = [&](int s) -> const Step & {
+        wait(&S.step_full[s % kSteps], (s / kSteps) & 1);
+        return S.step[s % kSteps];
+    };
+    auto close_step = [&](int s) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.step_free[s % kSteps]);
+    };
+    // The ring's order is the order in which the MMA warp uses it: K0 K1 K2 V0 K3 V1 ...
+    auto place_of_k = [](int s) { return s < 2 ? s : 2 * s - 2; };
+    auto place_of_v = [](int s) { return 2 * s + 3; };
+
+    if (warp < 8) {
+        // ---- softmax: one key of each tile per thread; the two groups take steps in turn ----
+        const int group = warp >> 2, quad = warp & 3, key = tid & 127;
+        const uint32_t s_at = tmem + group * (kSub * N) + (static_cast<uint32_t>(quad) << 21);
+        uint8_t *p_at = p_sh + group * (kDigits * F::kP);
+        float *max_sh = reinterpret_cast<float *>(S.step_max[group]);
+        float *sum_sh = reinterpret_cast<float *>(S.step_sum[group]);
+        // Rows pass in chunks of eight, twice: for the largest scores, then for the weights.  S is read from TMEM
+        // each time: the loops stay small enough for the instruction cache (unrolled over 32 rows, instruction
+        // fetches took 7 of every 18 stalled cycles), and no row count needs registers of its own.
+        for (int it = group;; it += 2) {
+            const int phase = (it >> 1) & 1;
+            const Step &st = open_step(it);
+            const bool stop = !st.live;
+            const int item = st.item & (kItems - 1), chunks = (st.rows + 7) >> 3;
+            const float *q_factor = S.q_factor[item];
+            const bool plain = st.plain, odd = st.odd;
+            float ks[kSub], f[kSub];
+            bool there[kSub];
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+                const int page = (u * kTile + key) >> P.page_shift;
+                const float2 sc = st.scale[page];
+                ks[u] = sc.x, f[u] = sc.y;
+                there[u] = (st.there >> page) & 1;
             }
-            for (int t = 0; t < part.tiles; ++t, ++it, j += kTile) {
-                const int buf = it & 1, phase = (it >> 1) & 1;
-                // the next tile's scales and the page of the one after it are under way while this one is worked on
-                const bool ok_now = ok;
-                const float ks_now = ks, vs_now = vs;
-                if (!ok_now && j >= part.start && j < part.stop) report(P.dev_status, SSD_DEV_BAD_PAGE);
-                if (t + 1 < part.tiles) {
-                    ok = page_ok(page_next);
-                    ks = vs = 0.f;
-                    if (ok) {
-                        ks = __ldg(P.ks + static_cast<int64_t>(page_next) * P.Hkv + part.head);
-                        vs = __ldg(P.vs + static_cast<int64_t>(page_next) * P.Hkv + part.head);
-                    }
-                    page_next = page_of(j + 2 * kTile);
+            const int key0 = st.key0 + key;
+            // scores of eight rows, without the rows' own factors
+            auto scores = [&](int r0, float(&s)[kSub][8]) {
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) tc::tmem_load<8>(s[u], s_at + u * N + r0);
+                tc::tmem_wait_load(s);
+#pragma unroll
+                for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[u][i] *= ks[u];
+                if (!plain) {
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int2 keys = S.row_keys[item][r0 + i];
+                            const int j = key0 + u * kTile;
+                            s[u][i] = there[u] && j >= keys.x && j <= keys.y ? s[u][i] : -INFINITY;
+                        }
                 }
-                const float vs_size = ok_now && fabsf(vs_now) <= 3.402823466e38f ? fabsf(vs_now) : 0.f;
-
-                wait(&S.s_full[buf], phase);
+            };
+            if (!stop) {
+                wait(&S.s_full[group], phase);
                 tc::fence_after();
-                float s[R];
-                const uint32_t at = tmem + buf * N + (static_cast<uint32_t>(warp) << 21);
+                // the output warps have read what this group's buffers held before
+                if (it >= 2) wait(&S.o_free[group], phase ^ 1);
+                // largest score of each row: over the thread's keys, the warp's lanes, the group's warps
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    float s[kSub][8];
+                    scores(c * 8, s);
+                    if (kSub == 2) {
 #pragma unroll
-                for (int r = 0; r < R; r += 8) {
-                    float d[kDigits][8];
-#pragma unroll
-                    for (int g = 0; g < kDigits; ++g) tc::tmem_load8(d[g], at + g * R + r);
-                    tc::tmem_wait_load(d);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        s[r + i] = fmaf(d[1][i], 0.0625f, d[0][i]);
-                        if (kDigits == 3) s[r + i] = fmaf(d[kDigits - 1][i], 0.00390625f, s[r + i]);
+                        for (int i = 0; i < 8; ++i) s[0][i] = fmaxf(s[0][i], s[kSub - 1][i]);
                     }
+                    reduce_lanes(s[0], lane, MaxOf());
+                    const int r = c * 8 + lane / 4;
+                    if (lane % 4 == 0) max_sh[r * 4 + quad] = s[0][0] * q_factor[r];
                 }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.s_free[buf]);
+            }
+            if (tc::barrier_or(1 + group, 128, stop || gave_up())) break;
 
-                const bool partial = !(ok_now && j >= common_from && j <= common_to);
-                uint64_t seen = ~0ull;
+            // weights 2^(score - largest), their sums over the keys, and the digits of weight x value scale (<= 256)
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                const int r0 = c * 8;
+                float s[kSub][8], sums[8];
+                scores(r0, s);
 #pragma unroll
-                for (int r = 0; r < R; ++r) s[r] *= ks_now * S.q_factor[ring_row][r];
-                if (__any_sync(0xFFFFFFFFu, partial)) {
-                    seen = 0;
+                for (int i = 0; i < 8; ++i) {
+                    const float4 m4 = S.step_max[group][r0 + i];
+                    // without a key the largest is -inf: 2^(-inf + 1e30) is 0 all the same
+                    const float m = fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), -1e30f);
+                    const float qf = q_factor[r0 + i];
+                    sums[i] = 0.f;
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const int2 keys = S.row_keys[ring_row][r];
-                        const bool v = ok_now && j >= keys.x && j <= keys.y;
-                        s[r] = v ? s[r] : -INFINITY;
-                        seen |= static_cast<uint64_t>(v) << r;
+                    for (int u = 0; u < kSub; ++u) {
+                        s[u][i] = ex2(fmaf(s[u][i], qf, -m));
+                        sums[i] += s[u][i];
                     }
                 }
-                // the output warps have read what this buffer held two tiles ago
-                if (it >= 2) wait(&S.o_free[buf], phase ^ 1);
-                float mine[(R + 31) / 32];
+                reduce_lanes(sums, lane, SumOf());
+                if (lane % 4 == 0) sum_sh[(r0 + lane / 4) * 4 + quad] = sums[0];
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float m = tc::warp_max(s[r]);
-                    if ((r & 31) == lane) mine[r >> 5] = m;
-                }
-                float *max_sh = reinterpret_cast<float *>(S.tile_max[buf]);
+                for (int u = 0; u < kSub; ++u) {
 #pragma unroll
-                for (int r = 0; r < (R + 31) / 32; ++r)
-                    if (r * 32 + lane < R) max_sh[(r * 32 + lane) * 4 + warp] = mine[r];
-                const float v_top = tc::warp_max(vs_size);
-                if (lane == 0) S.v_max[buf][warp] = v_top;
-                tc::named_barrier(1, 128);
-
-                // weights p = 2^(s - max); their digits carry p vs / v_ref times 256, v_ref a power of two
-                const float v_all = fmaxf(fmaxf(S.v_max[buf][0], S.v_max[buf][1]), fmaxf(S.v_max[buf][2], S.v_max[buf][3]));
-                const uint32_t v_exp = min(max(__float_as_uint(v_all) >> 23, 8u), 254u);  // 2^(v_exp - 126) > v_all
-                const float v_scale = __uint_as_float((254u + 7u - v_exp) << 23);           // 2^(134 - v_exp) = 256 / 2^(v_exp - 126)
-                float f = vs_now * v_scale;
-                if (!(fabsf(vs_now) <= 3.402823466e38f)) f = __int_as_float(0x7FC00000);
-                uint8_t *p_at = p_sh + buf * F::kP;
-                uint32_t words[kDigits][R / 4];
-                float *sum_sh = reinterpret_cast<float *>(S.tile_sum[buf]);
+                    for (int i = 0; i < 8; ++i) s[u][i] *= f[u];
+                    if (odd && !plain) {  // 0 times a scale that is not finite
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) {
+                            const int2 keys = S.row_keys[item][r0 + i];
+                            const int j = key0 + u * kTile;
+                            if (there[u] && j >= keys.x && j <= keys.y) continue;
 #pragma unroll
-                for (int r0 = 0; r0 < R; r0 += 8) {
-                    float p[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 m4 = S.tile_max[buf][r0 + i];
-                        float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-                        m = m == -INFINITY ? 0.f : m;
-                        p[i] = ex2(s[r0 + i] - m);
-                    }
-                    float w[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = (seen >> (r0 + i)) & 1 ? p[i] * f : 0.f;
-#pragma unroll
-                    for (int g = 0; g < kDigits; ++g) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t a = e4m3x2(w[4 * h], w[4 * h + 1]), b = e4m3x2(w[4 * h + 2], w[4 * h + 3]);
-                            words[g][r0 / 4 + h] = a | (b << 16);
-                            if (g + 1 < kDigits) {
-                                const float2 fa = floats_of_e4m3x2(a), fb = floats_of_e4m3x2(b);
-                                w[4 * h] = (w[4 * h] - fa.x) * 16.f;
-                                w[4 * h + 1] = (w[4 * h + 1] - fa.y) * 16.f;
-                                w[4 * h + 2] = (w[4 * h + 2] - fb.x) * 16.f;
-                                w[4 * h + 3] = (w[4 * h + 3] - fb.y) * 16.f;
-                            }
+                            for (int e = 0; e < 8; ++e)
+                                if (e == i) s[u][e] = 0.f;
                         }
                     }
-                    const float sum = sums_of_8(p, lane);
-                    if ((lane & 3) == 0) sum_sh[(r0 + lane / 4) * 4 + warp] = sum;
-                }
-                // columns g * R + r of this key's row
-                constexpr int kWords = kDigits * R / 4;
-                const uint32_t *flat = &words[0][0];
+                    uint8_t *to = p_at + tc::swizzled<kPitch>(u * kTile + key, c >> 1) + (c & 1) * 8;
 #pragma unroll
-                for (int c = 0; c < (kWords + 3) / 4; ++c) {
-                    uint4 v;
-                    v.x = flat[4 * c];
-                    v.y = 4 * c + 1 < kWords ? flat[4 * c + 1] : 0u;
-                    v.z = 4 * c + 2 < kWords ? flat[4 * c + 2] : 0u;
-                    v.w = 4 * c + 3 < kWords ? flat[4 * c + 3] : 0u;
-                    *reinterpret_cast<uint4 *>(p_at + tc::swizzled<kPitch>(tid, c)) = v;
-                }
-                if (partial) {
-                    // A weight of 0 times NaN is NaN: values that no row, or not every row, attends to are
-                    // cleared where that could happen.  NaN that some rows do attend to is put back by the output warps.
-                    const int slot = (2 * it + 1) % slots, round = (2 * it + 1) / slots;
-                    wait(&S.full[slot], round & 1);
-                    uint4 *row = reinterpret_cast<uint4 *>(ring + slot * F::kSlot + tid * D);
-                    if (seen == 0) {
+                    for (int g = 0; g < kDigits; ++g) {
+                        uint32_t words[2];
 #pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float *w = &s[u][4 * h];
+                            const uint32_t a = e4m3x2(w[0], w[1]), b = e4m3x2(w[2], w[3]);
+                            words[h] = a | (b << 16);
+                            if (g + 1 < kDigits) {
+                                const float2 fa = floats_of_e4m3x2(a), fb = floats_of_e4m3x2(b);
+                                w[0] -= fa.x, w[1] -= fa.y, w[2] -= fb.x, w[3] -= fb.y;
+                                if (F::kOut == 2 && g == 0) {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) w[e] *= F::kFine;
+                                }
+                            }
+                        }
+                        *reinterpret_cast<uint2 *>(to + g * F::kP) = make_uint2(words[0], words[1]);
+                    }
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.s_free[group]);
+            if (!plain) {
+                // A weight of 0 times NaN is NaN: values that no row, or not every row, attends to are
+                // cleared of it.  NaN that some rows do attend to is put back by the output warps.
+                const int place = place_of_v(it), slot = place % slots;
+                wait(&S.full[slot], (place / slots) & 1);
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                    const int j = key0 + u * kTile;
+                    const bool seen = there[u] && j >= st.start && j < st.stop;
+                    if (u >= st.subs || (seen && j >= st.common_from && j <= st.common_to)) continue;
+                    uint4 *row = reinterpret_cast<uint4 *>(ring + slot * F::kSlot + (u * kTile + key) * D);
+                    if (!seen) {
+#pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) row[c] = make_uint4(0, 0, 0, 0);
                     } else {
                         bool met = false;
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
                             uint4 w4 = row[c];
                             uint32_t *w = &w4.x;
@@ -586,290 +644,395 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
                         if (met) atomicExch(&S.nan_met, 1);
                     }
                 }
-                tc::fence_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.p_full[buf]);
-            }
-        }
-    } else if (warp < 8) {
-        // ---- output: one channel per thread -------------------------------------------
-        const int ch = tid - 128;
-        int it = 0;
-        while (walk.next(P, part)) {
-            float acc[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) acc[r] = 0.f;
-            float m_run = -INFINITY, l_run = 0.f;  // of row ch
-            for (int t = 0; t < part.tiles; ++t, ++it) {
-                const int buf = it & 1, phase = (it >> 1) & 1;
-                wait(&S.p_full[buf], phase);
-                if (ch < R) {
-                    const float4 m4 = S.tile_max[buf][ch], l4 = S.tile_sum[buf][ch];
-                    const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-                    const float v_all =
-                        fmaxf(fmaxf(S.v_max[buf][0], S.v_max[buf][1]), fmaxf(S.v_max[buf][2], S.v_max[buf][3]));
-                    const uint32_t v_exp = min(max(__float_as_uint(v_all) >> 23, 8u), 254u);
-                    const float v_unit = __uint_as_float((v_exp - 7u) << 23);  // 2^(v_exp - 134)
-                    const float m_new = fmaxf(m_run, m);
-                    const float ref = m_new == -INFINITY ? 0.f : m_new;
-                    const float old = ex2(m_run - ref), now = ex2(m - ref);
-                    l_run = l_run * old + ((l4.x + l4.y) + (l4.z + l4.w)) * (m == -INFINITY ? 1.f : now);
-                    m_run = m_new;
-                    S.joined[buf][ch] = make_float2(old, now * v_unit);
-                }
-                tc::named_barrier(2, 128);
-                wait(&S.o_full[buf], phase);
-                tc::fence_after();
-                const uint32_t at = tmem + (2 + buf) * N + (static_cast<uint32_t>(warp - 4) << 21);
-#pragma unroll
-                for (int r = 0; r < R; r += 8) {
-                    float d[kDigits][8];
-#pragma unroll
-                    for (int g = 0; g < kDigits; ++g) tc::tmem_load8(d[g], at + g * R + r);
-                    tc::tmem_wait_load(d);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float o = fmaf(d[1][i], 0.0625f, d[0][i]);
-                        if (kDigits == 3) o = fmaf(d[kDigits - 1][i], 0.00390625f, o);
-                        const float2 f = S.joined[buf][r + i];
-                        acc[r + i] = fmaf(o, f.y, acc[r + i] * f.x);
-                    }
-                }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.o_free[buf]);
-            }
-            if (*static_cast<volatile int *>(&S.nan_met) && ch < D) {
-                // rare: NaN among values that only some rows attend to, read again from the cache
-                const int high = part.pos0 + (part.row0 + part.rows - 1) / P.G, low = part.pos0 + part.row0 / P.G;
-                const int from = max(part.start, part.tile * kTile), to = min(part.stop, (part.tile + part.tiles) * kTile);
-                for (int j = from; j < to; ++j) {
-                    if (j <= low && (P.window == 0 || j > high - P.window)) continue;
-                    const int page = P.table[static_cast<int64_t>(part.b) * P.max_blocks + (j >> P.page_shift)];
-                    if (page < 0 || page >= P.num_pages) continue;
-                    const int64_t row = ((static_cast<int64_t>(page) * P.Hkv + part.head) << P.page_shift) +
-                                        (j & ((1 << P.page_shift) - 1));
-                    if ((P.v[row * D + ch] & 0x7F) != 0x7F) continue;
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const int pos = part.pos0 + (part.row0 + r) / P.G;
-                        if (j <= pos && (P.window == 0 || j > pos - P.window)) acc[r] = __int_as_float(0x7FC00000);
-                    }
-                }
-            }
-            const bool whole = part.from_start && part.to_end;
-            if (whole) {
-                if (ch < R) {
-                    const int row = part.row0 + ch;
-                    const int token = part.first + row / P.G, head = part.head * P.G + row % P.G;
-                    S.final[ch] = l_run == 0.f ? 0.f : 1.f / l_run;
-                    S.out_at[ch] = (static_cast<int64_t>(token) * P.Hq + head) * D;
-                }
-                tc::named_barrier(2, 128);
-                if (ch < D) {
-                    E *out = static_cast<E *>(P.out) + ch;
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        if (r < part.rows) out[S.out_at[r]] = narrow<E>(acc[r] * S.final[r]);
-                }
-                tc::named_barrier(2, 128);
-            } else {
-                const int slot = 2 * cta + (part.from_start ? 1 : 0);
-                if (ch < R) P.ws->ml[slot][ch] = make_float2(m_run, l_run);
-                if (ch < D)
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        if (r < part.rows) P.ws->o[slot][r][ch] = acc[r];
-                if (part.from_start && ch == 0) {
-                    Join jn{};
-                    jn.last_cta = part.last_cta;
-                    jn.first_token = part.first;
-                    jn.row0 = part.row0;
-                    jn.rows = part.rows;
-                    jn.head = part.head;
-                    P.ws->join[cta] = jn;
-                }
-            }
-        }
-    } else if (warp == 8) {
-        // ---- TMA: K and V of each tile, one slot each -----------------------------------
-        int it = 0;
-        int issued = 0;
-        const int pages_per_tile = kTile >> P.page_shift;
-        while (walk.next(P, part)) {
-            const int32_t *table = P.table + static_cast<int64_t>(part.b) * P.max_blocks;
-            // each lane holds one of 32 consecutive pages, and the one 32 later
-            const int page_of_tile = part.tile * pages_per_tile;
-            auto load_page = [&](int i) {
-                const int j = i << P.page_shift;
-                return j < part.stop && j + (1 << P.page_shift) > part.start ? __ldg(table + i) : -1;
-            };
-            int held = load_page(page_of_tile + lane), later = load_page(page_of_tile + 32 + lane);
-            int held_from = page_of_tile;
-            for (int t = 0; t < part.tiles; ++t, ++it) {
-                const int p0 = page_of_tile + t * pages_per_tile;
-                if (p0 - held_from >= 32) {
-                    held = later, held_from += 32;
-                    later = load_page(held_from + 32 + lane);
-                }
-                const int page = __shfl_sync(0xFFFFFFFFu, held, (p0 - held_from + (lane & (pages_per_tile - 1))) & 31);
-                const bool load = lane < pages_per_tile && page >= 0 && page < P.num_pages;
-                const int n = __popc(__ballot_sync(0xFFFFFFFFu, load));
-                const uint32_t bytes = static_cast<uint32_t>(n) * static_cast<uint32_t>(D << P.page_shift);
-                const int row = (page * P.Hkv + part.head) << P.page_shift;
-#pragma unroll
-                for (int what = 0; what < 2; ++what) {
-                    const int x = 2 * it + what, slot = x % slots, round = x / slots;
-                    if (round > 0) wait(&S.empty[slot], (round - 1) & 1);
-                    const bool go = __all_sync(0xFFFFFFFFu, !gave_up());
-                    if (go && lane == 0) mbar_arrive_expect_tx(&S.full[slot], bytes);
-                    __syncwarp();
-                    if (go && load)
-                        tc::tma_load_2d(ring + slot * F::kSlot + lane * (D << P.page_shift), what ? &v_map : &k_map, 0, row,
-                                        &S.full[slot]);
-                    issued = go ? x + 1 : issued;
-                }
-            }
-        }
-        if (gave_up())  // the copies under way still have to land before the CTA ends
-            for (int x = max(0, issued - slots); x < issued; ++x)
-                for (int i = 0; i < kSlices && !mbar_wait_suspend_for(&S.full[x % slots], (x / slots) & 1, kSliceNs); ++i) {
-                }
-    } else if (warp == 9) {
-        // ---- MMA ----------------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t kShapeS = tc::mma_shape(N, false, false), kShapeO = tc::mma_shape(N, true, true);
-            const uint64_t q_desc = tc::matrix_desc(q_sh, D);
-            int it = 0, item = 0;
-            auto output_of = [&](int i) {  // O^T = V^T P^T of tile i
-                const int buf = i & 1, phase = (i >> 1) & 1;
-                const int slot = (2 * i + 1) % slots, round = (2 * i + 1) / slots;
-                wait(&S.full[slot], round & 1);
-                wait(&S.p_full[buf], phase);
-                if (i >= 2) wait(&S.o_free[buf], phase ^ 1);
-                if (gave_up()) return;
-                tc::fence_after();
-                const uint64_t v_desc = tc::matrix_desc(ring + slot * F::kSlot, D);
-                const uint64_t p_desc = tc::matrix_desc(p_sh + buf * F::kP, kPitch);
-#pragma unroll
-                for (int k = 0; k < kTile / 32; ++k)
-                    tc::mma_e4m3(tmem + (2 + buf) * N, v_desc + k * (32 * D >> 4), p_desc + k * (32 * kPitch >> 4), kShapeO, k > 0);
-                tc::mma_commit(&S.o_full[buf]);
-                tc::mma_commit(&S.empty[slot]);
-            };
-            while (walk.next(P, part)) {
-                wait(&S.q_full, item & 1);
-                ++item;
-                for (int t = 0; t < part.tiles; ++t, ++it) {
-                    const int buf = it & 1, phase = (it >> 1) & 1;
-                    const int slot = (2 * it) % slots, round = (2 * it) / slots;
-                    wait(&S.full[slot], round & 1);
-                    if (it >= 2) wait(&S.s_free[buf], phase ^ 1);
-                    if (gave_up()) continue;
-                    tc::fence_after();
-                    const uint64_t k_desc = tc::matrix_desc(ring + slot * F::kSlot, D);
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k)  // 32 channels further inside the swizzled rows
-                        tc::mma_e4m3(tmem + buf * N, k_desc + k * 2, q_desc + k * 2, kShapeS, k > 0);
-                    tc::mma_commit(&S.s_full[buf]);
-                    tc::mma_commit(&S.empty[slot]);
-                    if (t == part.tiles - 1) tc::mma_commit(&S.q_free);
-                    if (it > 0) output_of(it - 1);
-                }
-            }
-            if (it > 0) output_of(it - 1);
-            if (gave_up()) {  // what was issued still has to end before the CTA does
-                tc::mma_commit(&S.drained);
-                for (int i = 0; i < kSlices && !mbar_wait_suspend_for(&S.drained, 0, kSliceNs); ++i) {
-                }
-            }
-        }
-        __syncwarp();
-    } else {
-        // ---- the queries' digits --------------------------------------------------------
-        constexpr int kPer = D / 32;  // channels per lane
-        constexpr int kBatch = 8;     // rows in flight
-        int item = 0;
-        while (walk.next(P, part)) {
-            const int ring_row = item % kRowRing;
-#pragma unroll 1
-            for (int r0 = 0; r0 < R; r0 += kBatch) {
-                float x[kBatch][kPer];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int row = part.row0 + r0 + i;
-                    const bool there = r0 + i < part.rows;
-                    const E *q = static_cast<const E *>(P.q) + (part.first + row / P.G) * P.q_stride +
-                                 static_cast<int64_t>(part.head * P.G + row % P.G) * D + lane * kPer;
-#pragma unroll
-                    for (int c = 0; c < kPer; c += 2) {
-                        uint32_t two = 0;
-                        if (there) two = __ldg(reinterpret_cast<const uint32_t *>(q + c));
-                        x[i][c] = wide(reinterpret_cast<const E *>(&two)[0]);
-                        x[i][c + 1] = wide(reinterpret_cast<const E *>(&two)[1]);
-                    }
-                }
-                if (r0 == 0 && item > 0) wait(&S.q_free, (item - 1) & 1);
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int r = r0 + i;
-                    float top = 0.f;
-                    bool odd = false;
-#pragma unroll
-                    for (int c = 0; c < kPer; ++c) {
-                        odd |= !(fabsf(x[i][c]) <= 3.402823466e38f);
-                        top = fmaxf(top, fabsf(x[i][c]));
-                    }
-                    top = tc::warp_max(top);
-                    odd = __any_sync(0xFFFFFFFFu, odd);
-                    // the largest is brought into [128, 256): k = 7 - its exponent
-                    const int e = static_cast<int>(__float_as_uint(top) >> 23);
-                    const int k = top == 0.f ? 0 : min(134 - e, 126);
-                    const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-                    uint32_t digit[kDigits];
-                    float left[kPer];
-#pragma unroll
-                    for (int c = 0; c < kPer; ++c) left[c] = x[i][c] * up;
-#pragma unroll
-                    for (int g = 0; g < kDigits; ++g) {
-                        digit[g] = 0;
-#pragma unroll
-                        for (int c = 0; c < kPer; c += 2) {
-                            const uint32_t two = e4m3x2(left[c], left[c + 1]);
-                            const float2 f = floats_of_e4m3x2(two);
-                            left[c] = (left[c] - f.x) * 16.f;
-                            left[c + 1] = (left[c + 1] - f.y) * 16.f;
-                            digit[g] |= two << (8 * c);
-                        }
-                        const int at = tc::swizzled<D>(g * R + r, lane * kPer / 16) + (lane * kPer) % 16;
-                        if (kPer == 4)
-                            *reinterpret_cast<uint32_t *>(q_sh + at) = digit[g];
-                        else
-                            *reinterpret_cast<uint16_t *>(q_sh + at) = static_cast<uint16_t>(digit[g]);
-                    }
-                    if (lane == 0) {
-                        const bool there = r < part.rows;
-                        const int pos = part.pos0 + (part.row0 + r) / P.G;
-                        // 2^-k in two steps: k reaches 126 and -120
-                        float f = P.scale * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-                        if (odd) f = __int_as_float(0x7FC00000);
-                        S.q_factor[ring_row][r] = there ? f : 0.f;
-                        S.row_keys[ring_row][r] =
-                            there ? make_int2(P.window > 0 ? pos + 1 - P.window : 0, pos) : make_int2(0, -1);
-                    }
-                }
             }
             tc::fence_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S.q_full);
-            ++item;
+            if (lane == 0) mbar_arrive(&S.p_full[group]);
+            close_step(it);
+        }
+    } else if (warp < 12) {
+        // ---- output: one channel per thread -------------------------------------------
+        const int ch = tid - 256, quad = warp & 3;
+        float acc[R];
+        float m_run = -INFINITY, l_run = 0.f;  // of row ch
+        for (int it = 0;; ++it) {
+            const int buf = it & 1, phase = (it >> 1) & 1;
+            const Step &st = open_step(it);
+            const bool stop = !st.live;
+            if (st.first) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) acc[r] = 0.f;
+                m_run = -INFINITY, l_run = 0.f;
+            }
+            if (!stop) wait(&S.p_full[buf], phase);
+            if (!stop && ch < st.rows) {
+                const float4 m4 = S.step_max[buf][ch], l4 = S.step_sum[buf][ch];
+                const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+                const float m_new = fmaxf(m_run, m);
+                const float ref = m_new == -INFINITY ? 0.f : m_new;
+                const float old = ex2(m_run - ref), now = ex2(m - ref);
+                l_run = l_run * old + ((l4.x + l4.y) + (l4.z + l4.w)) * (m == -INFINITY ? 1.f : now);
+                m_run = m_new;
+                S.joined[buf][ch] = make_float2(old, now * st.v_unit);
+            }
+            if (tc::barrier_or(3, 128, stop || gave_up())) break;
+            wait(&S.o_full[buf], phase);
+            tc::fence_after();
+            const uint32_t at = tmem + 2 * kSub * N + buf * (F::kOut * N) + (static_cast<uint32_t>(quad) << 21);
+            const int rows = st.rows;
+#pragma unroll
+            for (int r0 = 0; r0 < R; r0 += 8) {
+                if (r0 < rows) {
+                    float o[F::kOut][8];
+#pragma unroll
+                    for (int g = 0; g < F::kOut; ++g) tc::tmem_load<8>(o[g], at + g * N + r0);
+                    tc::tmem_wait_load(o);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (F::kOut == 2) o[0][i] = fmaf(o[F::kOut - 1][i], 1.f / F::kFine, o[0][i]);
+                        const float2 f = S.joined[buf][r0 + i];
+                        acc[r0 + i] = fmaf(o[0][i], f.y, acc[r0 + i] * f.x);
+                    }
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.o_free[buf]);
+            if (st.last) {
+                if (*static_cast<volatile int *>(&S.nan_met) && ch < D) {
+                    // rare: NaN among values that only some rows attend to, read again from the cache
+                    const int from = max(st.start, st.part_key0), to = min(st.stop, st.key0 + F::kStep);
+                    for (int j = from; j < to; ++j) {
+                        if (j >= st.common_from && j <= st.common_to) continue;
+                        const int page = P.table[static_cast<int64_t>(st.seq) * P.max_blocks + (j >> P.page_shift)];
+                        if (page < 0 || page >= P.num_pages) continue;
+                        const int64_t row = ((static_cast<int64_t>(page) * P.Hkv + st.head) << P.page_shift) +
+                                            (j & ((1 << P.page_shift) - 1));
+                        if ((P.v[row * D + ch] & 0x7F) != 0x7F) continue;
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            const int2 keys = S.row_keys[st.item][r];
+                            if (j >= keys.x && j <= keys.y) acc[r] = __int_as_float(0x7FC00000);
+                        }
+                    }
+                }
+                if (st.from_start && st.to_end) {
+                    if (ch < R) {
+                        const int row = st.row0 + ch;
+                        const int token = st.token0 + row / P.G, head = st.head * P.G + row % P.G;
+                        S.final[ch] = l_run == 0.f ? 0.f : 1.f / l_run;
+                        S.out_at[ch] = (static_cast<int64_t>(token) * P.Hq + head) * D;
+                    }
+                    tc::named_barrier(3, 128);
+                    if (ch < D) {
+                        E *out = static_cast<E *>(P.out) + ch;
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            if (r < st.rows) out[S.out_at[r]] = narrow<E>(acc[r] * S.final[r]);
+                    }
+                    tc::named_barrier(3, 128);
+                } else {
+                    const int slot = 2 * cta + (st.from_start ? 1 : 0);
+                    if (ch < R) P.ws->ml[slot][ch] = make_float2(m_run, l_run);
+                    if (ch < D)
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            if (r < st.rows) P.ws->o[slot][r][ch] = acc[r];
+                    if (st.from_start && ch == 0) {
+                        Join jn{};
+                        jn.last_cta = st.last_cta;
+                        jn.first_token = st.token0;
+                        jn.row0 = st.row0;
+                        jn.rows = st.rows;
+                        jn.head = st.head;
+                        P.ws->join[cta] = jn;
+                    }
+                }
+            }
+            close_step(it);
+        }
+    } else if (warp == 12) {
+        // ---- TMA ------------------------------------------------------------------------
+        int highest = -1;
+        auto load = [&](int s, int place, const CUtensorMap *map) {
+            const Step &st = S.step[s % kSteps];
+            const int slot = place % slots, round = place / slots;
+            if (round > 0) wait(&S.empty[slot], (round - 1) & 1);
+            if (__any_sync(kAll, gave_up())) return;
+            const bool mine = lane < 16 && ((st.there >> lane) & 1);
+            const int bytes = __popc(static_cast<uint32_t>(st.there)) * (D << P.page_shift);
+            if (lane == 0) mbar_arrive_expect_tx(&S.full[slot], static_cast<uint32_t>(bytes));
+            __syncwarp();
+            if (mine)
+                tc::tma_load_2d(ring + slot * F::kSlot + lane * (D << P.page_shift), map, 0,
+                                (st.page[lane] * P.Hkv + st.head) << P.page_shift, &S.full[slot]);
+            highest = max(highest, place);
+        };
+        int n = 0;
+        for (;; ++n) {
+            const Step &st = open_step(n);
+            if (!st.live || __any_sync(kAll, gave_up())) break;
+            load(n, place_of_k(n), &k_map);
+            if (n >= 2) {
+                load(n - 2, place_of_v(n - 2), &v_map);
+                close_step(n - 2);
+            }
+        }
+        for (int s = max(0, n - 2); s < n; ++s) {
+            load(s, place_of_v(s), &v_map);
+            close_step(s);
+        }
+        if (gave_up())  // the copies under way still have to land before the CTA ends
+            for (int x = max(0, highest - slots + 1); x <= highest; ++x)
+                drain_phase(&S.full[x % slots], (x / slots) & 1);
+    } else if (warp == 13) {
+        // ---- MMA ------------------------------------------------------------------------
+        const uint64_t ring_k = tc::matrix_desc(ring, D), q_desc = tc::matrix_desc(q_sh, D);
+        const uint64_t p_desc = tc::matrix_desc(p_sh, kPitch);
+        auto output_of = [&](int s, int subs, int columns) {  // O^T = V^T P^T of step s
+            const int buf = s & 1, phase = (s >> 1) & 1;
+            const int place = place_of_v(s), slot = place % slots;
+            wait(&S.full[slot], (place / slots) & 1);
+            wait(&S.p_full[buf], phase);
+            if (s >= 2) wait(&S.o_free[buf], phase ^ 1);
+            if (__any_sync(kAll, gave_up())) return;
+            tc::fence_after();
+            const uint32_t shape = tc::mma_shape(columns, true, true);
+            if (tc::elect_one()) {
+#pragma unroll 1
+                for (int u = 0; u < subs; ++u) {
+#pragma unroll 1
+                    for (int g = 0; g < kDigits; ++g)
+#pragma unroll
+                        for (int k = 0; k < kTile / 32; ++k)
+                            tc::mma_e4m3(tmem + 2 * kSub * N + buf * (F::kOut * N) + (F::kOut == 2 && g > 0 ? N : 0), ring_k + ((slot * F::kSlot + (u * kTile + k * 32) * D) >> 4),
+                                         p_desc + (((buf * kDigits + g) * F::kP + (u * kTile + k * 32) * kPitch) >> 4), shape,
+                                         u + k + (F::kOut == 2 ? (g == 2) : g) > 0);
+                }
+                tc::mma_commit(&S.o_full[buf]);
+                tc::mma_commit(&S.empty[slot]);
+            }
+            __syncwarp();
+        };
+        // tiles and columns of the last step, and of the one before
+        int n = 0, items = 0, subs_1 = 0, subs_2 = 0, columns_1 = 0, columns_2 = 0;
+        for (;; ++n) {
+            const int buf = n & 1, phase = (n >> 1) & 1;
+            const Step &st = open_step(n);
+            if (!st.live || __any_sync(kAll, gave_up())) break;
+            const int subs = st.subs, first = st.first, last = st.last, columns = (st.rows + 15) & ~15;
+            const uint32_t shape = tc::mma_shape(columns, false, false);
+            close_step(n);
+            if (first) wait(&S.q_full, items++ & 1);
+            const int place = place_of_k(n), slot = place % slots;
+            wait(&S.full[slot], (place / slots) & 1);
+            if (n >= 2) wait(&S.s_free[buf], phase ^ 1);
+            if (__any_sync(kAll, gave_up())) break;
+            tc::fence_after();
+            if (tc::elect_one()) {
+#pragma unroll 1
+                for (int u = 0; u < subs; ++u) {
+#pragma unroll 1
+                    for (int g = 0; g < kDigits; ++g)
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)  // 32 channels further inside the swizzled rows
+                            tc::mma_e4m3(tmem + buf * (kSub * N) + u * N, ring_k + ((slot * F::kSlot + u * kTile * D + k * 32) >> 4),
+                                         q_desc + ((g * F::kQ + k * 32) >> 4), shape, g + k > 0);
+                }
+                tc::mma_commit(&S.s_full[buf]);
+                tc::mma_commit(&S.empty[slot]);
+                if (last) tc::mma_commit(&S.q_free);
+            }
+            __syncwarp();
+            if (n >= 2) output_of(n - 2, subs_2, columns_2);
+            subs_2 = subs_1, subs_1 = subs;
+            columns_2 = columns_1, columns_1 = columns;
+        }
+        if (!__any_sync(kAll, gave_up())) {
+            if (n >= 2) output_of(n - 2, subs_2, columns_2);
+            if (n >= 1) output_of(n - 1, subs_1, columns_1);
+        }
+        if (__any_sync(kAll, gave_up())) {  // what was issued still has to end before the CTA does
+            if (tc::elect_one()) tc::mma_commit(&S.drained);
+            __syncwarp();
+            drain_phase(&S.drained, 0);
+        }
+    } else if (warp == 14) {
+        // ---- the queries' digits --------------------------------------------------------
+        constexpr int kPer = D / 32;  // channels per lane
+        constexpr int kBatch = 4;     // rows in flight
+        const float sign = P.scale < 0.f ? -1.f : 1.f, size = fabsf(P.scale);
+        int items = 0;
+        for (int it = 0;; ++it) {
+            const Step &st = open_step(it);
+            if (!st.live || __any_sync(kAll, gave_up())) break;
+            if (st.first) {
+                const int rows = st.rows, row0 = st.row0, token0 = st.token0, head0 = st.head * P.G, pos0 = st.pos0;
+#pragma unroll 1
+                for (int r0 = 0; r0 < rows; r0 += kBatch) {
+                    float x[kBatch][kPer];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int row = row0 + r0 + i;
+                        const bool there = r0 + i < rows;
+                        const E *q = static_cast<const E *>(P.q) + (token0 + row / P.G) * P.q_stride +
+                                     static_cast<int64_t>(head0 + row % P.G) * D + lane * kPer;
+#pragma unroll
+                        for (int c = 0; c < kPer; c += 2) {
+                            uint32_t two = 0;
+                            if (there) two = __ldg(reinterpret_cast<const uint32_t *>(q + c));
+                            x[i][c] = sign * wide(reinterpret_cast<const E *>(&two)[0]);
+                            x[i][c + 1] = sign * wide(reinterpret_cast<const E *>(&two)[1]);
+                        }
+                    }
+                    if (r0 == 0 && items > 0) wait(&S.q_free, (items - 1) & 1);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = r0 + i;
+                        float top = 0.f;
+                        bool odd = false;
+#pragma unroll
+                        for (int c = 0; c < kPer; ++c) {
+                            odd |= !(fabsf(x[i][c]) <= 3.402823466e38f);
+                            top = fmaxf(top, fabsf(x[i][c]));
+                        }
+                        top = tc::warp_max(top);
+                        odd = __any_sync(kAll, odd);
+                        // the largest is brought into [128, 256): k = 7 - its exponent
+                        const int e = static_cast<int>(__float_as_uint(top) >> 23);
+                        const int k = top == 0.f ? 0 : min(134 - e, 126);
+                        const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+                        float left[kPer];
+#pragma unroll
+                        for (int c = 0; c < kPer; ++c) left[c] = x[i][c] * up;
+#pragma unroll
+                        for (int g = 0; g < kDigits; ++g) {
+                            uint32_t digit = 0;
+#pragma unroll
+                            for (int c = 0; c < kPer; c += 2) {
+                                const uint32_t two = e4m3x2(left[c], left[c + 1]);
+                                const float2 f = floats_of_e4m3x2(two);
+                                left[c] -= f.x;
+                                left[c + 1] -= f.y;
+                                digit |= two << (8 * c);
+                            }
+                            uint8_t *to = q_sh + g * F::kQ + tc::swizzled<D>(r, lane * kPer / 16) + (lane * kPer) % 16;
+                            if (kPer == 4)
+                                *reinterpret_cast<uint32_t *>(to) = digit;
+                            else
+                                *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(digit);
+                        }
+                        if (lane == 0) {
+                            const bool there = r < rows;
+                            const int pos = pos0 + (row0 + r) / P.G;
+                            float f = size * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+                            if (odd) f = __int_as_float(0x7FC00000);
+                            S.q_factor[items % kItems][r] = there ? f : 0.f;
+                            S.row_keys[items % kItems][r] =
+                                there ? make_int2(P.window > 0 ? pos + 1 - P.window : 0, pos) : make_int2(0, -1);
+                        }
+                    }
+                }
+                tc::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.q_full);
+                ++items;
+            }
+            close_step(it);
+        }
+    } else {
+        // ---- scout: items, pages and scales ahead of the others ---------------------------
+        const int pages = F::kStep >> P.page_shift;  // of one step: 1 to 16
+        const int at_once = 32 / pages;              // steps whose pages the lanes look up together
+        const int my_step = lane / pages, my_page = lane % pages;
+        Part part;
+        int s = 0, items = 0;
+        while (walk.next(P, part)) {
+            if (__any_sync(kAll, gave_up())) break;
+            const int low = part.pos0 + part.row0 / P.G, high = part.pos0 + (part.row0 + part.rows - 1) / P.G;
+            const int common_to = low, common_from = P.window > 0 ? max(0, high + 1 - P.window) : 0;
+            const int32_t *table = P.table + static_cast<int64_t>(part.b) * P.max_blocks;
+            const int key0 = part.step * F::kStep;
+            auto look_up = [&](int t) {  // page of this lane's place in the steps from t on
+                const int j = key0 + (t + my_step) * F::kStep + (my_page << P.page_shift);
+                const bool in = t + my_step < part.steps && j < part.stop && j + (1 << P.page_shift) > part.start;
+                return in ? __ldg(table + (j >> P.page_shift)) : -2;
+            };
+            int next = look_up(0);
+            for (int t0 = 0; t0 < part.steps; t0 += at_once) {
+                const int page = next;
+                const bool there = page >= 0 && page < P.num_pages;
+                float ks = 0.f, vs = 0.f;
+                if (there) {
+                    const int64_t block = static_cast<int64_t>(page) * P.Hkv + part.head;
+                    ks = __ldg(P.ks + block);
+                    vs = __ldg(P.vs + block);
+                }
+                if (page != -2 && !there) report(P.dev_status, SSD_DEV_BAD_PAGE);
+                if (t0 + at_once < part.steps) next = look_up(t0 + at_once);
+                // Value scales are divided by a power of two above the step's largest, times 256: the weights'
+                // digits start at e4m3's upper end.
+                const bool finite = fabsf(vs) <= 3.402823466e38f;
+                float top = finite ? fabsf(vs) : 0.f;
+                for (int o = 1; o < pages; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+                const uint32_t e = min(max(__float_as_uint(top) >> 23, 8u), 254u);
+                const float f = finite ? vs * __uint_as_float((261u - e) << 23) : __int_as_float(0x7FC00000);
+                const uint32_t there_all = __ballot_sync(kAll, there), odd_all = __ballot_sync(kAll, !finite);
+                const uint32_t of_step = pages == 32 ? kAll : (1u << pages) - 1u;
+                const int n = min(at_once, part.steps - t0);
+                for (int i = 0; i < n; ++i, ++s) {
+                    const int slot = s % kSteps;
+                    if (s >= kSteps) wait(&S.step_free[slot], (s / kSteps - 1) & 1);
+                    if (__any_sync(kAll, gave_up())) break;
+                    Step &st = S.step[slot];
+                    if (my_step == i) {
+                        st.page[my_page] = page;
+                        st.scale[my_page] = make_float2(ks, f);
+                        if (my_page == 0) {
+                            const int k0 = key0 + (t0 + i) * F::kStep;
+                            const uint32_t mask = (there_all >> (i * pages)) & of_step;
+                            st.live = 1;
+                            st.first = t0 + i == 0;
+                            st.last = t0 + i == part.steps - 1;
+                            st.plain = mask == of_step && k0 >= common_from && k0 + F::kStep - 1 <= common_to;
+                            st.odd = ((odd_all >> (i * pages)) & of_step) != 0;
+                            st.key0 = k0;
+                            st.subs = k0 + kTile < part.stop ? kSub : 1;
+                            st.start = part.start, st.stop = part.stop;
+                            st.common_from = common_from, st.common_to = common_to;
+                            st.there = static_cast<int32_t>(mask);
+                            st.item = items % kItems;
+                            st.from_start = part.from_start, st.to_end = part.to_end, st.last_cta = part.last_cta;
+                            st.seq = part.b, st.head = part.head, st.row0 = part.row0, st.rows = part.rows;
+                            st.token0 = part.first, st.pos0 = part.pos0;
+                            st.part_key0 = key0;
+                            st.v_unit = __uint_as_float((e - 7u) << 23);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.step_full[slot]);
+                }
+            }
+            ++items;
+        }
+        // the end, once for each softmax group
+        for (int i = 0; i < 2; ++i, ++s) {
+            const int slot = s % kSteps;
+            if (s >= kSteps) wait(&S.step_free[slot], (s / kSteps - 1) & 1);
+            if (__any_sync(kAll, gave_up())) break;
+            if (lane == 0) {
+                S.step[slot].live = 0;
+                mbar_arrive(&S.step_full[slot]);
+            }
+            __syncwarp();
         }
     }
+    __syncwarp();
     if (tid == 0 && gave_up()) report(P.dev_status, SSD_DEV_TIMEOUT);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 9) tc::tmem_free(tmem, F::kColumns);
+    if (warp == 13) tc::tmem_free(tmem, F::kColumns);
 }
 
 // Joins the parts of the items that several CTAs share: one warp per row.
@@ -917,13 +1080,12 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
 
 struct Device {
     int sms = 0;
-    int smem_sm = 0, smem_cta = 0;
+    int smem_cta = 0;
 };
 int device_limits(Device *d) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d->smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&d->smem_cta, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) {
         cudaGetLastError();
         return SSD_ERR_CUDA;
@@ -934,20 +1096,17 @@ int device_limits(Device *d) {
 template <class F>
 int attend_launch(AttendParams P, const CUtensorMap &k_map, const CUtensorMap &v_map, const Device &dev, cudaStream_t stream) {
     auto *kernel = attend_kernel<F>;
-    const int fixed = 1024 + F::kQ + 2 * F::kP + static_cast<int>(sizeof(Shared<F::R>)) + (kSeqsInside + 1) * 4;
-    const int room = F::kCtas == 2 ? dev.smem_sm / 2 - 1024 : dev.smem_cta;
-    int slots = (room - fixed) / F::kSlot;
-    if (slots > kMaxSlots) slots = kMaxSlots;
-    if (slots < 3) return SSD_ERR_UNSUPPORTED;
-    const int dyn = fixed + slots * F::kSlot;
+    static_assert(kSlots<F> >= 4);
+    const int dyn = kFixedBytes<F> + kSlots<F> * F::kSlot;
+    if (dyn > dev.smem_cta) return SSD_ERR_UNSUPPORTED;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess) {
         cudaGetLastError();
         return SSD_ERR_CUDA;
     }
-    P.slots = slots;
     P.rows_per_item = F::R;
+    P.step_shift = log2_of(F::kStep);
     P.inside = static_cast<int64_t>(P.max_new) * P.G <= F::R && P.B <= kSeqsInside;
-    int ctas = dev.sms * F::kCtas;
+    int ctas = dev.sms;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     if (!P.inside) {
         if (static_cast<int64_t>(P.T) * P.G / F::R + P.B > kMaxPairs) return SSD_ERR_UNSUPPORTED;
@@ -972,15 +1131,11 @@ int attend_launch(AttendParams P, const CUtensorMap &k_map, const CUtensorMap &v
     return SSD_OK;
 }
 
-// Rows of an item: the fewest that hold the tokens of a sequence, so that few rows cost few columns.
+// Rows of an item: 64 cost the outputs' registers and the weights' shared memory, so 32 where they hold every sequence.
 template <class E, int D>
 int attend_dispatch(const AttendParams &P, const CUtensorMap &k, const CUtensorMap &v, const Device &dev, cudaStream_t s) {
-    const int64_t rows = static_cast<int64_t>(P.max_new) * P.G;
-    if (rows <= 8) return attend_launch<Form<E, D, 8>>(P, k, v, dev, s);
-    if (rows <= 16) return attend_launch<Form<E, D, 16>>(P, k, v, dev, s);
-    if (rows <= 32 || digits_of<E>() == 3) return attend_launch<Form<E, D, 32>>(P, k, v, dev, s);
-    if constexpr (digits_of<E>() == 2) return attend_launch<Form<E, D, 64>>(P, k, v, dev, s);
-    return SSD_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(P.max_new) * P.G <= 32) return attend_launch<Form<E, D, 32>>(P, k, v, dev, s);
+    return attend_launch<Form<E, D, 64>>(P, k, v, dev, s);
 }
 
 }  // namespace
