@@ -858,79 +858,77 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             drain_phase(&S.drained, 0);
         }
     } else if (warp == 14) {
-        // ---- the queries' digits --------------------------------------------------------
-        constexpr int kPer = D / 32;  // channels per lane
-        constexpr int kBatch = 4;     // rows in flight
+// ---- the queries' digits: eight rows at a time, four lanes to a row ------------------
+        constexpr int kPer = D / 4;  // channels per lane
         const float sign = P.scale < 0.f ? -1.f : 1.f, size = fabsf(P.scale);
+        const int sub = lane >> 2, part_of_row = lane & 3;
         int items = 0;
         for (int it = 0;; ++it) {
             const Step &st = open_step(it);
             if (!st.live || __any_sync(kAll, gave_up())) break;
             if (st.first) {
                 const int rows = st.rows, row0 = st.row0, token0 = st.token0, head0 = st.head * P.G, pos0 = st.pos0;
+                uint4 x[kPer / 8];
+                auto load = [&](int r) {
+                    const int row = row0 + r;
+                    const E *q = static_cast<const E *>(P.q) + (token0 + row / P.G) * P.q_stride +
+                                 static_cast<int64_t>(head0 + row % P.G) * D + part_of_row * kPer;
+#pragma unroll
+                    for (int c = 0; c < kPer / 8; ++c)
+                        x[c] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(q) + c) : make_uint4(0, 0, 0, 0);
+                };
+                load(sub);
+                if (items > 0) wait(&S.q_free, (items - 1) & 1);
 #pragma unroll 1
-                for (int r0 = 0; r0 < rows; r0 += kBatch) {
-                    float x[kBatch][kPer];
+                for (int r0 = 0; r0 < rows; r0 += 8) {
+                    const int r = r0 + sub;
+                    uint32_t two[kPer / 2];
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int row = row0 + r0 + i;
-                        const bool there = r0 + i < rows;
-                        const E *q = static_cast<const E *>(P.q) + (token0 + row / P.G) * P.q_stride +
-                                     static_cast<int64_t>(head0 + row % P.G) * D + lane * kPer;
+                    for (int c = 0; c < kPer / 8; ++c) two[4 * c] = x[c].x, two[4 * c + 1] = x[c].y, two[4 * c + 2] = x[c].z, two[4 * c + 3] = x[c].w;
+                    if (r0 + 8 < rows) load(r + 8);
+                    float top = 0.f;
+                    bool odd = false;
 #pragma unroll
-                        for (int c = 0; c < kPer; c += 2) {
-                            uint32_t two = 0;
-                            if (there) two = __ldg(reinterpret_cast<const uint32_t *>(q + c));
-                            x[i][c] = sign * wide(reinterpret_cast<const E *>(&two)[0]);
-                            x[i][c + 1] = sign * wide(reinterpret_cast<const E *>(&two)[1]);
-                        }
+                    for (int c = 0; c < kPer; ++c) {
+                        const float a = fabsf(wide(reinterpret_cast<const E *>(&two[c / 2])[c & 1]));
+                        odd |= !(a <= 3.402823466e38f);
+                        top = fmaxf(top, a);
                     }
-                    if (r0 == 0 && items > 0) wait(&S.q_free, (items - 1) & 1);
+                    top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+                    odd = (__ballot_sync(kAll, odd) >> (lane & 28)) & 15;
+                    // the largest is brought into [128, 256): k = 7 - its exponent
+                    const int e = static_cast<int>(__float_as_uint(top) >> 23);
+                    const int k = top == 0.f ? 0 : min(134 - e, 126);
+                    const float up = sign * __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = r0 + i;
-                        float top = 0.f;
-                        bool odd = false;
+                    for (int c0 = 0; c0 < kPer; c0 += 16) {  // one 16-byte chunk of each digit
+                        uint32_t digit[kDigits][4];
 #pragma unroll
-                        for (int c = 0; c < kPer; ++c) {
-                            odd |= !(fabsf(x[i][c]) <= 3.402823466e38f);
-                            top = fmaxf(top, fabsf(x[i][c]));
-                        }
-                        top = tc::warp_max(top);
-                        odd = __any_sync(kAll, odd);
-                        // the largest is brought into [128, 256): k = 7 - its exponent
-                        const int e = static_cast<int>(__float_as_uint(top) >> 23);
-                        const int k = top == 0.f ? 0 : min(134 - e, 126);
-                        const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-                        float left[kPer];
+                        for (int c = 0; c < 16; c += 2) {
+                            const E *v = reinterpret_cast<const E *>(&two[(c0 + c) / 2]);
+                            float a = wide(v[0]) * up, b = wide(v[1]) * up;
 #pragma unroll
-                        for (int c = 0; c < kPer; ++c) left[c] = x[i][c] * up;
-#pragma unroll
-                        for (int g = 0; g < kDigits; ++g) {
-                            uint32_t digit = 0;
-#pragma unroll
-                            for (int c = 0; c < kPer; c += 2) {
-                                const uint32_t two = e4m3x2(left[c], left[c + 1]);
-                                const float2 f = floats_of_e4m3x2(two);
-                                left[c] -= f.x;
-                                left[c + 1] -= f.y;
-                                digit |= two << (8 * c);
+                            for (int g = 0; g < kDigits; ++g) {
+                                const uint32_t d = e4m3x2(a, b);
+                                const float2 f = floats_of_e4m3x2(d);
+                                a -= f.x, b -= f.y;
+                                digit[g][c / 4] = c % 4 == 0 ? d : digit[g][c / 4] | (d << 16);
                             }
-                            uint8_t *to = q_sh + g * F::kQ + tc::swizzled<D>(r, lane * kPer / 16) + (lane * kPer) % 16;
-                            if (kPer == 4)
-                                *reinterpret_cast<uint32_t *>(to) = digit;
-                            else
-                                *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(digit);
                         }
-                        if (lane == 0) {
-                            const bool there = r < rows;
-                            const int pos = pos0 + (row0 + r) / P.G;
-                            float f = size * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-                            if (odd) f = __int_as_float(0x7FC00000);
-                            S.q_factor[items % kItems][r] = there ? f : 0.f;
-                            S.row_keys[items % kItems][r] =
-                                there ? make_int2(P.window > 0 ? pos + 1 - P.window : 0, pos) : make_int2(0, -1);
-                        }
+#pragma unroll
+                        for (int g = 0; g < kDigits; ++g)
+                            *reinterpret_cast<uint4 *>(q_sh + g * F::kQ + tc::swizzled<D>(r, (part_of_row * kPer + c0) / 16)) =
+                                make_uint4(digit[g][0], digit[g][1], digit[g][2], digit[g][3]);
+                    }
+                    if (part_of_row == 0) {
+                        const bool there = r < rows;
+                        const int pos = pos0 + (row0 + r) / P.G;
+                        float f = size * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+                        if (odd) f = __int_as_float(0x7FC00000);
+                        S.q_factor[items % kItems][r] = there ? f : 0.f;
+                        S.row_keys[items % kItems][r] =
+                            there ? make_int2(P.window > 0 ? pos + 1 - P.window : 0, pos) : make_int2(0, -1);
                     }
                 }
                 tc::fence_async_shared();
