@@ -43,7 +43,7 @@ constexpr int kTile = 128;
 constexpr int kMaxCtas = 160;
 constexpr int kMaxRows = 64;
 constexpr int kMaxHead = 128;
-constexpr int kSeqsInside = 512;   // sequences whose prefix sums every CTA makes itself
+constexpr int kSeqsInside = 256;   // sequences whose prefix sums every CTA makes itself
 constexpr int kMaxPairs = 1 << 18;  // (sequence, row block) pairs of a call with longer items
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -266,22 +266,26 @@ struct Form {
     // tiles of 128 keys in one step: two, unless the weights' digits then leave too few slots for K and V
     static constexpr int kSub = R > 32 && kDigits == 3 && D == 128 ? 1 : 2;
     static constexpr int kStep = kSub * kTile;
-    static constexpr int kPitch = R;  // bytes of one digit of a key's weights
-    // fp16 outputs: the weights' second and third digits are of 32 times what is left, and summed apart
-    static constexpr int kOut = kDigits == 3 ? 2 : 1;
-    static constexpr float kFine = 32.f;
-    static constexpr int kUsed = (2 * kSub + 2 * kOut) * N;
+    // O has two columns for each row.  Two digits of a weight (bf16) are the two columns of one product: an
+    // MMA of few columns takes the time of its 128 rows of V (39 clocks at 16 columns, 47 at 64, 62 at 128),
+    // so one of both digits costs little more than one of each.  Of three digits (fp16) the second and third
+    // share a column; they are of 32 times what is left.
+    static constexpr bool kBoth = kDigits == 2;
+    static constexpr float kFine = kBoth ? 1.f : 32.f;
+    static constexpr int kPasses = kBoth ? 1 : kDigits;   // products of O
+    static constexpr int kPitch = kBoth ? 2 * R : R;      // bytes of a key's weights in one product
+    static constexpr int kUsed = (2 * kSub + 4) * N;
     static constexpr int kColumns = kUsed <= 256 ? 256 : 512;
     static constexpr int kSlot = kStep * D;
     static constexpr int kQ = N * D;           // one digit of the queries
-    static constexpr int kP = kStep * kPitch;  // one digit of the weights
+    static constexpr int kP = kStep * kPitch;  // weights of one product
     static_assert((R == 32 || R == 64) && kUsed <= kColumns && kQ % 1024 == 0 && kP % 1024 == 0);
 };
 
 constexpr int kAttendWarps = 16;  // softmax 2 x 4, output 4, TMA, MMA, queries, scout
 constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kSteps = 8;    // steps that the scout may be ahead
-constexpr int kItems = 8;    // items whose row data may be in use at once
+constexpr int kItems = 6;    // items whose row data may be in use at once (steps s - 4 to s, when each is an item of its own)
 constexpr int kMaxSlots = 12;
 constexpr int kSharedBytes = 227 * 1024;  // of one CTA
 constexpr int kConsumers = 4 + 4 + 3;  // warps that read one step: a softmax group, output, TMA, MMA, queries
@@ -313,7 +317,7 @@ struct Shared {
     Step step[kSteps];
     float q_factor[kItems][R];
     int2 row_keys[kItems][R];  // first and last key of a row
-    float4 step_max[2][R];     // of the four warps of a softmax group
+    float4 step_max[4][R];     // of the four warps of a softmax group, for the last steps
     float4 step_sum[2][R];
     float2 joined[2][R];  // factors of the old and the new output
     float final[R];
@@ -373,7 +377,7 @@ __device__ __forceinline__ void reduce_lanes(float (&v)[kN], int lane, Op op) {
 
 // Shared memory besides the ring of K and V slots, which gets the rest.
 template <class F>
-constexpr int kFixedBytes = 1024 + F::kDigits * (F::kQ + 2 * F::kP) + static_cast<int>(sizeof(Shared<F::R>)) + (kSeqsInside + 1) * 4;
+constexpr int kFixedBytes = 1024 + F::kDigits * F::kQ + 2 * F::kPasses * F::kP + static_cast<int>(sizeof(Shared<F::R>)) + (kSeqsInside + 1) * 4;
 template <class F>
 constexpr int kSlots = (kSharedBytes - kFixedBytes<F>) / F::kSlot < kMaxSlots ? (kSharedBytes - kFixedBytes<F>) / F::kSlot : kMaxSlots;
 
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     uint8_t *ring = base;
     uint8_t *q_sh = ring + kSlots<F> * F::kSlot;
     uint8_t *p_sh = q_sh + kDigits * F::kQ;
-    Shared<R> &S = *reinterpret_cast<Shared<R> *>(p_sh + 2 * kDigits * F::kP);
+    Shared<R> &S = *reinterpret_cast<Shared<R> *>(p_sh + 2 * F::kPasses * F::kP);
     int32_t *sums_sh = reinterpret_cast<int32_t *>(&S + 1);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kAll, tid >> 5, 0);
@@ -484,17 +488,17 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         // ---- softmax: one key of each tile per thread; the two groups take steps in turn ----
         const int group = warp >> 2, quad = warp & 3, key = tid & 127;
         const uint32_t s_at = tmem + group * (kSub * N) + (static_cast<uint32_t>(quad) << 21);
-        uint8_t *p_at = p_sh + group * (kDigits * F::kP);
-        float *max_sh = reinterpret_cast<float *>(S.step_max[group]);
-        float *sum_sh = reinterpret_cast<float *>(S.step_sum[group]);
+        uint8_t *p_at = p_sh + group * (F::kPasses * F::kP);
         // Rows pass in chunks of eight, twice: for the largest scores, then for the weights.  S is read from TMEM
         // each time: the loops stay small enough for the instruction cache (unrolled over 32 rows, instruction
         // fetches took 7 of every 18 stalled cycles), and no row count needs registers of its own.
         for (int it = group;; it += 2) {
             const int phase = (it >> 1) & 1;
+            const float4 *max_of = S.step_max[it & 3];
+            float *max_sh = reinterpret_cast<float *>(S.step_max[it & 3]), *sum_sh = reinterpret_cast<float *>(S.step_sum[group]);
             const Step &st = open_step(it);
             const bool stop = !st.live;
-            const int item = st.item & (kItems - 1), chunks = (st.rows + 7) >> 3;
+            const int item = stop ? 0 : st.item, chunks = (st.rows + 7) >> 3;
             const float *q_factor = S.q_factor[item];
             const bool plain = st.plain, odd = st.odd;
             float ks[kSub], f[kSub];
@@ -530,8 +534,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (!stop) {
                 wait(&S.s_full[group], phase);
                 tc::fence_after();
-                // the output warps have read what this group's buffers held before
-                if (it >= 2) wait(&S.o_free[group], phase ^ 1);
                 // largest score of each row: over the thread's keys, the warp's lanes, the group's warps
 #pragma unroll 1
                 for (int c = 0; c < chunks; ++c) {
@@ -547,6 +549,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 }
             }
             if (tc::barrier_or(1 + group, 128, stop || gave_up())) break;
+            // the weights this group wrote before have been used
+            if (it >= 2) wait(&S.o_free[group], phase ^ 1);
 
             // weights 2^(score - largest), their sums over the keys, and the digits of weight x value scale (<= 256)
 #pragma unroll 1
@@ -556,7 +560,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 scores(r0, s);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float4 m4 = S.step_max[group][r0 + i];
+                    const float4 m4 = max_of[r0 + i];
                     // without a key the largest is -inf: 2^(-inf + 1e30) is 0 all the same
                     const float m = fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), -1e30f);
                     const float qf = q_factor[r0 + i];
@@ -584,7 +588,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                                 if (e == i) s[u][e] = 0.f;
                         }
                     }
-                    uint8_t *to = p_at + tc::swizzled<kPitch>(u * kTile + key, c >> 1) + (c & 1) * 8;
 #pragma unroll
                     for (int g = 0; g < kDigits; ++g) {
                         uint32_t words[2];
@@ -596,13 +599,16 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                             if (g + 1 < kDigits) {
                                 const float2 fa = floats_of_e4m3x2(a), fb = floats_of_e4m3x2(b);
                                 w[0] -= fa.x, w[1] -= fa.y, w[2] -= fb.x, w[3] -= fb.y;
-                                if (F::kOut == 2 && g == 0) {
+                                if (F::kFine != 1.f && g == 0) {
 #pragma unroll
                                     for (int e = 0; e < 4; ++e) w[e] *= F::kFine;
                                 }
                             }
                         }
-                        *reinterpret_cast<uint2 *>(to + g * F::kP) = make_uint2(words[0], words[1]);
+                        const int at = F::kBoth ? g * chunks + c : c;  // in units of 8 bytes of the key's row
+                        *reinterpret_cast<uint2 *>(p_at + (F::kBoth ? 0 : g * F::kP) +
+                                                   tc::swizzled<kPitch>(u * kTile + key, at >> 1) + (at & 1) * 8) =
+                            make_uint2(words[0], words[1]);
                     }
                 }
             }
@@ -666,7 +672,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             }
             if (!stop) wait(&S.p_full[buf], phase);
             if (!stop && ch < st.rows) {
-                const float4 m4 = S.step_max[buf][ch], l4 = S.step_sum[buf][ch];
+                const float4 m4 = S.step_max[it & 3][ch], l4 = S.step_sum[buf][ch];
                 const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
                 const float m_new = fmaxf(m_run, m);
                 const float ref = m_new == -INFINITY ? 0.f : m_new;
@@ -678,20 +684,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (tc::barrier_or(3, 128, stop || gave_up())) break;
             wait(&S.o_full[buf], phase);
             tc::fence_after();
-            const uint32_t at = tmem + 2 * kSub * N + buf * (F::kOut * N) + (static_cast<uint32_t>(quad) << 21);
-            const int rows = st.rows;
+            const uint32_t at = tmem + 2 * kSub * N + buf * (2 * N) + (static_cast<uint32_t>(quad) << 21);
+            const int rows = st.rows, second = F::kBoth ? (rows + 7) & ~7 : N;
 #pragma unroll
             for (int r0 = 0; r0 < R; r0 += 8) {
                 if (r0 < rows) {
-                    float o[F::kOut][8];
-#pragma unroll
-                    for (int g = 0; g < F::kOut; ++g) tc::tmem_load<8>(o[g], at + g * N + r0);
+                    float o[2][8];
+                    tc::tmem_load<8>(o[0], at + r0);
+                    tc::tmem_load<8>(o[1], at + second + r0);
                     tc::tmem_wait_load(o);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        if (F::kOut == 2) o[0][i] = fmaf(o[F::kOut - 1][i], 1.f / F::kFine, o[0][i]);
                         const float2 f = S.joined[buf][r0 + i];
-                        acc[r0 + i] = fmaf(o[0][i], f.y, acc[r0 + i] * f.x);
+                        acc[r0 + i] = fmaf(fmaf(o[1][i], 1.f / F::kFine, o[0][i]), f.y, acc[r0 + i] * f.x);
                     }
                 }
             }
@@ -802,12 +807,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 #pragma unroll 1
                 for (int u = 0; u < subs; ++u) {
 #pragma unroll 1
-                    for (int g = 0; g < kDigits; ++g)
+                    for (int g = 0; g < F::kPasses; ++g)
 #pragma unroll
                         for (int k = 0; k < kTile / 32; ++k)
-                            tc::mma_e4m3(tmem + 2 * kSub * N + buf * (F::kOut * N) + (F::kOut == 2 && g > 0 ? N : 0), ring_k + ((slot * F::kSlot + (u * kTile + k * 32) * D) >> 4),
-                                         p_desc + (((buf * kDigits + g) * F::kP + (u * kTile + k * 32) * kPitch) >> 4), shape,
-                                         u + k + (F::kOut == 2 ? (g == 2) : g) > 0);
+                            tc::mma_e4m3(tmem + 2 * kSub * N + buf * (2 * N) + (!F::kBoth && g > 0 ? N : 0),
+                                         ring_k + ((slot * F::kSlot + (u * kTile + k * 32) * D) >> 4),
+                                         p_desc + (((buf * F::kPasses + g) * F::kP + (u * kTile + k * 32) * kPitch) >> 4), shape,
+                                         u + k + (g == 2) > 0);
                 }
                 tc::mma_commit(&S.o_full[buf]);
                 tc::mma_commit(&S.empty[slot]);
@@ -820,8 +826,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const int buf = n & 1, phase = (n >> 1) & 1;
             const Step &st = open_step(n);
             if (!st.live || __any_sync(kAll, gave_up())) break;
-            const int subs = st.subs, first = st.first, last = st.last, columns = (st.rows + 15) & ~15;
-            const uint32_t shape = tc::mma_shape(columns, false, false);
+            const int subs = st.subs, first = st.first, last = st.last, rows = st.rows;
+            const uint32_t shape = tc::mma_shape((rows + 15) & ~15, false, false);
+            const int columns = F::kBoth ? 2 * ((rows + 7) & ~7) : (rows + 15) & ~15;  // of O
             close_step(n);
             if (first) wait(&S.q_full, items++ & 1);
             const int place = place_of_k(n), slot = place % slots;
