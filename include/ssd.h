@@ -524,8 +524,9 @@ int ssd_kv_append(const void *k, const void *v, int dtype, int64_t k_stride, int
  * digits next to its row's largest, and so does each softmax weight, rounded to
  * two or three of them (2^-8 and 2^-12 of the weight, as bf16 and fp16 would be).
  * workspace: ssd_kv_workspace_size() bytes, 256-byte aligned, zero-filled before
- *   its first use and left ready by each call; calls that share one must not
- *   overlap on the GPU.
+ *   its first use and left ready by each call (not by one that reported
+ *   SSD_DEV_TIMEOUT: zero it again); calls that share one must not overlap on the
+ *   GPU.
  */
 size_t ssd_kv_workspace_size(void);
 int ssd_kv_attend(const void *q, int dtype, int64_t q_stride, const void *k_cache, const void *v_cache,

@@ -634,6 +634,47 @@ def desc_fields(desc: torch.Tensor):
 # The loop around a round: the paged 8-bit cache and truncated sampling.
 # ---------------------------------------------------------------------------
 
+# These calls take microseconds on the GPU, so their Python side counts: tensors are
+# checked and turned into addresses in one go, and the current stream is looked up as a
+# plain number.
+try:
+    _current_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _current_stream(device: int) -> int:
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+def _stream_at(stream, t) -> int:
+    if stream is None:
+        return _current_stream(t.get_device())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _at(t, name: str, dtype, shape) -> int:
+    """Address of a contiguous CUDA tensor of that dtype and shape."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _cuda(t, name: str, dim: int):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {list(t.shape)}")
+    return t.shape
+
+
+def _status_at(dev_status):
+    return None if dev_status is None else _at(dev_status, "dev_status", torch.int32, dev_status.shape)
+
+
 def _on(stream, *made):
     """Tensors allocated here for a call on another stream than the current one: the
     allocator must not hand their memory on before that stream has used it."""
@@ -642,13 +683,6 @@ def _on(stream, *made):
         for t in made:
             if t is not None:
                 t.record_stream(s)
-
-
-def _shaped(t, name, dtype, shape):
-    _dev(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
 
 
 def kv_state(B: int, max_blocks: int, num_pages: int, device=None) -> dict:
@@ -671,83 +705,78 @@ def ssd_kv_plan(seq_len, new_len, held, block_table, ring, ring_state, page_size
     slots: updates seq_len, held, block_table, ring and ring_state in place and returns
     dict(cu_new [B+1], kv_len [B], slots [cap], positions [cap]), all int32."""
     i32 = torch.int32
-    _dev(seq_len, "seq_len", i32)
-    if seq_len.dim() != 1:
-        raise ValueError("seq_len must be [B]")
-    B = seq_len.shape[0]
-    _shaped(new_len, "new_len", i32, (B,))
-    _shaped(held, "held", i32, (B,))
-    if accept_len is not None:
-        _shaped(accept_len, "accept_len", i32, (B,))
-    _dev(block_table, "block_table", i32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    B, = _cuda(seq_len, "seq_len", 1)
+    rows, max_blocks = _cuda(block_table, "block_table", 2)
+    num_pages, = _cuda(ring, "ring", 1)
+    cap, of_b = int(cap), (B,)
+    if rows != B:
         raise ValueError("block_table must be [B, max_blocks]")
-    _dev(ring, "ring", i32)
-    _shaped(ring_state, "ring_state", i32, (2,))
-    if ring.dim() != 1:
-        raise ValueError("ring must be [num_pages]")
-    o = dict(out) if out is not None else {}
-    made = []
-    for name, shape in (("cu_new", (B + 1,)), ("kv_len", (B,)), ("slots", (int(cap),)), ("positions", (int(cap),))):
-        if name not in o:
-            o[name] = torch.empty(shape, dtype=i32, device=seq_len.device)
-            made.append(o[name])
-        _shaped(o[name], name, i32, shape)
+    if cap < 0:
+        raise ValueError("cap must not be negative")
+    o, made, at = ({} if out is None else dict(out)), [], []
+    for name, n in (("cu_new", B + 1), ("kv_len", B), ("slots", cap), ("positions", cap)):
+        t = o.get(name)
+        if t is None:
+            t = o[name] = torch.empty(n, dtype=i32, device=seq_len.device)
+            made.append(t)
+            at.append(t.data_ptr())
+        else:
+            at.append(_at(t, name, i32, (n,)))
     _check(lib().ssd_kv_plan(
-        _ptr(seq_len), _ptr(accept_len), _ptr(new_len), _ptr(held), B, _ptr(block_table),
-        int(block_table.shape[1]), _ptr(ring), _ptr(ring_state), int(ring.shape[0]), int(page_size), int(cap),
-        _ptr(o["cu_new"]), _ptr(o["kv_len"]), _ptr(o["slots"]), _ptr(o["positions"]),
-        _ptr(_opt(dev_status, "dev_status", i32)), _stream(stream)), "ssd_kv_plan")
-    _on(stream, *made)
+        _at(seq_len, "seq_len", i32, of_b), None if accept_len is None else _at(accept_len, "accept_len", i32, of_b),
+        _at(new_len, "new_len", i32, of_b), _at(held, "held", i32, of_b), B,
+        _at(block_table, "block_table", i32, (B, max_blocks)), max_blocks, _at(ring, "ring", i32, (num_pages,)),
+        _at(ring_state, "ring_state", i32, (2,)), num_pages, int(page_size), cap, *at, _status_at(dev_status),
+        _stream_at(stream, seq_len)), "ssd_kv_plan")
+    if stream is not None:
+        _on(stream, *made)
     return o
 
 
 _KV_DTYPES = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16, torch.float16: SSD_F16}
 
 
+_BYTES = (torch.float8_e4m3fn, torch.uint8)
+
+
 def _kv_cache(k_cache, v_cache, k_scale, v_scale):
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _dev(t, name)
-        if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
-            raise TypeError(f"{name} must be float8_e4m3fn or uint8, got {t.dtype}")
-        if t.dim() != 4 or t.shape != k_cache.shape:
-            raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, D]")
-    N, H, P, D = k_cache.shape
-    _shaped(k_scale, "k_scale", torch.float32, (N, H))
-    _shaped(v_scale, "v_scale", torch.float32, (N, H))
-    return N, H, P, D
+    """(num_pages, Hkv, page_size, D) and the four addresses."""
+    shape = _cuda(k_cache, "k_cache", 4)
+    kind = k_cache.dtype
+    if kind not in _BYTES:
+        raise TypeError(f"k_cache must be float8_e4m3fn or uint8, got {kind}")
+    blocks = shape[:2]
+    return shape, (_at(k_cache, "k_cache", kind, shape), _at(v_cache, "v_cache", kind, shape),
+                   _at(k_scale, "k_scale", torch.float32, blocks), _at(v_scale, "v_scale", torch.float32, blocks))
 
 
 def _tokens(t, name, H, D):
-    """Token stride of a [T, H, D] tensor whose heads and channels are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    """(T, heads, token stride) of a [T, H, D] tensor whose heads and channels are contiguous."""
+    T, heads, width = _cuda(t, name, 3)
     if t.dtype not in _KV_DTYPES:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != D or (H is not None and t.shape[1] != H):
+    if width != D or (H is not None and heads != H):
         raise ValueError(f"{name} must be [T, {'heads' if H is None else H}, {D}]")
-    T, heads, _ = t.shape
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+    ld, per_head, per_channel = t.stride()
+    if per_channel != 1 or (heads > 1 and per_head != D):
         raise ValueError(f"{name}: heads and channels must be contiguous")
-    ld = t.stride(0) if T > 1 else heads * D
+    if T <= 1:
+        ld = heads * D
     if ld < heads * D:
         raise ValueError(f"{name}: tokens overlap")
-    return int(ld)
+    return T, heads, ld
 
 
 def ssd_kv_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, *, dev_status=None, stream=None):
     """Stores keys and values [T, Hkv, D] (views with a longer token stride are fine) at
     `slots` of the e4m3 cache, growing the touched pages' power-of-two scales in place."""
-    N, H, P, D = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    ks, vs = _tokens(k, "k", H, D), _tokens(v, "v", H, D)
-    if v.shape != k.shape or v.dtype != k.dtype:
+    (N, H, P, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    (T, _, ks), (Tv, _, vs) = _tokens(k, "k", H, D), _tokens(v, "v", H, D)
+    if T != Tv or v.dtype is not k.dtype:
         raise ValueError("k and v must match in shape and dtype")
-    T = int(k.shape[0])
-    _shaped(slots, "slots", torch.int32, (T,))
     _check(lib().ssd_kv_append(
-        _ptr(k), _ptr(v), _KV_DTYPES[k.dtype], ks, vs, _ptr(slots), T, H, D, _ptr(k_cache), _ptr(v_cache),
-        _ptr(k_scale), _ptr(v_scale), N, P, _ptr(_opt(dev_status, "dev_status", torch.int32)),
-        _stream(stream)), "ssd_kv_append")
+        k.data_ptr(), v.data_ptr(), _KV_DTYPES[k.dtype], ks, vs, _at(slots, "slots", torch.int32, (T,)), T, H, D,
+        *cache, N, P, _status_at(dev_status), _stream_at(stream, k)), "ssd_kv_append")
 
 
 def kv_workspace(device=None) -> torch.Tensor:
@@ -759,36 +788,31 @@ def ssd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, kv
                   sm_scale: float, *, window: int = 0, out=None, workspace=None, dev_status=None, stream=None):
     """Causal attention of q [T, Hq, D] (bf16 or fp16) over the paged e4m3 cache: returns
     out [T, Hq, D].  cu_new and kv_len as from ssd_kv_plan."""
-    N, Hkv, P, D = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    ld = _tokens(q, "q", None, D)
-    T, Hq, _ = q.shape
-    _dev(kv_len, "kv_len", torch.int32)
-    if kv_len.dim() != 1:
-        raise ValueError("kv_len must be [B]")
-    B = int(kv_len.shape[0])
-    _shaped(cu_new, "cu_new", torch.int32, (B + 1,))
-    _dev(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    (N, Hkv, P, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    T, Hq, ld = _tokens(q, "q", None, D)
+    B, = _cuda(kv_len, "kv_len", 1)
+    rows, max_blocks = _cuda(block_table, "block_table", 2)
+    if rows != B:
         raise ValueError("block_table must be [B, max_blocks]")
-    made = []
+    i32, made = torch.int32, []
     if out is None:
         out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
         made.append(out)
-    _shaped(out, "out", q.dtype, (T, Hq, D))
     if workspace is None:
         workspace = kv_workspace(q.device)
         made.append(workspace)
-    _dev(workspace, "workspace", torch.uint8)
-    if stream is not None and made:
-        # the fill of a workspace made here runs on the current stream
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        s.wait_stream(torch.cuda.current_stream())
+        if stream is not None:
+            # its fill runs on the current stream
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+            s.wait_stream(torch.cuda.current_stream())
     _check(lib().ssd_kv_attend(
-        _ptr(q), _KV_DTYPES[q.dtype], ld, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), N, P,
-        int(Hq), Hkv, D, _ptr(block_table), int(block_table.shape[1]), _ptr(cu_new), _ptr(kv_len), B, int(T),
-        int(max_new), float(sm_scale), int(window), _ptr(out), _ptr(workspace), workspace.numel(),
-        _ptr(_opt(dev_status, "dev_status", torch.int32)), _stream(stream)), "ssd_kv_attend")
-    _on(stream, *made)
+        q.data_ptr(), _KV_DTYPES[q.dtype], ld, *cache, N, P, Hq, Hkv, D,
+        _at(block_table, "block_table", i32, (B, max_blocks)), max_blocks, _at(cu_new, "cu_new", i32, (B + 1,)),
+        _at(kv_len, "kv_len", i32, (B,)), B, T, int(max_new), float(sm_scale), int(window),
+        _at(out, "out", q.dtype, (T, Hq, D)), _at(workspace, "workspace", torch.uint8, workspace.shape),
+        workspace.numel(), _status_at(dev_status), _stream_at(stream, q)), "ssd_kv_attend")
+    if stream is not None:
+        _on(stream, *made)
     return out
 
 
@@ -798,45 +822,38 @@ def ssd_sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=N
     under temperature, top-k, top-p and min-p: returns dict(tokens, prob[, filtered]).
     filtered: True, or a tensor of the logits' shape and strides, for the logits with every
     dropped token at SSD_DROPPED_LOGIT."""
-    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
-        raise TypeError("logits must be a CUDA tensor")
+    R, V = _cuda(logits, "logits", 2)
     dt = _logit_dtype(logits)
-    if logits.dim() != 2:
-        raise ValueError("logits must be [rows, V]")
-    R, V = logits.shape
-    ld = logits.stride(0) if R > 1 else V
-    if logits.stride(1) != 1 or ld < V:
+    ld, step = logits.stride()
+    if R <= 1:
+        ld = V
+    if step != 1 or ld < V:
         raise ValueError("logits: rows must be contiguous and must not overlap")
-    _shaped(temperature, "temperature", torch.float32, (R,))
-    _shaped(uniforms, "uniforms", torch.float32, (R,))
-    for t, name, dty in ((top_k, "top_k", torch.int32), (top_p, "top_p", torch.float32),
-                         (min_p, "min_p", torch.float32)):
-        if t is not None:
-            _shaped(t, name, dty, (R,))
-    made = []
-
-    def new(t, name, dty):
-        if t is None:
-            t = torch.empty(R, dtype=dty, device=logits.device)
-            made.append(t)
-        return _shaped(t, name, dty, (R,))
-
-    tokens, prob = new(tokens, "tokens", torch.int32), new(prob, "prob", torch.float32)
+    f32, i32, of_r, made = torch.float32, torch.int32, (R,), []
+    if tokens is None:
+        tokens = torch.empty(R, dtype=i32, device=logits.device)
+        made.append(tokens)
+    if prob is None:
+        prob = torch.empty(R, dtype=f32, device=logits.device)
+        made.append(prob)
     if filtered is True:
         filtered = torch.empty((R, ld), dtype=logits.dtype, device=logits.device)[:, :V]
         made.append(filtered)
     elif filtered is False:
         filtered = None
     if filtered is not None:
-        if not isinstance(filtered, torch.Tensor) or not filtered.is_cuda or filtered.dtype != logits.dtype:
+        if not isinstance(filtered, torch.Tensor) or not filtered.is_cuda or filtered.dtype is not logits.dtype:
             raise TypeError("filtered must be a CUDA tensor of the logits' dtype")
         if filtered.shape != logits.shape or filtered.stride(1) != 1 or (R > 1 and filtered.stride(0) != ld):
             raise ValueError("filtered must have the logits' shape and strides")
     _check(lib().ssd_sample(
-        _ptr(logits), dt, int(R), int(V), int(ld), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
-        _ptr(uniforms), _ptr(tokens), _ptr(prob), _ptr(filtered), _ptr(_opt(dev_status, "dev_status", torch.int32)),
-        _stream(stream)), "ssd_sample")
-    _on(stream, *made)
+        logits.data_ptr(), dt, R, V, ld, _at(temperature, "temperature", f32, of_r),
+        None if top_k is None else _at(top_k, "top_k", i32, of_r), None if top_p is None else _at(top_p, "top_p", f32, of_r),
+        None if min_p is None else _at(min_p, "min_p", f32, of_r), _at(uniforms, "uniforms", f32, of_r),
+        _at(tokens, "tokens", i32, of_r), _at(prob, "prob", f32, of_r), None if filtered is None else filtered.data_ptr(),
+        _status_at(dev_status), _stream_at(stream, logits)), "ssd_sample")
+    if stream is not None:
+        _on(stream, *made)
     out = {"tokens": tokens, "prob": prob}
     if filtered is not None:
         out["filtered"] = filtered

@@ -28,10 +28,12 @@
 //
 // Work split.  All tiles of all items form one line, which the CTAs cut into equal
 // stretches: ragged lengths and few sequences fill the GPU alike.  A CTA whose stretch ends
-// inside an item leaves a partial result (output, maximum, sum) in the workspace, and a
-// second kernel, started as the first drains, joins the parts in the order of their keys.
+// inside an item leaves a partial result (output, maximum, sum) in the workspace, and the
+// CTA that brings an item's last part joins them all.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <atomic>
 
 #include "ssd_kv.h"
 #include "ssd_tc.h"
@@ -47,18 +49,10 @@ constexpr int kSeqsInside = 256;   // sequences whose prefix sums every CTA make
 constexpr int kMaxPairs = 1 << 18;  // (sequence, row block) pairs of a call with longer items
 constexpr float kLog2e = 1.4426950408889634f;
 
-// What a CTA tells the joining kernel: the item whose first part it holds.
-struct Join {
-    int32_t last_cta;  // -1: nothing to join
-    int32_t first_token;
-    int32_t row0, rows, head;
-    int32_t pad[3];
-};
-
 struct Workspace {
     float o[2 * kMaxCtas][kMaxRows][kMaxHead];
     float2 ml[2 * kMaxCtas][kMaxRows];
-    Join join[kMaxCtas];
+    int32_t arrived[kMaxCtas];  // parts of the item that starts in each CTA; left at 0
     int32_t pairs;              // of the schedule below
     int32_t sums[kMaxPairs + 1];  // steps before each pair
     int32_t seq[kMaxPairs];
@@ -128,8 +122,7 @@ struct Part {
     int first, pos0;      // of the sequence
     int start, stop;      // keys that any row attends to
     int step, steps;      // this part's
-    bool from_start, to_end;
-    int last_cta;         // CTA that holds the item's last step
+    int first_cta, parts;  // CTAs that the item is cut over: first_cta and the parts - 1 after it
 };
 
 struct Walk {
@@ -154,10 +147,9 @@ struct Walk {
         const int done = (unit - base) - part.head * all;
         part.step = k.step0 + done;
         part.steps = min(all - done, end - unit);
-        part.from_start = done == 0;
-        part.to_end = done + part.steps == all;
-        const int64_t item_end = static_cast<int64_t>(base) + static_cast<int64_t>(part.head + 1) * all;
-        part.last_cta = static_cast<int>((item_end * ctas - 1) / units);
+        const int64_t item = static_cast<int64_t>(base) + static_cast<int64_t>(part.head) * all;
+        part.first_cta = static_cast<int>(((item + 1) * ctas - 1) / units);
+        part.parts = static_cast<int>(((item + all) * ctas - 1) / units) - part.first_cta + 1;
         unit += part.steps;
         return true;
     }
@@ -301,7 +293,7 @@ struct Step {
     int32_t common_from, common_to;  // ... and that every row does
     int32_t there;      // bit p: page p is there
     int32_t item;       // row data of kItems
-    int32_t from_start, to_end, last_cta;
+    int32_t first_cta, parts;  // of the item
     int32_t seq, head, row0, rows, token0, pos0;
     int32_t part_key0;  // first key of the part
     float v_unit;       // what the weights' value scales were divided by
@@ -325,6 +317,7 @@ struct Shared {
     uint32_t tmem;
     int nan_met;
     int gave_up;
+    int last_part;
     int red[kAttendWarps];
 };
 
@@ -400,6 +393,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     const int cta = blockIdx.x;
     constexpr int slots = kSlots<F>;
 
+    if (tid == 0) tc::prefetch_map(&k_map), tc::prefetch_map(&v_map);
     // ---- schedule -------------------------------------------------------------------
     Walk walk;
     if (P.inside) {
@@ -461,7 +455,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         S.nan_met = 0;
         S.gave_up = 0;
         fence_mbar_init();
-        P.ws->join[cta].last_cta = -1;
     }
     if (busy && warp == 13) tc::tmem_alloc(&S.tmem, F::kColumns);
     tc::fence_before();
@@ -661,15 +654,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const int ch = tid - 256, quad = warp & 3;
         float acc[R];
         float m_run = -INFINITY, l_run = 0.f;  // of row ch
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r] = 0.f;
         for (int it = 0;; ++it) {
             const int buf = it & 1, phase = (it >> 1) & 1;
             const Step &st = open_step(it);
             const bool stop = !st.live;
-            if (st.first) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) acc[r] = 0.f;
-                m_run = -INFINITY, l_run = 0.f;
-            }
             if (!stop) wait(&S.p_full[buf], phase);
             if (!stop && ch < st.rows) {
                 const float4 m4 = S.step_max[it & 3][ch], l4 = S.step_sum[buf][ch];
@@ -721,7 +711,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         }
                     }
                 }
-                if (st.from_start && st.to_end) {
+                if (st.parts == 1) {
                     if (ch < R) {
                         const int row = st.row0 + ch;
                         const int token = st.token0 + row / P.G, head = st.head * P.G + row % P.G;
@@ -737,22 +727,92 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     }
                     tc::named_barrier(3, 128);
                 } else {
-                    const int slot = 2 * cta + (st.from_start ? 1 : 0);
-                    if (ch < R) P.ws->ml[slot][ch] = make_float2(m_run, l_run);
+                    // The part goes to the workspace; the CTA that brings the last one joins them, in the order of
+                    // their keys whoever that is.
+                    Workspace &W = *P.ws;
+                    const int rows = st.rows, parts = st.parts, first_cta = st.first_cta;
+                    auto slot_of = [&](int c) { return 2 * c + (c == first_cta ? 1 : 0); };
+                    const int slot = slot_of(cta);
+                    if (ch < rows) __stcg(&W.ml[slot][ch], make_float2(m_run, l_run));
                     if (ch < D)
 #pragma unroll
                         for (int r = 0; r < R; ++r)
-                            if (r < st.rows) P.ws->o[slot][r][ch] = acc[r];
-                    if (st.from_start && ch == 0) {
-                        Join jn{};
-                        jn.last_cta = st.last_cta;
-                        jn.first_token = st.token0;
-                        jn.row0 = st.row0;
-                        jn.rows = st.rows;
-                        jn.head = st.head;
-                        P.ws->join[cta] = jn;
+                            if (r < rows) __stcg(&W.o[slot][r][ch], acc[r]);
+                    __threadfence();
+                    tc::named_barrier(3, 128);
+                    if (ch == 0) S.last_part = atomicAdd(&W.arrived[first_cta], 1) == parts - 1;
+                    tc::named_barrier(3, 128);
+                    if (S.last_part) {
+                        __threadfence();
+                        if (ch == 0) W.arrived[first_cta] = 0;
+                        // each part's share of a row, in place of its maximum
+                        constexpr int kHeld = 8;
+                        if (ch < rows) {
+                            float2 ml[kHeld];
+#pragma unroll
+                            for (int i = 0; i < kHeld; ++i)
+                                ml[i] = i < parts ? __ldcg(&W.ml[slot_of(first_cta + i)][ch]) : make_float2(-INFINITY, 0.f);
+                            float top = -INFINITY, total = 0.f;
+#pragma unroll
+                            for (int i = 0; i < kHeld; ++i) top = fmaxf(top, ml[i].x);
+#pragma unroll 8
+                            for (int i = kHeld; i < parts; ++i) top = fmaxf(top, __ldcg(&W.ml[slot_of(first_cta + i)][ch]).x);
+                            const float ref = top == -INFINITY ? 0.f : top;
+                            auto weight = [&](float2 v) { return v.y * (v.x == -INFINITY ? 1.f : ex2(v.x - ref)); };
+#pragma unroll
+                            for (int i = 0; i < kHeld; ++i) total += weight(ml[i]);
+#pragma unroll 8
+                            for (int i = kHeld; i < parts; ++i) total += weight(__ldcg(&W.ml[slot_of(first_cta + i)][ch]));
+                            const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+                            for (int i = 0; i < kHeld; ++i)
+                                if (i < parts) __stcg(&W.ml[slot_of(first_cta + i)][ch].x, ex2(ml[i].x - ref) * inv);
+#pragma unroll 8
+                            for (int i = kHeld; i < parts; ++i) {
+                                float2 *at = &W.ml[slot_of(first_cta + i)][ch];
+                                __stcg(&at->x, ex2(__ldcg(at).x - ref) * inv);
+                            }
+                            const int row = st.row0 + ch;
+                            S.out_at[ch] = (static_cast<int64_t>(st.token0 + row / P.G) * P.Hq + st.head * P.G + row % P.G) * D;
+                        }
+                        tc::named_barrier(3, 128);
+                        if (ch < D) {
+                            E *out = static_cast<E *>(P.out) + ch;
+                            constexpr int kRows = 8;  // of four parts in flight
+#pragma unroll 1
+                            for (int r0 = 0; r0 < rows; r0 += kRows) {
+                                float sum[kRows];
+#pragma unroll
+                                for (int k = 0; k < kRows; ++k) sum[k] = 0.f;
+#pragma unroll 1
+                                for (int i = 0; i < parts; i += 4) {
+                                    float w[4][kRows], o[4][kRows];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const int from = slot_of(first_cta + min(i + e, parts - 1));
+#pragma unroll
+                                        for (int k = 0; k < kRows; ++k) {
+                                            const int row = min(r0 + k, rows - 1);
+                                            w[e][k] = i + e < parts ? __ldcg(&W.ml[from][row].x) : 0.f;
+                                            o[e][k] = i + e < parts ? __ldcg(&W.o[from][row][ch]) : 0.f;
+                                        }
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                                        for (int k = 0; k < kRows; ++k) sum[k] = fmaf(w[e][k], o[e][k], sum[k]);
+                                }
+#pragma unroll
+                                for (int k = 0; k < kRows; ++k)
+                                    if (r0 + k < rows) out[S.out_at[r0 + k]] = narrow<E>(sum[k]);
+                            }
+                        }
+                        tc::named_barrier(3, 128);
                     }
                 }
+#pragma unroll
+                for (int r = 0; r < R; ++r) acc[r] = 0.f;
+                m_run = -INFINITY, l_run = 0.f;
             }
             close_step(it);
         }
@@ -1007,7 +1067,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                             st.common_from = common_from, st.common_to = common_to;
                             st.there = static_cast<int32_t>(mask);
                             st.item = items % kItems;
-                            st.from_start = part.from_start, st.to_end = part.to_end, st.last_cta = part.last_cta;
+                            st.first_cta = part.first_cta, st.parts = part.parts;
                             st.seq = part.b, st.head = part.head, st.row0 = part.row0, st.rows = part.rows;
                             st.token0 = part.first, st.pos0 = part.pos0;
                             st.part_key0 = key0;
@@ -1040,58 +1100,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     if (warp == 13) tc::tmem_free(tmem, F::kColumns);
 }
 
-// Joins the parts of the items that several CTAs share: one warp per row.
-template <class E, int D>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendParams P) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int cta = blockIdx.x, lane = threadIdx.x & 31;
-    const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
-    const Join jn = P.ws->join[cta];
-    if (jn.last_cta < 0 || r >= jn.rows) return;
-    const int parts = jn.last_cta - cta + 1;
-    auto slot = [&](int i) { return i == 0 ? 2 * cta + 1 : 2 * (cta + i); };
-    float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, P.ws->ml[slot(i)][r].x);
-    top = tc::warp_max(top);
-    const float ref = top == -INFINITY ? 0.f : top;
-    constexpr int kPer = D / 32;
-    float acc[kPer], total = 0.f;
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-        float w = 0.f, l = 0.f;
-        if (i0 + lane < parts) {
-            const float2 ml = P.ws->ml[slot(i0 + lane)][r];
-            w = ex2(ml.x - ref);
-            l = ml.y * (ml.x == -INFINITY ? 1.f : w);
-        }
-        const int n = min(32, parts - i0);
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
-            total += __shfl_sync(0xFFFFFFFFu, l, i);
-            const float *o = &P.ws->o[slot(i0 + i)][r][lane * kPer];
-#pragma unroll
-            for (int c = 0; c < kPer; ++c) acc[c] = fmaf(wi, o[c], acc[c]);
-        }
-    }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    const int row = jn.row0 + r;
-    E *out = static_cast<E *>(P.out) +
-             (static_cast<int64_t>(jn.first_token + row / P.G) * P.Hq + jn.head * P.G + row % P.G) * D + lane * kPer;
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) out[c] = narrow<E>(acc[c] * inv);
-}
-
 struct Device {
-    int sms = 0;
+    int id = 0, sms = 0;
     int smem_cta = 0;
 };
 int device_limits(Device *d) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d->smem_cta, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) {
+    if (cudaGetDevice(&d->id) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->id) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d->smem_cta, cudaDevAttrMaxSharedMemoryPerBlockOptin, d->id) != cudaSuccess) {
         cudaGetLastError();
         return SSD_ERR_CUDA;
     }
@@ -1104,9 +1120,14 @@ int attend_launch(AttendParams P, const CUtensorMap &k_map, const CUtensorMap &v
     static_assert(kSlots<F> >= 4);
     const int dyn = kFixedBytes<F> + kSlots<F> * F::kSlot;
     if (dyn > dev.smem_cta) return SSD_ERR_UNSUPPORTED;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess) {
-        cudaGetLastError();
-        return SSD_ERR_CUDA;
+    static std::atomic<uint64_t> ready{0};  // devices on which this kernel may take that much
+    const uint64_t bit = 1ull << (dev.id & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess) {
+            cudaGetLastError();
+            return SSD_ERR_CUDA;
+        }
+        ready.fetch_or(bit, std::memory_order_relaxed);
     }
     P.rows_per_item = F::R;
     P.step_shift = log2_of(F::kStep);
@@ -1120,19 +1141,6 @@ int attend_launch(AttendParams P, const CUtensorMap &k_map, const CUtensorMap &v
     }
     kernel<<<static_cast<unsigned>(ctas), kAttendThreads, static_cast<size_t>(dyn), stream>>>(P, k_map, v_map);
     if (launched() != SSD_OK) return SSD_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), (F::R + 3) / 4);
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join_kernel<typename F::E, F::D>, P) != cudaSuccess) {
-        cudaGetLastError();
-        return SSD_ERR_CUDA;
-    }
     return SSD_OK;
 }
 
