@@ -74,6 +74,7 @@ struct AttendParams {
     int window;
     int rows_per_item;
     int step_shift;  // log2 of the keys of one step
+    int item_cost;   // what starting an item counts in the split, in steps
     int inside;  // the schedule is made by every CTA in shared memory
     void *out;
     Workspace *ws;
@@ -129,29 +130,35 @@ struct Walk {
     const int32_t *sums, *seq, *row0;
     int unit, end, pair;
     int units, ctas;
+    // A CTA's units are steps, after item_cost units for the start of each item.
     __device__ __forceinline__ bool next(const AttendParams &P, Part &part) {
-        if (unit >= end) return false;
-        while (sums[pair + 1] <= unit) ++pair;
-        const int base = sums[pair], span = sums[pair + 1] - base;
-        const int b = P.inside ? pair : seq[pair];
-        part.b = b;
-        part.row0 = P.inside ? 0 : row0[pair];
-        const Seq s = load_seq(P, b);
-        part.first = s.first;
-        part.pos0 = s.pos0;
-        part.rows = min(P.rows_per_item, s.n * P.G - part.row0);
-        const Span k = key_span(P, s, part.row0, part.row0 + part.rows);
-        part.start = k.start, part.stop = k.stop;
-        const int all = span / P.Hkv;  // == k.steps
-        part.head = (unit - base) / all;
-        const int done = (unit - base) - part.head * all;
-        part.step = k.step0 + done;
-        part.steps = min(all - done, end - unit);
-        const int64_t item = static_cast<int64_t>(base) + static_cast<int64_t>(part.head) * all;
-        part.first_cta = static_cast<int>(((item + 1) * ctas - 1) / units);
-        part.parts = static_cast<int>(((item + all) * ctas - 1) / units) - part.first_cta + 1;
-        unit += part.steps;
-        return true;
+        for (;;) {
+            if (unit >= end) return false;
+            while (sums[pair + 1] <= unit) ++pair;
+            const int base = sums[pair], all = (sums[pair + 1] - base) / P.Hkv;
+            const int head = (unit - base) / all, done = (unit - base) - head * all - P.item_cost;
+            if (done < 0) {
+                unit -= done;
+                continue;
+            }
+            const int b = P.inside ? pair : seq[pair];
+            part.b = b;
+            part.row0 = P.inside ? 0 : row0[pair];
+            const Seq s = load_seq(P, b);
+            part.first = s.first;
+            part.pos0 = s.pos0;
+            part.rows = min(P.rows_per_item, s.n * P.G - part.row0);
+            const Span k = key_span(P, s, part.row0, part.row0 + part.rows);
+            part.start = k.start, part.stop = k.stop;
+            part.head = head;
+            part.step = k.step0 + done;
+            part.steps = min(k.steps - done, end - unit);
+            const int64_t item = static_cast<int64_t>(base) + static_cast<int64_t>(head) * all;
+            part.first_cta = static_cast<int>(((item + P.item_cost + 1) * ctas - 1) / units);
+            part.parts = static_cast<int>(((item + all) * ctas - 1) / units) - part.first_cta + 1;
+            unit += part.steps;
+            return true;
+        }
     }
 };
 
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(kScheduleThreads) schedule_kernel(const __grid
             const int b = last_not_above(blocks, P.B, p);
             const int row0 = (p - blocks[b]) * P.rows_per_item;
             const Seq s = load_seq(P, b);
-            v = key_span(P, s, row0, min(row0 + P.rows_per_item, s.n * P.G)).steps * P.Hkv;
+            v = (key_span(P, s, row0, min(row0 + P.rows_per_item, s.n * P.G)).steps + P.item_cost) * P.Hkv;
             W.seq[p] = b;
             W.row0[p] = row0;
         }
@@ -244,6 +251,13 @@ __device__ __forceinline__ float2 floats_of_e4m3x2(uint32_t two) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// Two halves as e4m3, the low one in the low byte; rounding and range as e4m3x2.
+__device__ __forceinline__ uint32_t e4m3x2_of_halves(__half2 v) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&v)));
+    return r;
+}
+
 template <class E>
 constexpr int digits_of() {
     return sizeof(E) == 2 && __is_same(E, __half) ? 3 : 2;
@@ -258,6 +272,9 @@ struct Form {
     // tiles of 128 keys in one step: two, unless the weights' digits then leave too few slots for K and V
     static constexpr int kSub = R > 32 && kDigits == 3 && D == 128 ? 1 : 2;
     static constexpr int kStep = kSub * kTile;
+    // Starting an item (its queries' digits, a drained pipeline) takes 2.3 us, a step of up to 32 rows 1.4 us and
+    // one of 64 rows 3 us.
+    static constexpr int kItemCost = R > 32 ? 1 : 2;
     // O has two columns for each row.  Two digits of a weight (bf16) are the two columns of one product: an
     // MMA of few columns takes the time of its 128 rows of V (39 clocks at 16 columns, 47 at 64, 62 at 128),
     // so one of both digits costs little more than one of each.  Of three digits (fp16) the second and third
@@ -276,7 +293,7 @@ struct Form {
 
 constexpr int kAttendWarps = 16;  // softmax 2 x 4, output 4, TMA, MMA, queries, scout
 constexpr int kAttendThreads = 32 * kAttendWarps;
-constexpr int kSteps = 8;    // steps that the scout may be ahead
+constexpr int kSteps = 6;    // steps that the scout may be ahead
 constexpr int kItems = 6;    // items whose row data may be in use at once (steps s - 4 to s, when each is an item of its own)
 constexpr int kMaxSlots = 12;
 constexpr int kSharedBytes = 227 * 1024;  // of one CTA
@@ -307,9 +324,10 @@ struct Shared {
     uint64_t step_full[kSteps], step_free[kSteps];
     uint64_t s_full[2], s_free[2], p_full[2], o_full[2], o_free[2], q_full, q_free, drained;
     Step step[kSteps];
-    float q_factor[kItems][R];
-    int2 row_keys[kItems][R];  // first and last key of a row
-    float4 step_max[4][R];     // of the four warps of a softmax group, for the last steps
+    alignas(16) float q_factor[kItems][R];
+    int32_t row_last[kItems][R];  // last key of a row
+    alignas(16) float step_max[4][4][R];  // of the last steps and the four warps of a softmax group
+    alignas(16) float row_max[8][R];      // a softmax warp's copy of what they come to
     float4 step_sum[2][R];
     float2 joined[2][R];  // factors of the old and the new output
     float final[R];
@@ -340,11 +358,13 @@ __device__ __forceinline__ void drain_phase(uint64_t *bar, uint32_t parity) {
     }
 }
 
+// Whether a row whose last key is `last` attends to key j >= 0.
+__device__ __forceinline__ bool attends(const AttendParams &P, int last, int j) {
+    return j <= last && (P.window == 0 || j > last - P.window);
+}
+
 // Reduces each of kN values over the 32 lanes: kN / 32 results per lane (one where kN < 32), of the
 // values from lane * kN / 32 on.  Each round halves the values by trading halves with a partner lane.
-struct MaxOf {
-    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
 struct SumOf {
     __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
@@ -404,7 +424,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             int v = 0;
             if (b < P.B) {
                 const Seq s = load_seq(P, b);
-                if (s.n > 0) v = key_span(P, s, 0, s.n * P.G).steps * P.Hkv;
+                if (s.n > 0) v = (key_span(P, s, 0, s.n * P.G).steps + P.item_cost) * P.Hkv;
             }
             const int sum = block_sums<kAttendThreads>(v, carry, S.red);
             if (b < P.B) sums_sh[b + 1] = sum;
@@ -487,8 +507,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         // fetches took 7 of every 18 stalled cycles), and no row count needs registers of its own.
         for (int it = group;; it += 2) {
             const int phase = (it >> 1) & 1;
-            const float4 *max_of = S.step_max[it & 3];
-            float *max_sh = reinterpret_cast<float *>(S.step_max[it & 3]), *sum_sh = reinterpret_cast<float *>(S.step_sum[group]);
+            float(&max_sh)[4][R] = S.step_max[it & 3];
+            float *sum_sh = reinterpret_cast<float *>(S.step_sum[group]);
             const Step &st = open_step(it);
             const bool stop = !st.live;
             const int item = stop ? 0 : st.item, chunks = (st.rows + 7) >> 3;
@@ -504,11 +524,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 there[u] = (st.there >> page) & 1;
             }
             const int key0 = st.key0 + key;
-            // scores of eight rows, without the rows' own factors
-            auto scores = [&](int r0, float(&s)[kSub][8]) {
+            auto fetch = [&](int r0, float(&s)[kSub][8]) {
 #pragma unroll
                 for (int u = 0; u < kSub; ++u) tc::tmem_load<8>(s[u], s_at + u * N + r0);
-                tc::tmem_wait_load(s);
+            };
+            // Scores of eight rows, without the rows' own factors; `next` holds what was fetched of them and then
+            // gets the following rows under way.
+            auto scores = [&](int r0, float(&next)[kSub][8], float(&s)[kSub][8]) {
+                tc::tmem_wait_load(next);
+#pragma unroll
+                for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[u][i] = next[u][i];
+                if (r0 + 8 < chunks * 8) fetch(r0 + 8, next);
 #pragma unroll
                 for (int u = 0; u < kSub; ++u)
 #pragma unroll
@@ -518,9 +546,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     for (int u = 0; u < kSub; ++u)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const int2 keys = S.row_keys[item][r0 + i];
-                            const int j = key0 + u * kTile;
-                            s[u][i] = there[u] && j >= keys.x && j <= keys.y ? s[u][i] : -INFINITY;
+                            s[u][i] = there[u] && attends(P, S.row_last[item][r0 + i], key0 + u * kTile) ? s[u][i] : -INFINITY;
                         }
                 }
             };
@@ -528,17 +554,24 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 wait(&S.s_full[group], phase);
                 tc::fence_after();
                 // largest score of each row: over the thread's keys, the warp's lanes, the group's warps
+                float next[kSub][8];
+                fetch(0, next);
 #pragma unroll 1
                 for (int c = 0; c < chunks; ++c) {
                     float s[kSub][8];
-                    scores(c * 8, s);
+                    scores(c * 8, next, s);
                     if (kSub == 2) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) s[0][i] = fmaxf(s[0][i], s[kSub - 1][i]);
                     }
-                    reduce_lanes(s[0], lane, MaxOf());
-                    const int r = c * 8 + lane / 4;
-                    if (lane % 4 == 0) max_sh[r * 4 + quad] = s[0][0] * q_factor[r];
+                    // (2.3 clocks a reduction; the shuffles that trade halves take 8 a row)
+                    float mine = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float m = tc::warp_max(s[0][i]);
+                        mine = lane == i ? m : mine;
+                    }
+                    if (lane < 8) max_sh[quad][c * 8 + lane] = mine * q_factor[c * 8 + lane];
                 }
             }
             if (tc::barrier_or(1 + group, 128, stop || gave_up())) break;
@@ -546,17 +579,32 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (it >= 2) wait(&S.o_free[group], phase ^ 1);
 
             // weights 2^(score - largest), their sums over the keys, and the digits of weight x value scale (<= 256)
+            // each lane joins the four warps' maxima of one row in 32; without a key the largest is -inf, and
+            // 2^(-inf + 1e30) is 0 all the same
+            float *row_max = S.row_max[warp];
+#pragma unroll
+            for (int i = 0; i < R / 32; ++i) {
+                const int r = i * 32 + lane;
+                row_max[r] = fmaxf(fmaxf(fmaxf(max_sh[0][r], max_sh[1][r]), fmaxf(max_sh[2][r], max_sh[3][r])), -1e30f);
+            }
+            __syncwarp();
+            float next[kSub][8];
+            fetch(0, next);
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const int r0 = c * 8;
-                float s[kSub][8], sums[8];
-                scores(r0, s);
+                float s[kSub][8], sums[8], qfs[8], ms[8];
+                scores(r0, next, s);
+#pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                    const float4 q4 = *reinterpret_cast<const float4 *>(q_factor + r0 + i);
+                    qfs[i] = q4.x, qfs[i + 1] = q4.y, qfs[i + 2] = q4.z, qfs[i + 3] = q4.w;
+                    const float4 m4 = *reinterpret_cast<const float4 *>(row_max + r0 + i);
+                    ms[i] = m4.x, ms[i + 1] = m4.y, ms[i + 2] = m4.z, ms[i + 3] = m4.w;
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float4 m4 = max_of[r0 + i];
-                    // without a key the largest is -inf: 2^(-inf + 1e30) is 0 all the same
-                    const float m = fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), -1e30f);
-                    const float qf = q_factor[r0 + i];
+                    const float m = ms[i], qf = qfs[i];
                     sums[i] = 0.f;
 #pragma unroll
                     for (int u = 0; u < kSub; ++u) {
@@ -568,40 +616,53 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 if (lane % 4 == 0) sum_sh[(r0 + lane / 4) * 4 + quad] = sums[0];
 #pragma unroll
                 for (int u = 0; u < kSub; ++u) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s[u][i] *= f[u];
                     if (odd && !plain) {  // 0 times a scale that is not finite
 #pragma unroll 1
                         for (int i = 0; i < 8; ++i) {
-                            const int2 keys = S.row_keys[item][r0 + i];
-                            const int j = key0 + u * kTile;
-                            if (there[u] && j >= keys.x && j <= keys.y) continue;
+                            if (there[u] && attends(P, S.row_last[item][r0 + i], key0 + u * kTile)) continue;
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 if (e == i) s[u][e] = 0.f;
                         }
                     }
+                    uint32_t words[kDigits][2];
+                    if (F::kBoth) {
+                        // Two digits hold 2^-8 of a weight, so halves (2^-11) do between: the product with the value
+                        // scale, and what is left after the first digit, which is exact.
+                        const __half2 f2 = __float2half2_rn(f[u]);
 #pragma unroll
-                    for (int g = 0; g < kDigits; ++g) {
-                        uint32_t words[2];
+                        for (int h = 0; h < 4; ++h) {
+                            const __half2 w = __hmul2(__floats2half2_rn(s[u][2 * h], s[u][2 * h + 1]), f2);
+                            const uint32_t a = e4m3x2_of_halves(w);
+                            const uint32_t back = halves_of_e4m3x2(a);
+                            const uint32_t b = e4m3x2_of_halves(__hsub2(w, *reinterpret_cast<const __half2 *>(&back)));
+                            words[0][h / 2] = h % 2 == 0 ? a : words[0][h / 2] | (a << 16);
+                            words[1][h / 2] = h % 2 == 0 ? b : words[1][h / 2] | (b << 16);
+                        }
+                    } else {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float *w = &s[u][4 * h];
-                            const uint32_t a = e4m3x2(w[0], w[1]), b = e4m3x2(w[2], w[3]);
-                            words[h] = a | (b << 16);
-                            if (g + 1 < kDigits) {
-                                const float2 fa = floats_of_e4m3x2(a), fb = floats_of_e4m3x2(b);
-                                w[0] -= fa.x, w[1] -= fa.y, w[2] -= fb.x, w[3] -= fb.y;
-                                if (F::kFine != 1.f && g == 0) {
+                        for (int i = 0; i < 8; ++i) s[u][i] *= f[u];
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) w[e] *= F::kFine;
+                        for (int g = 0; g < kDigits; ++g)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float *w = &s[u][4 * h];
+                                const uint32_t a = e4m3x2(w[0], w[1]), b = e4m3x2(w[2], w[3]);
+                                words[g][h] = a | (b << 16);
+                                if (g + 1 < kDigits) {
+                                    const float2 fa = floats_of_e4m3x2(a), fb = floats_of_e4m3x2(b);
+                                    const float up = g == 0 ? F::kFine : 1.f;
+                                    w[0] = (w[0] - fa.x) * up, w[1] = (w[1] - fa.y) * up;
+                                    w[2] = (w[2] - fb.x) * up, w[3] = (w[3] - fb.y) * up;
                                 }
                             }
-                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < kDigits; ++g) {
                         const int at = F::kBoth ? g * chunks + c : c;  // in units of 8 bytes of the key's row
                         *reinterpret_cast<uint2 *>(p_at + (F::kBoth ? 0 : g * F::kP) +
                                                    tc::swizzled<kPitch>(u * kTile + key, at >> 1) + (at & 1) * 8) =
-                            make_uint2(words[0], words[1]);
+                            make_uint2(words[g][0], words[g][1]);
                     }
                 }
             }
@@ -662,8 +723,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const bool stop = !st.live;
             if (!stop) wait(&S.p_full[buf], phase);
             if (!stop && ch < st.rows) {
-                const float4 m4 = S.step_max[it & 3][ch], l4 = S.step_sum[buf][ch];
-                const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+                const float(&ms)[4][R] = S.step_max[it & 3];
+                const float4 l4 = S.step_sum[buf][ch];
+                const float m = fmaxf(fmaxf(ms[0][ch], ms[1][ch]), fmaxf(ms[2][ch], ms[3][ch]));
                 const float m_new = fmaxf(m_run, m);
                 const float ref = m_new == -INFINITY ? 0.f : m_new;
                 const float old = ex2(m_run - ref), now = ex2(m - ref);
@@ -706,8 +768,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         if ((P.v[row * D + ch] & 0x7F) != 0x7F) continue;
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
-                            const int2 keys = S.row_keys[st.item][r];
-                            if (j >= keys.x && j <= keys.y) acc[r] = __int_as_float(0x7FC00000);
+                            if (attends(P, S.row_last[st.item][r], j)) acc[r] = __int_as_float(0x7FC00000);
                         }
                     }
                 }
@@ -994,8 +1055,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         float f = size * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
                         if (odd) f = __int_as_float(0x7FC00000);
                         S.q_factor[items % kItems][r] = there ? f : 0.f;
-                        S.row_keys[items % kItems][r] =
-                            there ? make_int2(P.window > 0 ? pos + 1 - P.window : 0, pos) : make_int2(0, -1);
+                        S.row_last[items % kItems][r] = there ? pos : -1;
                     }
                 }
                 tc::fence_async_shared();
@@ -1131,6 +1191,7 @@ int attend_launch(AttendParams P, const CUtensorMap &k_map, const CUtensorMap &v
     }
     P.rows_per_item = F::R;
     P.step_shift = log2_of(F::kStep);
+    P.item_cost = F::kItemCost;
     P.inside = static_cast<int64_t>(P.max_new) * P.G <= F::R && P.B <= kSeqsInside;
     int ctas = dev.sms;
     if (ctas > kMaxCtas) ctas = kMaxCtas;

@@ -116,6 +116,17 @@ __device__ __forceinline__ bool barrier_or(int id, int threads, bool mine) {
     return any != 0;
 }
 
+// Registers of this warpgroup's threads from here on.  The shares of all of a CTA's warps together stay within
+// what it was launched with.
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // True for one lane of a converged warp, in a form that keeps what follows warp-uniform.
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
