@@ -2,8 +2,15 @@
 // (sm_103a).
 //
 // What is kept is a prefix of the ranking (logit desc, id asc), so it is described by its
-// last value and, among tokens of that value, its last id.  Each limit is found bit by
-// bit on the ordered bits of the logit with counts (top-k) or sums of weights (top-p).
+// last value and, among tokens of that value, its last id.
+//
+// A cluster of CTAs takes a row: each holds one slice in shared memory, read from HBM once,
+// and every pass after that runs on chip.  A limit (k tokens, or a share of the weight) is
+// found on the distance d = max - z, whose float bits order the tokens: a histogram over 512
+// ranges of those bits, of counts or of exact weights, names the range that the limit falls
+// into, and the next one divides that range, until it holds at most 256 tokens, which are
+// ranked against one another, or tokens of one value, which rank by id.  Every CTA adds up
+// the cluster's histograms itself, so that one cluster barrier does for each.
 //
 // Weights.  w = exp((z - m) / tau) = 2^t, t = d * c with d = z - m and c = log2(e) / tau
 // both carried as two floats, so that t is exact to about 2^-45 of itself.  t is split
@@ -13,9 +20,10 @@
 // on no order, a prefix and a total agree to the last bit, and the rank or id at which a
 // sum passes its limit is decided as the real numbers would, but for cases closer than
 // 2^-28 of a weight.
-//
-// One CTA per row; every pass reads the row again (L2 holds it).
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "ssd_kv.h"
 #include "ssd_device.cuh"
@@ -23,8 +31,16 @@
 namespace ssd {
 namespace {
 
-constexpr int kSampleThreads = 1024;
+namespace cg = cooperative_groups;
+
+constexpr int kSampleThreads = 512;
 constexpr int kSampleWarps = kSampleThreads / 32;
+constexpr int kBins = kSampleThreads;  // a thread adds up one bin
+constexpr int kList = 256;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+// The first histogram: 32 ranges for each power of two of d from 2^-6 on, what is nearer and
+// what is farther in one range each.
+constexpr uint32_t kNear = 0x3C800000u, kFirstShift = 18, kInfinite = 0x7F800000u;
 
 struct SampleParams {
     const void *logits;
@@ -37,6 +53,8 @@ struct SampleParams {
     float *prob;
     void *filtered;
     int32_t *dev_status;
+    int slice;    // 16-byte vectors of a CTA
+    int aligned;  // rows start on 16-byte boundaries
 };
 
 // 2^t in fixed point, t = (z - m) * (c_hi + c_lo) <= 0.  All lanes call; `table` is this
@@ -68,28 +86,6 @@ struct Weigher {
     }
 };
 
-template <class T>
-__device__ __forceinline__ T sample_sum(T v, T *red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    T r = 0;
-    for (int w = 0; w < kSampleWarps; ++w) r += red[w];
-    return r;
-}
-
-template <class D>
-__device__ __forceinline__ void store_logit(void *p, int64_t i, float v);
-template <>
-__device__ __forceinline__ void store_logit<F32Tag>(void *p, int64_t i, float v) {
-    static_cast<float *>(p)[i] = v;
-}
-template <>
-__device__ __forceinline__ void store_logit<BF16Tag>(void *p, int64_t i, float v) {
-    static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16(v);
-}
 
 // What is kept: ordered value above `key`, or equal to it and id <= `id`; and value >= `least`.
 struct Kept {
@@ -102,36 +98,488 @@ struct Kept {
     }
 };
 
+struct Histogram {
+    uint32_t count[kBins], low[kBins], high[kBins];  // weights: 64 bits in two words
+};
+
+struct Shared {
+    Histogram hist[2];
+    uint64_t list[kList];    // this CTA's tokens of the range
+    uint64_t ranked[kList];  // the cluster's
+    uint64_t ranked_weight[kList];
+    uint64_t sums[2][2];     // published to the cluster, in turn
+    uint64_t best;
+    int odd;
+    int listed;
+    int result;
+    uint64_t warp_sum[kSampleWarps];
+    uint64_t red[kSampleWarps];
+    uint32_t red32[kSampleWarps];
+    uint64_t found_above, found_total;
+    uint32_t found_bin, found_in, found_rank;
+    uint64_t full;
+};
+
+template <class D>
+__device__ __forceinline__ void store_logit(void *p, int64_t i, float v);
+template <>
+__device__ __forceinline__ void store_logit<F32Tag>(void *p, int64_t i, float v) {
+    static_cast<float *>(p)[i] = v;
+}
+template <>
+__device__ __forceinline__ void store_logit<BF16Tag>(void *p, int64_t i, float v) {
+    static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16(v);
+}
+
+template <class D>
+struct Row {
+    static constexpr int kVec = D::kVec;
+    const SampleParams &P;
+    Shared &S;
+    const uint4 *slice;
+    cg::cluster_group cluster;
+    int ctas, rank, first_id;  // id of the slice's first token
+    int vectors;               // of the slice
+    int turn = 0;              // which of the two published words / histograms is next
+    float m;
+    Weigher weigh;
+
+    __device__ __forceinline__ Row(const SampleParams &p, Shared &s, const uint4 *sl)
+        : P(p), S(s), slice(sl), cluster(cg::this_cluster()) {
+        ctas = static_cast<int>(cluster.num_blocks());
+        rank = static_cast<int>(cluster.block_rank());
+        first_id = rank * P.slice * kVec;
+        const int left = P.V - first_id;
+        vectors = left <= 0 ? 0 : min(P.slice, (left + kVec - 1) / kVec);
+    }
+    // fn(z, id, there) for every token of the slice, whole warps at a time
+    template <class Fn>
+    __device__ __forceinline__ void each(Fn &&fn) {
+        for (int v0 = 0; v0 < vectors; v0 += kSampleThreads) {
+            const int v = v0 + static_cast<int>(threadIdx.x);
+            float z[kVec];
+            const bool in = v < vectors;
+            decode_vec<D>(slice[in ? v : 0], z);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const int id = first_id + v * kVec + e;
+                fn(z[e], id, in && id < P.V);
+            }
+        }
+    }
+    __device__ __forceinline__ uint32_t distance(float z) const { return __float_as_uint(m - z); }
+
+    // Sums of two words over the cluster; every thread gets them.
+    __device__ __forceinline__ void cluster_sum(uint64_t &a, uint64_t &b) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(kAll, a, o);
+            b += __shfl_xor_sync(kAll, b, o);
+        }
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) S.red[threadIdx.x >> 5] = a, S.warp_sum[threadIdx.x >> 5] = b;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            uint64_t x = 0, y = 0;
+            for (int w = 0; w < kSampleWarps; ++w) x += S.red[w], y += S.warp_sum[w];
+            S.sums[turn][0] = x, S.sums[turn][1] = y;
+        }
+        cluster.sync();
+        a = b = 0;
+        for (int c = 0; c < ctas; ++c) {
+            const uint64_t *s = cluster.map_shared_rank(&S.sums[turn][0], c);
+            a += s[0], b += s[1];
+        }
+        turn ^= 1;
+    }
+
+    // The first id, in ascending order, at which the sum of weight(z, id) passes `target`; `mine` is the sum over
+    // this warp's stretch of the slice (warps take consecutive stretches).  -1 in CTAs that do not hold it.
+    __device__ __forceinline__ int warp_stretch() const { return (vectors + kSampleWarps - 1) / kSampleWarps; }
+    template <class Weight>
+    __device__ __forceinline__ uint64_t stretch_sum(Weight &&weight) {
+        const int n = warp_stretch(), from = static_cast<int>(threadIdx.x >> 5) * n, to = min(from + n, vectors);
+        uint64_t s = 0;
+        for (int v0 = from; v0 < to; v0 += 32) {
+            const int v = v0 + static_cast<int>(threadIdx.x & 31);
+            float z[kVec];
+            decode_vec<D>(slice[v < to ? v : 0], z);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const int id = first_id + v * kVec + e;
+                s += weight(z[e], id, v < to && id < P.V);
+            }
+        }
+        return s;
+    }
+    // Publishes the stretches' sums; returns the cluster's total, and what lies before this CTA in `before`.
+    __device__ __forceinline__ uint64_t publish(uint64_t s, uint64_t &before) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) S.warp_sum[threadIdx.x >> 5] = s;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            uint64_t x = 0;
+            for (int w = 0; w < kSampleWarps; ++w) x += S.warp_sum[w];
+            S.sums[turn][0] = x;
+        }
+        cluster.sync();
+        uint64_t total = 0;
+        before = 0;
+        for (int c = 0; c < ctas; ++c) {
+            const uint64_t x = cluster.map_shared_rank(&S.sums[turn][0], c)[0];
+            if (c < rank) before += x;
+            total += x;
+        }
+        turn ^= 1;
+        return total;
+    }
+    template <class Weight>
+    __device__ __forceinline__ int locate(Weight &&weight, uint64_t before, uint64_t target) {
+        int w = 0;
+        uint64_t run = before;
+        for (; w < kSampleWarps; ++w) {
+            const uint64_t s = S.warp_sum[w];
+            if (run <= target && run + s > target) break;
+            run += s;
+        }
+        if (w == kSampleWarps || static_cast<int>(threadIdx.x >> 5) != w) return -1;
+        const int lane = static_cast<int>(threadIdx.x & 31);
+        const int n = warp_stretch(), from = w * n, to = min(from + n, vectors);
+        for (int v0 = from; v0 < to; v0 += 32) {
+            const int v = v0 + lane;
+            float z[kVec];
+            uint64_t each_w[kVec], s = 0;
+            decode_vec<D>(slice[v < to ? v : 0], z);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const int id = first_id + v * kVec + e;
+                each_w[e] = weight(z[e], id, v < to && id < P.V);
+                s += each_w[e];
+            }
+            uint64_t upto = s;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t x = __shfl_up_sync(kAll, upto, o);
+                if (lane >= o) upto += x;
+            }
+            const uint32_t over = __ballot_sync(kAll, run + upto > target);
+            if (over) {
+                const int l = __ffs(over) - 1;
+                int id = -1;
+                uint64_t x = run + upto - s;
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    x += each_w[e];
+                    if (id < 0 && x > target) id = first_id + v * kVec + e;
+                }
+                return __shfl_sync(kAll, id, l);
+            }
+            run += __shfl_sync(kAll, upto, 31);
+        }
+        return -1;
+    }
+
+    // The weight of a token that is in; all lanes of a warp call, and skip it together where none is.
+    __device__ __forceinline__ uint64_t weight_if(float z, bool in) {
+        in = in && z > -INFINITY;
+        if (!__any_sync(kAll, in)) return 0;
+        const uint64_t x = weigh(in ? z : m);
+        return in ? x : 0;
+    }
+
+    // Narrows `kept` to the ranks that a limit leaves.  kMass: while the weight above a rank is below `share` of
+    // what is kept; else the first `k` ranks.
+    template <bool kMass>
+    __device__ void limit_to(Kept &kept, int k, float share) {
+        uint32_t lo = 0, hi = kInfinite + 1, shift = 0;  // bits of d: the range looked at, from the second level on
+        bool first = true;
+        uint64_t above = 0, in_range = 0;  // tokens or weight above the range; tokens in it
+        double goal = 0.0;
+        // a level divides its range by 512: three and the first end at single distances
+        for (int level = 0; level < 8; ++level) {
+            Histogram &H = S.hist[level & 1];
+            const int t = static_cast<int>(threadIdx.x);
+            H.count[t] = 0;
+            if (kMass) H.low[t] = H.high[t] = 0;
+            __syncthreads();
+            each([&](float z, int id, bool there) {
+                const uint32_t d = distance(z);
+                bool in = there && d >= lo && d < hi && (!kMass || kept(z, id));
+                const int bin = first ? min(max((static_cast<int>(d - kNear) >> kFirstShift) + 1, 0), kBins - 1)
+                                      : static_cast<int>((d - lo) >> shift);
+                if (!__any_sync(kAll, in)) return;
+                // a warp of one value (constant rows) adds once
+                const uint32_t d0 = __shfl_sync(kAll, d, 0);
+                const bool same = __all_sync(kAll, in && d == d0);
+                const bool adds = same ? (t & 31) == 0 : in;
+                const uint32_t times = same ? 32 : 1;
+                if (kMass) {
+                    const uint64_t w = weight_if(z, in) * times;
+                    if (adds && w) {
+                        const uint32_t part = static_cast<uint32_t>(w);
+                        const uint32_t was = atomicAdd(&H.low[bin], part);
+                        const uint32_t carry = was + part < was ? 1u : 0u;
+                        const uint32_t rest = static_cast<uint32_t>(w >> 32) + carry;
+                        if (rest) atomicAdd(&H.high[bin], rest);
+                    }
+                }
+                if (adds) atomicAdd(&H.count[bin], times);
+            });
+            cluster.sync();
+            // every CTA adds up all histograms: thread t bin t
+            uint32_t count = 0;
+            uint64_t mass = 0;
+            for (int c = 0; c < ctas; ++c) {
+                const Histogram *h = cluster.map_shared_rank(&H, c);
+                count += h->count[t];
+                if (kMass) mass += (static_cast<uint64_t>(h->high[t]) << 32) + h->low[t];
+            }
+            const uint64_t mine = kMass ? mass : count;
+            uint64_t upto = mine;
+            const int lane = t & 31;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t x = __shfl_up_sync(kAll, upto, o);
+                if (lane >= o) upto += x;
+            }
+            if (lane == 31) S.red[t >> 5] = upto;
+            __syncthreads();
+            uint64_t before = 0, total = 0;
+            for (int w = 0; w < kSampleWarps; ++w) {
+                const uint64_t x = S.red[w];
+                if (w < (t >> 5)) before += x;
+                total += x;
+            }
+            upto += before;
+            if (first) goal = kMass ? static_cast<double>(share) * static_cast<double>(total) : static_cast<double>(k);
+            const double start = static_cast<double>(above + upto - mine), end = static_cast<double>(above + upto);
+            if (mine && start < goal && end >= goal) {
+                S.found_bin = static_cast<uint32_t>(t);
+                S.found_above = above + upto - mine;
+                S.found_in = count;
+            }
+            __syncthreads();
+            const uint32_t bin = S.found_bin;
+            above = S.found_above;
+            in_range = S.found_in;
+            if (first) {
+                lo = bin == 0 ? 0 : kNear + ((bin - 1) << kFirstShift);
+                hi = bin == 0 ? kNear : (bin == kBins - 1 ? kInfinite + 1 : kNear + (bin << kFirstShift));
+                first = false;
+            } else {
+                lo += bin << shift;
+                hi = min(hi, lo + (1u << shift));
+            }
+            if (in_range <= kList || hi - lo == 1) break;
+            shift = 0;
+            while (((hi - lo - 1) >> shift) >= kBins) ++shift;
+            __syncthreads();
+        }
+        if (in_range <= kList) {
+            rank_range<kMass>(kept, lo, hi, above, goal);
+            return;
+        }
+        // Many tokens at one distance: of one value as a rule (a bf16 row has few), which rank by id.  Distances are
+        // rounded, so values far below the largest may share one: then the last value kept is found bit by bit.
+        uint32_t low_key = 0xFFFFFFFFu, high_key = 0;
+        each([&](float z, int id, bool there) {
+            const uint32_t d = distance(z);
+            if (there && d >= lo && d < hi && (!kMass || kept(z, id))) {
+                const uint32_t o = ordered_bits(z);
+                low_key = min(low_key, o), high_key = max(high_key, o);
+            }
+        });
+        // the cluster's extremes, by sums of one word each: published as the block's own first
+        low_key = __reduce_min_sync(kAll, low_key), high_key = __reduce_max_sync(kAll, high_key);
+        const int t = static_cast<int>(threadIdx.x);
+        __syncthreads();
+        if ((t & 31) == 0) S.red[t >> 5] = (static_cast<uint64_t>(low_key) << 32) | high_key;
+        __syncthreads();
+        if (t == 0) {
+            for (int w = 0; w < kSampleWarps; ++w) {
+                low_key = min(low_key, static_cast<uint32_t>(S.red[w] >> 32));
+                high_key = max(high_key, static_cast<uint32_t>(S.red[w]));
+            }
+            S.sums[turn][0] = low_key, S.sums[turn][1] = high_key;
+        }
+        cluster.sync();
+        for (int c = 0; c < ctas; ++c) {
+            const uint64_t *s = cluster.map_shared_rank(&S.sums[turn][0], c);
+            low_key = min(low_key, static_cast<uint32_t>(s[0])), high_key = max(high_key, static_cast<uint32_t>(s[1]));
+        }
+        turn ^= 1;
+        uint32_t key = low_key;
+        if (low_key != high_key) {
+            key = 0;
+            auto upto = [&](uint32_t from) {  // tokens or weight of the range from that key on
+                uint64_t s = 0, none = 0;
+                each([&](float z, int id, bool there) {
+                    const uint32_t d = distance(z);
+                    const bool in = there && d >= lo && d < hi && ordered_bits(z) >= from && (!kMass || kept(z, id));
+                    s += kMass ? weight_if(z, in) : static_cast<uint64_t>(in);
+                });
+                cluster_sum(s, none);
+                return s;
+            };
+            for (int bit = 31; bit >= 0; --bit) {
+                const uint32_t c = key | (1u << bit);
+                if (c <= high_key && static_cast<double>(above + upto(c)) >= goal) key = c;
+            }
+            if (key < 0xFFFFFFFFu) above += upto(key + 1);
+        }
+        uint64_t ties;
+        if (kMass) {
+            const uint64_t one = weigh(value_of_ordered(key));
+            const double n = one ? ceil((goal - static_cast<double>(above)) / static_cast<double>(one)) : 1.0;
+            ties = n < 1.0 ? 1 : (n > static_cast<double>(P.V) ? static_cast<uint64_t>(P.V) : static_cast<uint64_t>(n));
+        } else {
+            ties = static_cast<uint64_t>(k) - above;
+        }
+        auto tie = [&](float z, int id, bool there) {
+            return static_cast<uint64_t>(there && ordered_bits(z) == key && (!kMass || kept(z, id)));
+        };
+        uint64_t before;
+        publish(stretch_sum(tie), before);
+        const int id = locate(tie, before, ties - 1);
+        if (id >= 0 && (t & 31) == 0)
+            for (int c = 0; c < ctas; ++c) *cluster.map_shared_rank(&S.result, c) = id;
+        cluster.sync();
+        kept.key = key;
+        kept.id = S.result;
+    }
+
+    // The few tokens with lo <= d < hi against one another.
+    template <bool kMass>
+    __device__ __forceinline__ void rank_range(Kept &kept, uint32_t lo, uint32_t hi, uint64_t above, double goal) {
+        const int t = static_cast<int>(threadIdx.x);
+        if (t == 0) S.listed = 0;
+        __syncthreads();
+        each([&](float z, int id, bool there) {
+            const uint32_t d = distance(z);
+            if (there && d >= lo && d < hi && (!kMass || kept(z, id))) {
+                const int at = atomicAdd(&S.listed, 1);
+                if (at < kList) S.list[at] = make_key(z, id);
+            }
+        });
+        cluster.sync();
+        int n = 0;
+        for (int c = 0; c < ctas; ++c) {
+            const int here = min(*cluster.map_shared_rank(&S.listed, c), kList - n);
+            const uint64_t *list = cluster.map_shared_rank(&S.list[0], c);
+            for (int i = t; i < here; i += kSampleThreads) S.ranked[n + i] = list[i];
+            n += here;
+        }
+        __syncthreads();
+        const uint64_t own = t < n ? S.ranked[t] : 0;
+        if (kMass && t < kList) {
+            const uint64_t w = weight_if(key_value(own), t < n);
+            S.ranked_weight[t] = w;
+        }
+        __syncthreads();
+        bool in = false;
+        int place = 0;
+        if (t < n) {
+            uint64_t higher = above;
+            for (int i = 0; i < n; ++i)
+                if (S.ranked[i] > own) {
+                    ++place;
+                    if (kMass) higher += S.ranked_weight[i];
+                }
+            if (!kMass) higher += static_cast<uint64_t>(place);
+            in = static_cast<double>(higher) < goal;
+        }
+        const int left = __syncthreads_count(in);
+        if (in && place == left - 1) S.found_above = own;
+        __syncthreads();
+        const uint64_t last = S.found_above;
+        kept.key = static_cast<uint32_t>(last >> 32);
+        kept.id = key_id(last);
+        // the next limit's histogram may use what others still read: they are past it after its own barrier
+    }
+};
+
 template <class D>
 __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_constant__ SampleParams P) {
-    __shared__ uint64_t red[kSampleWarps];
-    __shared__ uint64_t scan[kSampleThreads];
-    __shared__ int red_i[kSampleWarps];
-    __shared__ uint64_t hit_before;
-    __shared__ int hit_thread;
-    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-    const int V = P.V;
+    extern __shared__ __align__(16) uint8_t raw[];
+    Shared &S = *reinterpret_cast<Shared *>(raw);
+    uint4 *slice = reinterpret_cast<uint4 *>(raw + (sizeof(Shared) + 15) / 16 * 16);
+    constexpr int kVec = D::kVec;
+    Row<D> R(P, S, slice);
+    const int row = static_cast<int>(blockIdx.x) / R.ctas, tid = threadIdx.x, lane = tid & 31;
     const int64_t at = static_cast<int64_t>(row) * P.ld;
-    // V rounded up so that whole warps call the weigher
-    const int V32 = (V + 31) & ~31;
 
-    // largest logit (lowest id), and the row's validity
+    // ---- the slice, its largest logit (lowest id) and its validity --------------------------
     uint64_t best = 0;
     int odd = 0;
-    for (int i = tid; i < V; i += kSampleThreads) {
-        const float z = load_logit<D>(P.logits, at + i);
-        odd |= !(z < INFINITY);
-        const uint64_t k = make_key(z, i);
-        best = k > best ? k : best;
+    const char *src = static_cast<const char *>(P.logits) + (at + R.first_id) * D::kBytes;
+    auto look = [&](int v, const uint4 &w) {
+        float z[kVec];
+        decode_vec<D>(w, z);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const int id = R.first_id + v * kVec + e;
+            if (id < P.V) {
+                odd |= !(z[e] < INFINITY);
+                const uint64_t k = make_key(z[e], id);
+                best = k > best ? k : best;
+            }
+        }
+    };
+    const int whole = P.aligned ? max(0, min(R.vectors, (P.V - R.first_id) / kVec)) : 0;
+    constexpr int kFlight = 4;
+    for (int v0 = tid; v0 < whole; v0 += kSampleThreads * kFlight) {
+        uint4 w[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const int v = v0 + i * kSampleThreads;
+            if (v < whole) w[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + v);
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const int v = v0 + i * kSampleThreads;
+            if (v < whole) {
+                slice[v] = w[i];
+                look(v, w[i]);
+            }
+        }
+    }
+    for (int v = whole + tid; v < R.vectors; v += kSampleThreads) {
+        float z[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const int id = R.first_id + v * kVec + e;
+            z[e] = id < P.V ? load_logit<D>(P.logits, at + id) : -INFINITY;
+        }
+        uint4 w;
+        uint32_t *words = &w.x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            words[e] = kVec == 4 ? __float_as_uint(z[e])
+                                 : (__float_as_uint(z[2 * e % kVec]) >> 16) | (__float_as_uint(z[(2 * e + 1) % kVec]) & 0xFFFF0000u);
+        slice[v] = w;
+        look(v, w);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t t = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+        const uint64_t t = __shfl_xor_sync(kAll, best, o);
         best = t > best ? t : best;
     }
-    if (lane == 0) red[tid >> 5] = best;
+    if (lane == 0) S.red[tid >> 5] = best;
     odd = __syncthreads_or(odd);
-    for (int w = 0; w < kSampleWarps; ++w) best = red[w] > best ? red[w] : best;
+    if (tid == 0) {
+        for (int w = 0; w < kSampleWarps; ++w) best = S.red[w] > best ? S.red[w] : best;
+        S.best = best;
+        S.odd = odd;
+    }
+    R.cluster.sync();
+    best = 0;
+    for (int c = 0; c < R.ctas; ++c) {
+        const uint64_t b = *R.cluster.map_shared_rank(&S.best, c);
+        best = b > best ? b : best;
+        odd |= *R.cluster.map_shared_rank(&S.odd, c);
+    }
     const float m = key_value(best);
     const float tau = P.tau[row], u = P.u[row];
     const int top_k = P.top_k ? P.top_k[row] : 0;
@@ -141,149 +589,135 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
     if (odd || !(m > -INFINITY)) bad |= SSD_DEV_NONFINITE;
     if (!(tau >= 0.f) || !(tau < INFINITY)) bad |= SSD_DEV_BAD_TEMPERATURE;
     if (top_p != top_p || min_p != min_p || !(u >= 0.f && u < 1.f)) bad |= SSD_DEV_BAD_PARAM;
+
+    const Kept only{static_cast<uint32_t>(best >> 32), key_id(best), -INFINITY};
+    Kept kept{0u, P.V, -INFINITY};
     if (bad) {
-        if (tid == 0) {
+        if (R.rank == 0 && tid == 0) {
             report(P.dev_status, bad);
             P.tokens[row] = -1;
             if (P.prob) P.prob[row] = __int_as_float(0x7FC00000);
         }
-        if (P.filtered)
-            for (int i = tid; i < V; i += kSampleThreads)
-                store_logit<D>(P.filtered, at + i, load_logit<D>(P.logits, at + i));
-        return;
-    }
-
-    Kept kept{0u, V, -INFINITY};
-    int token = key_id(best);
-    float prob = 1.f;
-    if (tau == 0.f) {
-        kept = Kept{static_cast<uint32_t>(best >> 32), token, -INFINITY};
+    } else if (tau == 0.f) {
+        kept = only;
+        if (R.rank == 0 && tid == 0) {
+            P.tokens[row] = only.id;
+            if (P.prob) P.prob[row] = 1.f;
+        }
     } else {
+        R.m = m;
         const double c = fmin(1.4426950408889634074 / static_cast<double>(tau), 1e30);
-        Weigher w;
-        w.m = m;
-        w.c_hi = static_cast<float>(c);
-        w.c_lo = static_cast<float>(c - static_cast<double>(w.c_hi));
-        w.table = static_cast<uint32_t>(rint(exp2(static_cast<double>(lane) / 32.0) * 134217728.0));
-
-        auto count = [&](auto &&pred) {
-            int n = 0;
-            for (int i = tid; i < V; i += kSampleThreads) n += pred(load_logit<D>(P.logits, at + i), i) ? 1 : 0;
-            return sample_sum(n, red_i);
-        };
-        auto mass = [&](auto &&pred) {
-            uint64_t s = 0;
-            for (int i = tid; i < V32; i += kSampleThreads) {
-                const float z = i < V ? load_logit<D>(P.logits, at + i) : -INFINITY;
-                const bool in = i < V && z > -INFINITY && pred(z, i);
-                const uint64_t x = w(in ? z : m);
-                s += in ? x : 0;
-            }
-            return sample_sum(s, red);
-        };
-        if (top_k > 0 && top_k < V) {
-            // the value of rank top_k: the largest that at least top_k tokens reach
-            uint32_t key = 0;
-            for (int bit = 31; bit >= 0; --bit) {
-                const uint32_t c2 = key | (1u << bit);
-                if (count([&](float z, int) { return ordered_bits(z) >= c2; }) >= top_k) key = c2;
-            }
-            const int above = count([&](float z, int) { return ordered_bits(z) > key; });
-            // among tokens of that value, the lowest ids
-            int id = 0;
-            for (int bit = 30; bit >= 0; --bit) {
-                const int c2 = id + (1 << bit);
-                if (c2 < V &&
-                    count([&](float z, int i) { return ordered_bits(z) == key && i < c2; }) < top_k - above)
-                    id = c2;
-            }
-            kept.key = key, kept.id = id;
-        }
-        if (top_p < 1.f) {
-            const uint64_t total = mass(kept);
-            const double limit = static_cast<double>(top_p) * static_cast<double>(total);
-            // the last value kept: the largest v such that the values >= v hold the limit
-            uint32_t key = 0;
-            for (int bit = 31; bit >= 0; --bit) {
-                const uint32_t c2 = key | (1u << bit);
-                const uint64_t s = mass([&](float z, int i) { return kept(z, i) && ordered_bits(z) >= c2; });
-                if (static_cast<double>(s) >= limit && s > 0) key = c2;
-            }
-            const uint64_t above = mass([&](float z, int i) { return kept(z, i) && ordered_bits(z) > key; });
-            const uint64_t each = w(value_of_ordered(key));
-            // ranks of that value: kept while what is above them is below the limit
-            const double ties = each ? ceil((limit - static_cast<double>(above)) / static_cast<double>(each)) : 1.0;
-            const int want = ties < 1.0 ? 1 : (ties > static_cast<double>(V) ? V : static_cast<int>(ties));
-            int id = 0;
-            for (int bit = 30; bit >= 0; --bit) {
-                const int c2 = id + (1 << bit);
-                if (c2 < V &&
-                    count([&](float z, int i) { return kept(z, i) && ordered_bits(z) == key && i < c2; }) < want)
-                    id = c2;
-            }
-            kept.key = key, kept.id = id;
-        }
+        R.weigh.m = m;
+        R.weigh.c_hi = static_cast<float>(c);
+        R.weigh.c_lo = static_cast<float>(c - static_cast<double>(R.weigh.c_hi));
+        R.weigh.table = static_cast<uint32_t>(rint(exp2(static_cast<double>(lane) / 32.0) * 134217728.0));
+        if (top_k > 0 && top_k < P.V) R.template limit_to<false>(kept, top_k, 0.f);
+        if (top_p <= 0.f || min_p > 1.f)
+            kept = only;
+        else if (top_p < 1.f)
+            R.template limit_to<true>(kept, 0, top_p);
         if (min_p > 0.f) {
             // w >= min_p as a least logit, rounded up to a float; the largest logit stays
             const double least = static_cast<double>(m) + static_cast<double>(tau) * log(static_cast<double>(min_p));
-            kept.least = __double2float_ru(least);
-            if (min_p >= 1.f) kept.least = m;
-            if (min_p > 1.f) kept.key = static_cast<uint32_t>(best >> 32), kept.id = key_id(best);
+            kept.least = min_p >= 1.f ? m : __double2float_ru(least);
         }
-        const uint64_t total = mass(kept);
-        // first id whose cumulative kept weight passes u * total
+        // ---- the first id at which the kept weight passes u of its total ------------------------
+        auto weight = [&](float z, int id, bool there) { return R.weight_if(z, there && kept(z, id)); };
+        uint64_t before;
+        const uint64_t total = R.publish(R.stretch_sum(weight), before);
         const uint64_t target = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
-        const int each = ((V + kSampleThreads - 1) / kSampleThreads);
-        uint64_t s = 0;
-        for (int k = 0; k < each; ++k) {
-            const int i = tid * each + k;
-            const float z = i < V ? load_logit<D>(P.logits, at + i) : -INFINITY;
-            const bool in = i < V && z > -INFINITY && kept(z, i);
-            const uint64_t x = w(in ? z : m);
-            s += in ? x : 0;
+        const int token = R.locate(weight, before, target);
+        if (token >= 0 && lane == 0) {
+            P.tokens[row] = token;
+            if (P.prob) {
+                const double z = static_cast<double>(load_logit<D>(P.logits, at + token));
+                P.prob[row] = static_cast<float>(exp((z - static_cast<double>(m)) / static_cast<double>(tau)) * 8796093022208.0 /
+                                                 static_cast<double>(total));
+            }
         }
-        scan[tid] = s;
-        if (tid == 0) hit_thread = -1;
-        __syncthreads();
-        if (tid == 0) {
-            uint64_t run = 0;
-            for (int k = 0; k < kSampleThreads; ++k) {
-                if (run + scan[k] > target) {
-                    hit_thread = k, hit_before = run;
-                    break;
+    }
+    if (P.filtered) {
+        for (int v = tid; v < R.vectors; v += kSampleThreads) {
+            float z[kVec];
+            decode_vec<D>(slice[v], z);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const int id = R.first_id + v * kVec + e;
+                if (!bad && !(kept(z[e], id) && z[e] > -INFINITY)) z[e] = SSD_DROPPED_LOGIT;
+            }
+            if (v < whole) {
+                uint4 w;
+                uint32_t *words = &w.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (kVec == 4) {
+                        words[e] = __float_as_uint(z[e]);
+                    } else {
+                        const __nv_bfloat162 two = __floats2bfloat162_rn(z[2 * e % kVec], z[(2 * e + 1) % kVec]);
+                        words[e] = *reinterpret_cast<const uint32_t *>(&two);
+                    }
                 }
-                run += scan[k];
+                __stcs(reinterpret_cast<uint4 *>(static_cast<char *>(P.filtered) + (at + R.first_id) * D::kBytes) + v, w);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const int id = R.first_id + v * kVec + e;
+                    if (id < P.V) store_logit<D>(P.filtered, at + id, z[e]);
+                }
             }
         }
-        __syncthreads();
-        if (hit_thread >= 0) {
-            uint64_t run = hit_before;
-            int found = -1;
-            for (int k = 0; k < each; ++k) {
-                const int i = hit_thread * each + k;
-                const float z = i < V ? load_logit<D>(P.logits, at + i) : -INFINITY;
-                const bool in = i < V && z > -INFINITY && kept(z, i);
-                const uint64_t x = w(in ? z : m);
-                run += in ? x : 0;
-                if (found < 0 && run > target) found = i;
-            }
-            token = found;
-        }
-        if (tid == 0 && P.prob) {
-            const double z = static_cast<double>(load_logit<D>(P.logits, at + token));
-            prob = static_cast<float>(exp((z - static_cast<double>(m)) / static_cast<double>(tau)) *
-                                      8796093022208.0 / static_cast<double>(total));
-        }
     }
-    if (tid == 0) {
-        P.tokens[row] = token;
-        if (P.prob) P.prob[row] = prob;
+    R.cluster.sync();  // no CTA leaves while another reads its shared memory
+}
+
+constexpr size_t kFixedBytes = (sizeof(Shared) + 15) / 16 * 16;
+
+template <class D>
+int sample_launch(SampleParams P, cudaStream_t stream) {
+    int dev = 0, sms = 0, most = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return SSD_ERR_CUDA;
     }
-    if (P.filtered)
-        for (int i = tid; i < V; i += kSampleThreads) {
-            const float z = load_logit<D>(P.logits, at + i);
-            store_logit<D>(P.filtered, at + i, kept(z, i) && z > -INFINITY ? z : SSD_DROPPED_LOGIT);
+    auto *kernel = sample_kernel<D>;
+    static std::atomic<uint64_t> ready{0};
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+            cudaGetLastError();
+            return SSD_ERR_CUDA;
         }
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    // The fewest CTAs to a row that leave two of them on an SM; more, down to 4 KB slices, where the rows are too
+    // few to fill the GPU.
+    const int vectors = (P.V + D::kVec - 1) / D::kVec;
+    auto slice = [&](int ctas) { return (vectors + ctas - 1) / ctas; };
+    int ctas = 1;
+    while (ctas < 16 && kFixedBytes + static_cast<size_t>(slice(ctas)) * 16 > 112 * 1024) ctas *= 2;
+    while (ctas < 16 && static_cast<int64_t>(P.rows) * ctas * 2 <= 2 * sms && slice(ctas * 2) >= 256) ctas *= 2;
+    P.slice = slice(ctas);
+    const size_t dyn = kFixedBytes + static_cast<size_t>(P.slice) * 16;
+    if (dyn > static_cast<size_t>(most) || static_cast<int64_t>(P.rows) * ctas > 0x7FFFFFFF) return SSD_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(P.rows * ctas));
+    cfg.blockDim = dim3(kSampleThreads);
+    cfg.dynamicSmemBytes = dyn;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, P) != cudaSuccess) {
+        cudaGetLastError();
+        return SSD_ERR_CUDA;
+    }
+    return SSD_OK;
 }
 
 }  // namespace
@@ -296,12 +730,10 @@ extern "C" int ssd_sample(const void *logits, int dtype, int rows, int V, int64_
     if (dtype != SSD_F32 && dtype != SSD_BF16) return SSD_ERR_DTYPE;
     if (!logits || !temperature || !uniforms || !tokens || rows < 1 || V < 2 || ld < V) return SSD_ERR_INVALID_ARG;
     if (V > (dtype == SSD_F32 ? SSD_MAX_V_F32 : SSD_MAX_V_BF16)) return SSD_ERR_UNSUPPORTED;
-    const SampleParams P{logits,   rows,     V,      ld,   temperature, top_k,    top_p,
-                         min_p,    uniforms, tokens, prob, filtered,    dev_status};
+    const int bytes = dtype == SSD_F32 ? 4 : 2;
+    SampleParams P{logits,   rows,   V,    ld,       temperature, top_k, top_p, min_p,
+                   uniforms, tokens, prob, filtered, dev_status,  0,     0};
+    P.aligned = aligned(logits, 16) && (rows == 1 || ld * bytes % 16 == 0) && (!filtered || aligned(filtered, 16));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == SSD_F32)
-        sample_kernel<F32Tag><<<static_cast<unsigned>(rows), kSampleThreads, 0, s>>>(P);
-    else
-        sample_kernel<BF16Tag><<<static_cast<unsigned>(rows), kSampleThreads, 0, s>>>(P);
-    return launched();
+    return dtype == SSD_F32 ? sample_launch<F32Tag>(P, s) : sample_launch<BF16Tag>(P, s);
 }
