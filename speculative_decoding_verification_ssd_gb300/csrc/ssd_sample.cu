@@ -62,7 +62,8 @@ struct SampleParams {
 struct Weigher {
     float m, c_hi, c_lo;
     uint32_t table;
-    __device__ __forceinline__ uint64_t operator()(float z) const {
+    // The weight as `value` * 2^-(27 + shift), 2^27 <= value < 2^28; false below 2^-60.
+    __device__ __forceinline__ bool parts(float z, uint32_t &value, int &shift) const {
         const float d = z - m;
         // what the subtraction rounded off, exact (m >= z; both finite)
         const float bb = d - z;
@@ -80,23 +81,68 @@ struct Weigher {
         q = fmaf(g, q, 0.6931471806f) * g;
         const uint32_t base = __shfl_sync(0xFFFFFFFFu, table, k & 31);
         const int more = __float_as_int(fmaf(static_cast<float>(base), q, magic)) - __float_as_int(magic);
-        const uint64_t v = static_cast<uint64_t>(base + static_cast<uint32_t>(more)) << 16;
-        const int shift = -(k >> 5);
-        return t > -60.f ? v >> shift : 0;
+        value = base + static_cast<uint32_t>(more);
+        shift = -(k >> 5);
+        return t > -60.f;
+    }
+    __device__ __forceinline__ uint64_t operator()(float z) const {
+        uint32_t value;
+        int shift;
+        const bool there = parts(z, value, shift);
+        return there ? (static_cast<uint64_t>(value) << 16) >> shift : 0;
     }
 };
 
+// 2^(i / 32) in units of 2^-27.
+__device__ const uint32_t kPowers[32] = {
+    134217728u, 137156714u, 140160054u, 143229160u,
+    146365470u, 149570457u, 152845623u, 156192507u,
+    159612677u, 163107740u, 166679334u, 170329136u,
+    174058859u, 177870251u, 181765103u, 185745240u,
+    189812531u, 193968884u, 198216250u, 202556621u,
+    206992033u, 211524568u, 216156353u, 220889561u,
+    225726413u, 230669177u, 235720175u, 240881774u,
+    246156398u, 251546522u, 257054673u, 262683438u,};
 
-// What is kept: ordered value above `key`, or equal to it and id <= `id`; and value >= `least`.
+// What is kept: values above `last`, or equal to it with an id up to `id`; and values >= `least`.
 struct Kept {
-    uint32_t key;
+    float last;
     int id;
     float least;
     __device__ __forceinline__ bool operator()(float z, int i) const {
-        const uint32_t o = ordered_bits(z);
-        return (o > key || (o == key && i <= id)) && z >= least;
+        return (z > last || (z == last && i <= id)) && z >= least;
     }
+    // no value above this is left out, none below it kept
+    __device__ __forceinline__ float border() const { return fmaxf(last, least); }
 };
+
+// Largest of a vector's values (NaN left out).
+template <class D>
+__device__ __forceinline__ float vector_max(const uint4 &w);
+template <>
+__device__ __forceinline__ float vector_max<F32Tag>(const uint4 &w) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+template <>
+__device__ __forceinline__ float vector_max<BF16Tag>(const uint4 &w) {
+    auto two = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(two(w.x), two(w.y)), __hmax2(two(w.z), two(w.w)));
+    return __bfloat162float(__hmax(__low2bfloat16(m), __high2bfloat16(m)));
+}
+// Whether any of a vector's values is NaN: the maximum that passes NaN on.
+template <class D>
+__device__ __forceinline__ bool vector_nan(const uint4 &w);
+template <>
+__device__ __forceinline__ bool vector_nan<F32Tag>(const uint4 &w) {
+    const float a = __uint_as_float(w.x), b = __uint_as_float(w.y), c = __uint_as_float(w.z), d = __uint_as_float(w.w);
+    return a != a || b != b || c != c || d != d;
+}
+template <>
+__device__ __forceinline__ bool vector_nan<BF16Tag>(const uint4 &w) {
+    auto two = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); };
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(two(w.x), two(w.y)), __hmax2_nan(two(w.z), two(w.w)));
+    return isnan(__bfloat162float(__low2bfloat16(m))) || isnan(__bfloat162float(__high2bfloat16(m)));
+}
 
 struct Histogram {
     uint32_t count[kBins], low[kBins], high[kBins];  // weights: 64 bits in two words
@@ -115,9 +161,10 @@ struct Shared {
     uint64_t warp_sum[kSampleWarps];
     uint64_t red[kSampleWarps];
     uint32_t red32[kSampleWarps];
-    uint64_t found_above, found_total;
-    uint32_t found_bin, found_in, found_rank;
-    uint64_t full;
+    uint64_t found_above, goal, target;
+    uint32_t found_bin, found_in;
+    float c_hi, c_lo;
+    double drop;  // tau log(min_p)
 };
 
 template <class D>
@@ -152,14 +199,17 @@ struct Row {
         const int left = P.V - first_id;
         vectors = left <= 0 ? 0 : min(P.slice, (left + kVec - 1) / kVec);
     }
-    // fn(z, id, there) for every token of the slice, whole warps at a time
+    // fn(z, id, there) for the tokens of the slice, whole warps at a time; vectors whose largest logit is below
+    // `border` are passed over where a warp has no other.
     template <class Fn>
-    __device__ __forceinline__ void each(Fn &&fn) {
+    __device__ __forceinline__ void each(float border, Fn &&fn) {
         for (int v0 = 0; v0 < vectors; v0 += kSampleThreads) {
             const int v = v0 + static_cast<int>(threadIdx.x);
-            float z[kVec];
             const bool in = v < vectors;
-            decode_vec<D>(slice[in ? v : 0], z);
+            const uint4 w = slice[in ? v : 0];
+            if (!__any_sync(kAll, in && vector_max<D>(w) >= border)) continue;
+            float z[kVec];
+            decode_vec<D>(w, z);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 const int id = first_id + v * kVec + e;
@@ -168,6 +218,11 @@ struct Row {
         }
     }
     __device__ __forceinline__ uint32_t distance(float z) const { return __float_as_uint(m - z); }
+    // A value that every token nearer than d exceeds: m - d less what the distances and this difference are rounded by.
+    __device__ __forceinline__ float nearest(uint32_t d) const {
+        const float x = __uint_as_float(min(d, 0x7F7FFFFFu));
+        return m - x - (fabsf(m) + x) * 1e-6f;
+    }
 
     // Sums of two words over the cluster; every thread gets them.
     __device__ __forceinline__ void cluster_sum(uint64_t &a, uint64_t &b) {
@@ -197,13 +252,15 @@ struct Row {
     // this warp's stretch of the slice (warps take consecutive stretches).  -1 in CTAs that do not hold it.
     __device__ __forceinline__ int warp_stretch() const { return (vectors + kSampleWarps - 1) / kSampleWarps; }
     template <class Weight>
-    __device__ __forceinline__ uint64_t stretch_sum(Weight &&weight) {
+    __device__ __forceinline__ uint64_t stretch_sum(float border, Weight &&weight) {
         const int n = warp_stretch(), from = static_cast<int>(threadIdx.x >> 5) * n, to = min(from + n, vectors);
         uint64_t s = 0;
         for (int v0 = from; v0 < to; v0 += 32) {
             const int v = v0 + static_cast<int>(threadIdx.x & 31);
+            const uint4 w = slice[v < to ? v : 0];
+            if (!__any_sync(kAll, v < to && vector_max<D>(w) >= border)) continue;
             float z[kVec];
-            decode_vec<D>(slice[v < to ? v : 0], z);
+            decode_vec<D>(w, z);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 const int id = first_id + v * kVec + e;
@@ -236,7 +293,7 @@ struct Row {
         return total;
     }
     template <class Weight>
-    __device__ __forceinline__ int locate(Weight &&weight, uint64_t before, uint64_t target) {
+    __device__ __forceinline__ int locate(Weight &&weight, uint64_t before, uint64_t target, float &value) {
         int w = 0;
         uint64_t run = before;
         for (; w < kSampleWarps; ++w) {
@@ -268,12 +325,14 @@ struct Row {
             if (over) {
                 const int l = __ffs(over) - 1;
                 int id = -1;
+                float at = 0.f;
                 uint64_t x = run + upto - s;
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) {
                     x += each_w[e];
-                    if (id < 0 && x > target) id = first_id + v * kVec + e;
+                    if (id < 0 && x > target) id = first_id + v * kVec + e, at = z[e];
                 }
+                value = __shfl_sync(kAll, at, l);
                 return __shfl_sync(kAll, id, l);
             }
             run += __shfl_sync(kAll, upto, 31);
@@ -296,7 +355,8 @@ struct Row {
         uint32_t lo = 0, hi = kInfinite + 1, shift = 0;  // bits of d: the range looked at, from the second level on
         bool first = true;
         uint64_t above = 0, in_range = 0;  // tokens or weight above the range; tokens in it
-        double goal = 0.0;
+        uint64_t goal = static_cast<uint64_t>(k);
+        const float border = kMass ? kept.border() : -INFINITY;
         // a level divides its range by 512: three and the first end at single distances
         for (int level = 0; level < 8; ++level) {
             Histogram &H = S.hist[level & 1];
@@ -304,7 +364,7 @@ struct Row {
             H.count[t] = 0;
             if (kMass) H.low[t] = H.high[t] = 0;
             __syncthreads();
-            each([&](float z, int id, bool there) {
+            each(first ? border : nearest(hi), [&](float z, int id, bool there) {
                 const uint32_t d = distance(z);
                 bool in = there && d >= lo && d < hi && (!kMass || kept(z, id));
                 const int bin = first ? min(max((static_cast<int>(d - kNear) >> kFirstShift) + 1, 0), kBins - 1)
@@ -353,9 +413,13 @@ struct Row {
                 total += x;
             }
             upto += before;
-            if (first) goal = kMass ? static_cast<double>(share) * static_cast<double>(total) : static_cast<double>(k);
-            const double start = static_cast<double>(above + upto - mine), end = static_cast<double>(above + upto);
-            if (mine && start < goal && end >= goal) {
+            if (kMass && first) {
+                // sums are whole numbers: below share * total is below that rounded up
+                if (t == 0) S.goal = static_cast<uint64_t>(ceil(static_cast<double>(share) * static_cast<double>(total)));
+                __syncthreads();
+                goal = S.goal;
+            }
+            if (mine && above + upto - mine < goal && above + upto >= goal) {
                 S.found_bin = static_cast<uint32_t>(t);
                 S.found_above = above + upto - mine;
                 S.found_in = count;
@@ -384,7 +448,7 @@ struct Row {
         // Many tokens at one distance: of one value as a rule (a bf16 row has few), which rank by id.  Distances are
         // rounded, so values far below the largest may share one: then the last value kept is found bit by bit.
         uint32_t low_key = 0xFFFFFFFFu, high_key = 0;
-        each([&](float z, int id, bool there) {
+        each(nearest(hi), [&](float z, int id, bool there) {
             const uint32_t d = distance(z);
             if (there && d >= lo && d < hi && (!kMass || kept(z, id))) {
                 const uint32_t o = ordered_bits(z);
@@ -415,7 +479,7 @@ struct Row {
             key = 0;
             auto upto = [&](uint32_t from) {  // tokens or weight of the range from that key on
                 uint64_t s = 0, none = 0;
-                each([&](float z, int id, bool there) {
+                each(nearest(hi), [&](float z, int id, bool there) {
                     const uint32_t d = distance(z);
                     const bool in = there && d >= lo && d < hi && ordered_bits(z) >= from && (!kMass || kept(z, id));
                     s += kMass ? weight_if(z, in) : static_cast<uint64_t>(in);
@@ -425,38 +489,38 @@ struct Row {
             };
             for (int bit = 31; bit >= 0; --bit) {
                 const uint32_t c = key | (1u << bit);
-                if (c <= high_key && static_cast<double>(above + upto(c)) >= goal) key = c;
+                if (c <= high_key && above + upto(c) >= goal) key = c;
             }
             if (key < 0xFFFFFFFFu) above += upto(key + 1);
         }
-        uint64_t ties;
+        // ranks of that value: kept while what is above them is below the goal
+        const float value = value_of_ordered(key);
+        uint64_t ties = goal - above;
         if (kMass) {
-            const uint64_t one = weigh(value_of_ordered(key));
-            const double n = one ? ceil((goal - static_cast<double>(above)) / static_cast<double>(one)) : 1.0;
-            ties = n < 1.0 ? 1 : (n > static_cast<double>(P.V) ? static_cast<uint64_t>(P.V) : static_cast<uint64_t>(n));
-        } else {
-            ties = static_cast<uint64_t>(k) - above;
+            const uint64_t one = weigh(value);
+            ties = one ? (goal - above + one - 1) / one : 1;
         }
         auto tie = [&](float z, int id, bool there) {
-            return static_cast<uint64_t>(there && ordered_bits(z) == key && (!kMass || kept(z, id)));
+            return static_cast<uint64_t>(there && z == value && (!kMass || kept(z, id)));
         };
         uint64_t before;
-        publish(stretch_sum(tie), before);
-        const int id = locate(tie, before, ties - 1);
+        publish(stretch_sum(value, tie), before);
+        float unused;
+        const int id = locate(tie, before, ties - 1, unused);
         if (id >= 0 && (t & 31) == 0)
             for (int c = 0; c < ctas; ++c) *cluster.map_shared_rank(&S.result, c) = id;
         cluster.sync();
-        kept.key = key;
+        kept.last = value;
         kept.id = S.result;
     }
 
     // The few tokens with lo <= d < hi against one another.
     template <bool kMass>
-    __device__ __forceinline__ void rank_range(Kept &kept, uint32_t lo, uint32_t hi, uint64_t above, double goal) {
+    __device__ __forceinline__ void rank_range(Kept &kept, uint32_t lo, uint32_t hi, uint64_t above, uint64_t goal) {
         const int t = static_cast<int>(threadIdx.x);
         if (t == 0) S.listed = 0;
         __syncthreads();
-        each([&](float z, int id, bool there) {
+        each(nearest(hi), [&](float z, int id, bool there) {
             const uint32_t d = distance(z);
             if (there && d >= lo && d < hi && (!kMass || kept(z, id))) {
                 const int at = atomicAdd(&S.listed, 1);
@@ -488,13 +552,13 @@ struct Row {
                     if (kMass) higher += S.ranked_weight[i];
                 }
             if (!kMass) higher += static_cast<uint64_t>(place);
-            in = static_cast<double>(higher) < goal;
+            in = higher < goal;
         }
         const int left = __syncthreads_count(in);
         if (in && place == left - 1) S.found_above = own;
         __syncthreads();
         const uint64_t last = S.found_above;
-        kept.key = static_cast<uint32_t>(last >> 32);
+        kept.last = key_value(last);
         kept.id = key_id(last);
         // the next limit's histogram may use what others still read: they are past it after its own barrier
     }
@@ -514,19 +578,21 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
     uint64_t best = 0;
     int odd = 0;
     const char *src = static_cast<const char *>(P.logits) + (at + R.first_id) * D::kBytes;
-    auto look = [&](int v, const uint4 &w) {
-        float z[kVec];
-        decode_vec<D>(w, z);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const int id = R.first_id + v * kVec + e;
-            if (id < P.V) {
-                odd |= !(z[e] < INFINITY);
-                const uint64_t k = make_key(z[e], id);
-                best = k > best ? k : best;
-            }
-        }
+    float top = -INFINITY;
+    int top_at = -1;
+    auto look = [&](int v, const uint4 &w) {  // a thread's vectors come in ascending order
+        const float x = vector_max<D>(w);
+        odd |= vector_nan<D>(w);
+        if (x > top) top = x, top_at = v;
     };
+    if (tid == kSampleThreads - 1) {
+        // 64-bit arithmetic is slow here: one thread does it, while the slice is on its way
+        const float tau = P.tau[row], least = P.min_p ? P.min_p[row] : 0.f;
+        const double c = fmin(1.4426950408889634074 / static_cast<double>(tau), 1e30);
+        S.c_hi = static_cast<float>(c);
+        S.c_lo = static_cast<float>(c - static_cast<double>(S.c_hi));
+        if (least > 0.f) S.drop = static_cast<double>(tau) * log(static_cast<double>(least));
+    }
     const int whole = P.aligned ? max(0, min(R.vectors, (P.V - R.first_id) / kVec)) : 0;
     constexpr int kFlight = 4;
     for (int v0 = tid; v0 < whole; v0 += kSampleThreads * kFlight) {
@@ -561,6 +627,14 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
         slice[v] = w;
         look(v, w);
     }
+    odd |= top == INFINITY;
+    if (top_at >= 0) {
+        float z[kVec];
+        decode_vec<D>(slice[top_at], z);
+#pragma unroll
+        for (int e = kVec - 1; e >= 0; --e)
+            if (z[e] == top) best = make_key(top, R.first_id + top_at * kVec + e);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const uint64_t t = __shfl_xor_sync(kAll, best, o);
@@ -580,7 +654,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
         best = b > best ? b : best;
         odd |= *R.cluster.map_shared_rank(&S.odd, c);
     }
-    const float m = key_value(best);
+    const float m = best ? key_value(best) : -INFINITY;
     const float tau = P.tau[row], u = P.u[row];
     const int top_k = P.top_k ? P.top_k[row] : 0;
     const float top_p = P.top_p ? P.top_p[row] : 1.f;
@@ -590,8 +664,8 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
     if (!(tau >= 0.f) || !(tau < INFINITY)) bad |= SSD_DEV_BAD_TEMPERATURE;
     if (top_p != top_p || min_p != min_p || !(u >= 0.f && u < 1.f)) bad |= SSD_DEV_BAD_PARAM;
 
-    const Kept only{static_cast<uint32_t>(best >> 32), key_id(best), -INFINITY};
-    Kept kept{0u, P.V, -INFINITY};
+    const Kept only{m, key_id(best), -INFINITY};
+    Kept kept{-INFINITY, P.V, -INFINITY};
     if (bad) {
         if (R.rank == 0 && tid == 0) {
             report(P.dev_status, bad);
@@ -606,59 +680,61 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
         }
     } else {
         R.m = m;
-        const double c = fmin(1.4426950408889634074 / static_cast<double>(tau), 1e30);
         R.weigh.m = m;
-        R.weigh.c_hi = static_cast<float>(c);
-        R.weigh.c_lo = static_cast<float>(c - static_cast<double>(R.weigh.c_hi));
-        R.weigh.table = static_cast<uint32_t>(rint(exp2(static_cast<double>(lane) / 32.0) * 134217728.0));
+        R.weigh.c_hi = S.c_hi, R.weigh.c_lo = S.c_lo;
+        R.weigh.table = __ldg(&kPowers[lane]);
         if (top_k > 0 && top_k < P.V) R.template limit_to<false>(kept, top_k, 0.f);
         if (top_p <= 0.f || min_p > 1.f)
             kept = only;
         else if (top_p < 1.f)
             R.template limit_to<true>(kept, 0, top_p);
-        if (min_p > 0.f) {
-            // w >= min_p as a least logit, rounded up to a float; the largest logit stays
-            const double least = static_cast<double>(m) + static_cast<double>(tau) * log(static_cast<double>(min_p));
-            kept.least = min_p >= 1.f ? m : __double2float_ru(least);
-        }
+        // w >= min_p as a least logit, rounded up to a float; the largest logit stays
+        if (min_p > 0.f) kept.least = min_p >= 1.f ? m : __double2float_ru(static_cast<double>(m) + S.drop);
         // ---- the first id at which the kept weight passes u of its total ------------------------
-        auto weight = [&](float z, int id, bool there) { return R.weight_if(z, there && kept(z, id)); };
+        const bool all = kept.border() == -INFINITY && kept.id >= P.V;
+        auto weight = [&](float z, int id, bool there) { return R.weight_if(z, there && (all || kept(z, id))); };
         uint64_t before;
-        const uint64_t total = R.publish(R.stretch_sum(weight), before);
-        const uint64_t target = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
-        const int token = R.locate(weight, before, target);
-        if (token >= 0 && lane == 0) {
-            P.tokens[row] = token;
-            if (P.prob) {
-                const double z = static_cast<double>(load_logit<D>(P.logits, at + token));
-                P.prob[row] = static_cast<float>(exp((z - static_cast<double>(m)) / static_cast<double>(tau)) * 8796093022208.0 /
-                                                 static_cast<double>(total));
+        const uint64_t total = R.publish(R.stretch_sum(kept.border(), weight), before);
+        if (tid == 0) S.target = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
+        __syncthreads();
+        float z;
+        const int token = R.locate(weight, before, S.target, z);
+        if (token >= 0) {  // one warp of the cluster
+            uint32_t value;
+            int shift;
+            R.weigh.parts(z, value, shift);
+            if (lane == 0) {
+                P.tokens[row] = token;
+                // value * 2^-(27 + shift) of total * 2^-43
+                if (P.prob)
+                    P.prob[row] = static_cast<float>(static_cast<double>(value) * __hiloint2double((1023 + 16 - shift) << 20, 0) /
+                                                     static_cast<double>(total));
             }
         }
     }
     if (P.filtered) {
+        const uint32_t dropped = kVec == 4 ? __float_as_uint(SSD_DROPPED_LOGIT)
+                                           : static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16(SSD_DROPPED_LOGIT)));
         for (int v = tid; v < R.vectors; v += kSampleThreads) {
-            float z[kVec];
-            decode_vec<D>(slice[v], z);
+            uint4 w = slice[v];
+            uint32_t *words = &w.x;
+            if (!bad) {
+                float z[kVec];
+                decode_vec<D>(w, z);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const int id = R.first_id + v * kVec + e;
-                if (!bad && !(kept(z[e], id) && z[e] > -INFINITY)) z[e] = SSD_DROPPED_LOGIT;
+                for (int e = 0; e < kVec; ++e) {
+                    if (kept(z[e], R.first_id + v * kVec + e) && z[e] > -INFINITY) continue;
+                    if (kVec == 4)
+                        words[e % 4] = dropped;
+                    else
+                        words[e / 2 % 4] = e % 2 ? (words[e / 2 % 4] & 0xFFFFu) | (dropped << 16) : (words[e / 2 % 4] & 0xFFFF0000u) | dropped;
+                }
             }
             if (v < whole) {
-                uint4 w;
-                uint32_t *words = &w.x;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (kVec == 4) {
-                        words[e] = __float_as_uint(z[e]);
-                    } else {
-                        const __nv_bfloat162 two = __floats2bfloat162_rn(z[2 * e % kVec], z[(2 * e + 1) % kVec]);
-                        words[e] = *reinterpret_cast<const uint32_t *>(&two);
-                    }
-                }
                 __stcs(reinterpret_cast<uint4 *>(static_cast<char *>(P.filtered) + (at + R.first_id) * D::kBytes) + v, w);
             } else {
+                float z[kVec];
+                decode_vec<D>(w, z);
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) {
                     const int id = R.first_id + v * kVec + e;
