@@ -80,7 +80,9 @@ struct Weigher {
         q = fmaf(g, q, 0.2402265070f);
         q = fmaf(g, q, 0.6931471806f) * g;
         const uint32_t base = __shfl_sync(0xFFFFFFFFu, table, k & 31);
-        const int more = __float_as_int(fmaf(static_cast<float>(base), q, magic)) - __float_as_int(magic);
+        // base as a float, cut off at 24 bits: its part of the product ends 2^-29 below
+        const float rough = __uint_as_float((base >> 4) + 0x4C800000u);
+        const int more = __float_as_int(fmaf(rough, q, magic)) - __float_as_int(magic);
         value = base + static_cast<uint32_t>(more);
         shift = -(k >> 5);
         return t > -60.f;
@@ -153,17 +155,13 @@ struct Shared {
     uint64_t list[kList];    // this CTA's tokens of the range
     uint64_t ranked[kList];  // the cluster's
     uint64_t ranked_weight[kList];
-    uint64_t sums[2][2];     // published to the cluster, in turn
-    uint64_t best;
-    int odd;
+    uint64_t sums[2][2][kSampleWarps];  // two words of each warp, published to the cluster in turn
+    uint64_t best[kSampleWarps];
     int listed;
     int result;
-    uint64_t warp_sum[kSampleWarps];
     uint64_t red[kSampleWarps];
-    uint32_t red32[kSampleWarps];
     uint64_t found_above, goal, target;
     uint32_t found_bin, found_in;
-    float c_hi, c_lo;
     double drop;  // tau log(min_p)
 };
 
@@ -187,7 +185,8 @@ struct Row {
     cg::cluster_group cluster;
     int ctas, rank, first_id;  // id of the slice's first token
     int vectors;               // of the slice
-    int turn = 0;              // which of the two published words / histograms is next
+    float top = -INFINITY;     // of this thread's vectors
+    int turn = 0, published = 0;  // which of the published words is next, and which holds the stretches' sums
     float m;
     Weigher weigh;
 
@@ -199,15 +198,26 @@ struct Row {
         const int left = P.V - first_id;
         vectors = left <= 0 ? 0 : min(P.slice, (left + kVec - 1) / kVec);
     }
-    // fn(z, id, there) for the tokens of the slice, whole warps at a time; vectors whose largest logit is below
-    // `border` are passed over where a warp has no other.
+    // fn(vector, index, there) for vectors [from, to) of the slice in steps of `step`, whole warps at a time; those
+    // whose largest logit is below `border` are passed over where a warp has no other.
+    template <class Fn>
+    __device__ __forceinline__ void scan(int from, int to, int step, int offset, float border, Fn &&fn) {
+        for (int v0 = from; v0 < to; v0 += step) {
+            const int v = v0 + offset;
+            const uint4 w = slice[v < to ? v : 0];
+            if (__any_sync(kAll, v < to && vector_max<D>(w) >= border)) fn(w, v, v < to);
+        }
+    }
+    // Element e of a vector, e not known when compiling.
+    __device__ __forceinline__ static float pick(const uint4 &w, int e) {
+        if (kVec == 4) return __uint_as_float(e & 2 ? (e & 1 ? w.w : w.z) : (e & 1 ? w.y : w.x));
+        const uint32_t two = e & 4 ? (e & 2 ? w.w : w.z) : (e & 2 ? w.y : w.x);
+        return __uint_as_float(e & 1 ? two & 0xFFFF0000u : two << 16);
+    }
+    // fn(z, id, there) for the tokens of the slice.
     template <class Fn>
     __device__ __forceinline__ void each(float border, Fn &&fn) {
-        for (int v0 = 0; v0 < vectors; v0 += kSampleThreads) {
-            const int v = v0 + static_cast<int>(threadIdx.x);
-            const bool in = v < vectors;
-            const uint4 w = slice[in ? v : 0];
-            if (!__any_sync(kAll, in && vector_max<D>(w) >= border)) continue;
+        scan(0, vectors, kSampleThreads, static_cast<int>(threadIdx.x), border, [&](const uint4 &w, int v, bool in) {
             float z[kVec];
             decode_vec<D>(w, z);
 #pragma unroll
@@ -215,6 +225,46 @@ struct Row {
                 const int id = first_id + v * kVec + e;
                 fn(z[e], id, in && id < P.V);
             }
+        });
+    }
+    // add(z, weight, times) for the tokens of a vector that pred(z, id) takes.  Where few do, each lane goes from one
+    // of its own to the next, and the warp weighs as often as its fullest lane has any; where a warp's tokens are
+    // all one value, lane 0 adds them all at once.
+    template <class Pred, class Add>
+    __device__ __forceinline__ void weigh_vector(const uint4 &w, int v, bool in, Pred &&pred, Add &&add) {
+        float z[kVec];
+        decode_vec<D>(w, z);
+        uint32_t mask = 0;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const int id = first_id + v * kVec + e;
+            mask |= (in && id < P.V && z[e] > -INFINITY && pred(z[e], id) ? 1u : 0u) << e;
+        }
+        const int most = static_cast<int>(__reduce_max_sync(kAll, static_cast<uint32_t>(__popc(mask))));
+        if (most == 0) return;
+        if (most * 4 <= kVec * 3) {
+            for (int i = 0; i < most; ++i) {
+                const bool here = mask != 0;
+                const float x = here ? pick(w, __ffs(mask) - 1) : m;
+                mask &= mask - 1;
+                const uint64_t weight = weigh(x);
+                if (here) add(x, weight, 1u);
+            }
+            return;
+        }
+        const uint32_t x0 = __shfl_sync(kAll, w.x, 0);
+        const bool flat = w.x == x0 && w.y == x0 && w.z == x0 && w.w == x0 && (kVec == 4 || x0 >> 16 == (x0 & 0xFFFFu)) &&
+                          mask == (1u << kVec) - 1u;
+        if (__all_sync(kAll, flat)) {
+            const uint64_t weight = weigh(z[0]);
+            if ((threadIdx.x & 31) == 0) add(z[0], weight * (32u * kVec), 32u * kVec);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const bool here = (mask >> e) & 1;
+            const uint64_t weight = weigh(here ? z[e] : m);
+            if (here) add(z[e], weight, 1u);
         }
     }
     __device__ __forceinline__ uint32_t distance(float z) const { return __float_as_uint(m - z); }
@@ -224,80 +274,75 @@ struct Row {
         return m - x - (fabsf(m) + x) * 1e-6f;
     }
 
-    // Sums of two words over the cluster; every thread gets them.
-    __device__ __forceinline__ void cluster_sum(uint64_t &a, uint64_t &b) {
+    // What each warp of the cluster published in word `which`, joined by op(cta, word) over the lanes of every warp:
+    // no second stage in the CTA, and all the loads are under way together.
+    template <class Op>
+    __device__ __forceinline__ void gather(const uint64_t *words, Op &&op) {
+        const int lane = static_cast<int>(threadIdx.x & 31);
+#pragma unroll 4
+        for (int i = lane; i < ctas * kSampleWarps; i += 32)
+            op(i / kSampleWarps, cluster.map_shared_rank(words, i / kSampleWarps)[i % kSampleWarps]);
+    }
+    __device__ __forceinline__ uint64_t warp_total(uint64_t x) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(kAll, a, o);
-            b += __shfl_xor_sync(kAll, b, o);
-        }
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) S.red[threadIdx.x >> 5] = a, S.warp_sum[threadIdx.x >> 5] = b;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            uint64_t x = 0, y = 0;
-            for (int w = 0; w < kSampleWarps; ++w) x += S.red[w], y += S.warp_sum[w];
-            S.sums[turn][0] = x, S.sums[turn][1] = y;
-        }
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+        return x;
+    }
+    // Sum over the cluster; every thread gets it.
+    __device__ __forceinline__ uint64_t cluster_sum(uint64_t a) {
+        a = warp_total(a);
+        if ((threadIdx.x & 31) == 0) S.sums[turn][0][threadIdx.x >> 5] = a;
         cluster.sync();
-        a = b = 0;
-        for (int c = 0; c < ctas; ++c) {
-            const uint64_t *s = cluster.map_shared_rank(&S.sums[turn][0], c);
-            a += s[0], b += s[1];
-        }
+        uint64_t total = 0;
+        gather(&S.sums[turn][0][0], [&](int, uint64_t x) { total += x; });
         turn ^= 1;
+        return warp_total(total);
     }
 
     // The first id, in ascending order, at which the sum of weight(z, id) passes `target`; `mine` is the sum over
     // this warp's stretch of the slice (warps take consecutive stretches).  -1 in CTAs that do not hold it.
     __device__ __forceinline__ int warp_stretch() const { return (vectors + kSampleWarps - 1) / kSampleWarps; }
-    template <class Weight>
-    __device__ __forceinline__ uint64_t stretch_sum(float border, Weight &&weight) {
+    // This warp's part of the sum of weights, or (for ties) of tokens, that pred takes.
+    template <bool kWeigh, class Pred>
+    __device__ __forceinline__ uint64_t stretch_sum(float border, Pred &&pred) {
         const int n = warp_stretch(), from = static_cast<int>(threadIdx.x >> 5) * n, to = min(from + n, vectors);
         uint64_t s = 0;
-        for (int v0 = from; v0 < to; v0 += 32) {
-            const int v = v0 + static_cast<int>(threadIdx.x & 31);
-            const uint4 w = slice[v < to ? v : 0];
-            if (!__any_sync(kAll, v < to && vector_max<D>(w) >= border)) continue;
-            float z[kVec];
-            decode_vec<D>(w, z);
+        scan(from, to, 32, static_cast<int>(threadIdx.x & 31), border, [&](const uint4 &w, int v, bool in) {
+            if (kWeigh) {
+                weigh_vector(w, v, in, pred, [&](float, uint64_t weight, uint32_t) { s += weight; });
+            } else {
+                float z[kVec];
+                decode_vec<D>(w, z);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const int id = first_id + v * kVec + e;
-                s += weight(z[e], id, v < to && id < P.V);
+                for (int e = 0; e < kVec; ++e) {
+                    const int id = first_id + v * kVec + e;
+                    s += in && id < P.V && pred(z[e], id) ? 1 : 0;
+                }
             }
-        }
+        });
         return s;
     }
     // Publishes the stretches' sums; returns the cluster's total, and what lies before this CTA in `before`.
     __device__ __forceinline__ uint64_t publish(uint64_t s, uint64_t &before) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) S.warp_sum[threadIdx.x >> 5] = s;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            uint64_t x = 0;
-            for (int w = 0; w < kSampleWarps; ++w) x += S.warp_sum[w];
-            S.sums[turn][0] = x;
-        }
+        s = warp_total(s);
+        if ((threadIdx.x & 31) == 0) S.sums[turn][0][threadIdx.x >> 5] = s;
         cluster.sync();
-        uint64_t total = 0;
-        before = 0;
-        for (int c = 0; c < ctas; ++c) {
-            const uint64_t x = cluster.map_shared_rank(&S.sums[turn][0], c)[0];
-            if (c < rank) before += x;
+        uint64_t total = 0, first = 0;
+        gather(&S.sums[turn][0][0], [&](int cta, uint64_t x) {
             total += x;
-        }
+            if (cta < rank) first += x;
+        });
+        published = turn;
         turn ^= 1;
-        return total;
+        before = warp_total(first);
+        return warp_total(total);
     }
     template <class Weight>
     __device__ __forceinline__ int locate(Weight &&weight, uint64_t before, uint64_t target, float &value) {
         int w = 0;
         uint64_t run = before;
         for (; w < kSampleWarps; ++w) {
-            const uint64_t s = S.warp_sum[w];
+            const uint64_t s = S.sums[published][0][w];
             if (run <= target && run + s > target) break;
             run += s;
         }
@@ -348,15 +393,58 @@ struct Row {
         return in ? x : 0;
     }
 
+    __device__ __forceinline__ static int first_bin(uint32_t d) {
+        return min(max((static_cast<int>(d - kNear) >> kFirstShift) + 1, 0), kBins - 1);
+    }
+    __device__ __forceinline__ static uint32_t first_end(uint32_t bin) {
+        return bin == 0 ? kNear : (bin == kBins - 1 ? kInfinite + 1 : kNear + (bin << kFirstShift));
+    }
+    // A range of d, from 0 on, that holds the largest tokens of at least k threads (k at most the cluster's threads).
+    __device__ __forceinline__ uint32_t range_of_top(int k) {
+        Histogram &H = S.hist[1];
+        const int t = static_cast<int>(threadIdx.x);
+        H.count[t] = 0;
+        __syncthreads();
+        atomicAdd(&H.count[first_bin(distance(top))], 1u);
+        cluster.sync();
+        uint32_t count = 0;
+#pragma unroll 4
+        for (int c = 0; c < ctas; ++c) count += cluster.map_shared_rank(&H, c)->count[t];
+        uint32_t upto = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(kAll, upto, o);
+            if ((t & 31) >= o) upto += x;
+        }
+        if ((t & 31) == 31) S.red[t >> 5] = upto;
+        __syncthreads();
+        for (int w = 0; w < (t >> 5); ++w) upto += static_cast<uint32_t>(S.red[w]);
+        if (upto - count < static_cast<uint32_t>(k) && upto >= static_cast<uint32_t>(k)) S.found_bin = static_cast<uint32_t>(t);
+        __syncthreads();
+        return first_end(S.found_bin);
+    }
+
     // Narrows `kept` to the ranks that a limit leaves.  kMass: while the weight above a rank is below `share` of
     // what is kept; else the first `k` ranks.
     template <bool kMass>
     __device__ void limit_to(Kept &kept, int k, float share) {
-        uint32_t lo = 0, hi = kInfinite + 1, shift = 0;  // bits of d: the range looked at, from the second level on
+        uint32_t lo = 0, hi = kInfinite + 1, shift = 0;  // bits of d: the range looked at
         bool first = true;
         uint64_t above = 0, in_range = 0;  // tokens or weight above the range; tokens in it
         uint64_t goal = static_cast<uint64_t>(k);
-        const float border = kMass ? kept.border() : -INFINITY;
+        float border = -INFINITY;
+        uint32_t light = 0xFFFFFFFFu;  // d from which tokens only count for the total
+        if (kMass) {
+            border = kept.border();
+            // What lies beyond tau ln(V / (1 - share)) weighs less than 1 - share of the largest alone, so the border
+            // comes before it.  (Beyond the histogram's evenly divided part nothing is left out.)
+            const float d = 1.0001f / weigh.c_hi * log2f(static_cast<float>(P.V) / (1.f - share));
+            if (d < 1000.f) light = __float_as_uint(d);
+        } else if (k <= ctas * kSampleThreads) {
+            // k threads' largest tokens are k tokens: no token beyond the k-th of those is among the k first
+            hi = range_of_top(k);
+            border = nearest(hi);
+        }
         // a level divides its range by 512: three and the first end at single distances
         for (int level = 0; level < 8; ++level) {
             Histogram &H = S.hist[level & 1];
@@ -364,33 +452,52 @@ struct Row {
             H.count[t] = 0;
             if (kMass) H.low[t] = H.high[t] = 0;
             __syncthreads();
-            each(first ? border : nearest(hi), [&](float z, int id, bool there) {
-                const uint32_t d = distance(z);
-                bool in = there && d >= lo && d < hi && (!kMass || kept(z, id));
-                const int bin = first ? min(max((static_cast<int>(d - kNear) >> kFirstShift) + 1, 0), kBins - 1)
-                                      : static_cast<int>((d - lo) >> shift);
-                if (!__any_sync(kAll, in)) return;
-                // a warp of one value (constant rows) adds once
-                const uint32_t d0 = __shfl_sync(kAll, d, 0);
-                const bool same = __all_sync(kAll, in && d == d0);
-                const bool adds = same ? (t & 31) == 0 : in;
-                const uint32_t times = same ? 32 : 1;
-                if (kMass) {
-                    const uint64_t w = weight_if(z, in) * times;
-                    if (adds && w) {
-                        const uint32_t part = static_cast<uint32_t>(w);
-                        const uint32_t was = atomicAdd(&H.low[bin], part);
-                        const uint32_t carry = was + part < was ? 1u : 0u;
-                        const uint32_t rest = static_cast<uint32_t>(w >> 32) + carry;
-                        if (rest) atomicAdd(&H.high[bin], rest);
-                    }
-                }
-                if (adds) atomicAdd(&H.count[bin], times);
-            });
+            uint64_t rest = 0;
+            auto add = [&](int bin, uint64_t w) {
+                const uint32_t part = static_cast<uint32_t>(w);
+                const uint32_t was = atomicAdd(&H.low[bin], part);
+                const uint32_t carry = was + part < was ? 1u : 0u;
+                const uint32_t more = static_cast<uint32_t>(w >> 32) + carry;
+                if (more) atomicAdd(&H.high[bin], more);
+            };
+            auto bin_of = [&](uint32_t d) { return first ? first_bin(d) : static_cast<int>((d - lo) >> shift); };
+            const float from = first ? border : nearest(hi);
+            if (kMass) {
+                scan(0, vectors, kSampleThreads, t, from, [&](const uint4 &w, int v, bool in) {
+                    weigh_vector(
+                        w, v, in,
+                        [&](float z, int id) {
+                            const uint32_t d = distance(z);
+                            return d >= lo && d < hi && kept(z, id);
+                        },
+                        [&](float z, uint64_t weight, uint32_t times) {
+                            const uint32_t d = distance(z);
+                            if (d >= light) {
+                                rest += weight;
+                            } else {
+                                add(bin_of(d), weight);
+                                atomicAdd(&H.count[bin_of(d)], times);
+                            }
+                        });
+                });
+            } else {
+                each(from, [&](float z, int, bool there) {
+                    const uint32_t d = distance(z);
+                    const bool in = there && d >= lo && d < hi;
+                    const uint32_t d0 = __shfl_sync(kAll, d, 0);
+                    const bool alike = __all_sync(kAll, in && d == d0);  // constant rows
+                    if (alike ? (t & 31) == 0 : in) atomicAdd(&H.count[bin_of(d)], alike ? 32u : 1u);
+                });
+            }
+            if (kMass && first && light != 0xFFFFFFFFu) {
+                rest = warp_total(rest);
+                if ((t & 31) == 0 && rest) add(kBins - 1, rest);
+            }
             cluster.sync();
             // every CTA adds up all histograms: thread t bin t
             uint32_t count = 0;
             uint64_t mass = 0;
+#pragma unroll 4
             for (int c = 0; c < ctas; ++c) {
                 const Histogram *h = cluster.map_shared_rank(&H, c);
                 count += h->count[t];
@@ -430,8 +537,9 @@ struct Row {
             in_range = S.found_in;
             if (first) {
                 lo = bin == 0 ? 0 : kNear + ((bin - 1) << kFirstShift);
-                hi = bin == 0 ? kNear : (bin == kBins - 1 ? kInfinite + 1 : kNear + (bin << kFirstShift));
+                hi = min(min(hi, first_end(bin)), light);
                 first = false;
+                light = 0xFFFFFFFFu;
             } else {
                 lo += bin << shift;
                 hi = min(hi, lo + (1u << shift));
@@ -455,37 +563,25 @@ struct Row {
                 low_key = min(low_key, o), high_key = max(high_key, o);
             }
         });
-        // the cluster's extremes, by sums of one word each: published as the block's own first
         low_key = __reduce_min_sync(kAll, low_key), high_key = __reduce_max_sync(kAll, high_key);
         const int t = static_cast<int>(threadIdx.x);
-        __syncthreads();
-        if ((t & 31) == 0) S.red[t >> 5] = (static_cast<uint64_t>(low_key) << 32) | high_key;
-        __syncthreads();
-        if (t == 0) {
-            for (int w = 0; w < kSampleWarps; ++w) {
-                low_key = min(low_key, static_cast<uint32_t>(S.red[w] >> 32));
-                high_key = max(high_key, static_cast<uint32_t>(S.red[w]));
-            }
-            S.sums[turn][0] = low_key, S.sums[turn][1] = high_key;
-        }
+        if ((t & 31) == 0) S.sums[turn][0][t >> 5] = low_key, S.sums[turn][1][t >> 5] = high_key;
         cluster.sync();
-        for (int c = 0; c < ctas; ++c) {
-            const uint64_t *s = cluster.map_shared_rank(&S.sums[turn][0], c);
-            low_key = min(low_key, static_cast<uint32_t>(s[0])), high_key = max(high_key, static_cast<uint32_t>(s[1]));
-        }
+        gather(&S.sums[turn][0][0], [&](int, uint64_t x) { low_key = min(low_key, static_cast<uint32_t>(x)); });
+        gather(&S.sums[turn][1][0], [&](int, uint64_t x) { high_key = max(high_key, static_cast<uint32_t>(x)); });
+        low_key = __reduce_min_sync(kAll, low_key), high_key = __reduce_max_sync(kAll, high_key);
         turn ^= 1;
         uint32_t key = low_key;
         if (low_key != high_key) {
             key = 0;
             auto upto = [&](uint32_t from) {  // tokens or weight of the range from that key on
-                uint64_t s = 0, none = 0;
+                uint64_t s = 0;
                 each(nearest(hi), [&](float z, int id, bool there) {
                     const uint32_t d = distance(z);
                     const bool in = there && d >= lo && d < hi && ordered_bits(z) >= from && (!kMass || kept(z, id));
                     s += kMass ? weight_if(z, in) : static_cast<uint64_t>(in);
                 });
-                cluster_sum(s, none);
-                return s;
+                return cluster_sum(s);
             };
             for (int bit = 31; bit >= 0; --bit) {
                 const uint32_t c = key | (1u << bit);
@@ -500,11 +596,10 @@ struct Row {
             const uint64_t one = weigh(value);
             ties = one ? (goal - above + one - 1) / one : 1;
         }
-        auto tie = [&](float z, int id, bool there) {
-            return static_cast<uint64_t>(there && z == value && (!kMass || kept(z, id)));
-        };
+        auto is_tie = [&](float z, int id) { return z == value && (!kMass || kept(z, id)); };
+        auto tie = [&](float z, int id, bool there) { return static_cast<uint64_t>(there && is_tie(z, id)); };
         uint64_t before;
-        publish(stretch_sum(value, tie), before);
+        publish(stretch_sum<false>(value, is_tie), before);
         float unused;
         const int id = locate(tie, before, ties - 1, unused);
         if (id >= 0 && (t & 31) == 0)
@@ -585,14 +680,6 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
         odd |= vector_nan<D>(w);
         if (x > top) top = x, top_at = v;
     };
-    if (tid == kSampleThreads - 1) {
-        // 64-bit arithmetic is slow here: one thread does it, while the slice is on its way
-        const float tau = P.tau[row], least = P.min_p ? P.min_p[row] : 0.f;
-        const double c = fmin(1.4426950408889634074 / static_cast<double>(tau), 1e30);
-        S.c_hi = static_cast<float>(c);
-        S.c_lo = static_cast<float>(c - static_cast<double>(S.c_hi));
-        if (least > 0.f) S.drop = static_cast<double>(tau) * log(static_cast<double>(least));
-    }
     const int whole = P.aligned ? max(0, min(R.vectors, (P.V - R.first_id) / kVec)) : 0;
     constexpr int kFlight = 4;
     for (int v0 = tid; v0 < whole; v0 += kSampleThreads * kFlight) {
@@ -635,26 +722,28 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
         for (int e = kVec - 1; e >= 0; --e)
             if (z[e] == top) best = make_key(top, R.first_id + top_at * kVec + e);
     }
+    constexpr uint64_t kOdd = ~0ull;  // no token's key
+    if (odd) best = kOdd;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const uint64_t t = __shfl_xor_sync(kAll, best, o);
         best = t > best ? t : best;
     }
-    if (lane == 0) S.red[tid >> 5] = best;
-    odd = __syncthreads_or(odd);
-    if (tid == 0) {
-        for (int w = 0; w < kSampleWarps; ++w) best = S.red[w] > best ? S.red[w] : best;
-        S.best = best;
-        S.odd = odd;
+    if (lane == 0) S.best[tid >> 5] = best;
+    if (tid == kSampleThreads - 1 && P.min_p) {
+        // 64-bit arithmetic is slow here: one thread does it
+        const float least = P.min_p[row];
+        if (least > 0.f) S.drop = static_cast<double>(P.tau[row]) * log(static_cast<double>(least));
     }
     R.cluster.sync();
-    best = 0;
-    for (int c = 0; c < R.ctas; ++c) {
-        const uint64_t b = *R.cluster.map_shared_rank(&S.best, c);
-        best = b > best ? b : best;
-        odd |= *R.cluster.map_shared_rank(&S.odd, c);
+    R.gather(&S.best[0], [&](int, uint64_t x) { best = x > best ? x : best; });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t t = __shfl_xor_sync(kAll, best, o);
+        best = t > best ? t : best;
     }
-    const float m = best ? key_value(best) : -INFINITY;
+    odd = best == kOdd;
+    const float m = best && !odd ? key_value(best) : -INFINITY;
     const float tau = P.tau[row], u = P.u[row];
     const int top_k = P.top_k ? P.top_k[row] : 0;
     const float top_p = P.top_p ? P.top_p[row] : 1.f;
@@ -680,8 +769,13 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
         }
     } else {
         R.m = m;
+        R.top = top;
         R.weigh.m = m;
-        R.weigh.c_hi = S.c_hi, R.weigh.c_lo = S.c_lo;
+        // log2(e) / tau as two floats: the quotient, and what it left over
+        constexpr float kLog2eHigh = 1.44269502f, kLog2eLow = 1.92596299e-8f;
+        const float c = __fdiv_rn(kLog2eHigh, tau);
+        R.weigh.c_hi = fminf(c, 1e30f);
+        R.weigh.c_lo = c < 1e30f ? __fdiv_rn(fmaf(-c, tau, kLog2eHigh) + kLog2eLow, tau) : 0.f;
         R.weigh.table = __ldg(&kPowers[lane]);
         if (top_k > 0 && top_k < P.V) R.template limit_to<false>(kept, top_k, 0.f);
         if (top_p <= 0.f || min_p > 1.f)
@@ -692,9 +786,10 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
         if (min_p > 0.f) kept.least = min_p >= 1.f ? m : __double2float_ru(static_cast<double>(m) + S.drop);
         // ---- the first id at which the kept weight passes u of its total ------------------------
         const bool all = kept.border() == -INFINITY && kept.id >= P.V;
-        auto weight = [&](float z, int id, bool there) { return R.weight_if(z, there && (all || kept(z, id))); };
+        auto taken = [&](float z, int id) { return all || kept(z, id); };
+        auto weight = [&](float z, int id, bool there) { return R.weight_if(z, there && taken(z, id)); };
         uint64_t before;
-        const uint64_t total = R.publish(R.stretch_sum(kept.border(), weight), before);
+        const uint64_t total = R.publish(R.template stretch_sum<true>(kept.border(), taken), before);
         if (tid == 0) S.target = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
         __syncthreads();
         float z;
