@@ -433,6 +433,7 @@ struct Row {
         uint64_t above = 0, in_range = 0;  // tokens or weight above the range; tokens in it
         uint64_t goal = static_cast<uint64_t>(k);
         float border = -INFINITY;
+        bool few = false;  // the range may hold at most kList tokens
         uint32_t light = 0xFFFFFFFFu;  // d from which tokens only count for the total
         if (kMass) {
             border = kept.border();
@@ -444,9 +445,12 @@ struct Row {
             // k threads' largest tokens are k tokens: no token beyond the k-th of those is among the k first
             hi = range_of_top(k);
             border = nearest(hi);
+            few = k <= kList / 2;
         }
         // a level divides its range by 512: three and the first end at single distances
         for (int level = 0; level < 8; ++level) {
+            if (few && rank_range<kMass>(kept, lo, hi, above, goal)) return;
+            if (!first && hi - lo == 1) break;
             Histogram &H = S.hist[level & 1];
             const int t = static_cast<int>(threadIdx.x);
             H.count[t] = 0;
@@ -544,14 +548,10 @@ struct Row {
                 lo += bin << shift;
                 hi = min(hi, lo + (1u << shift));
             }
-            if (in_range <= kList || hi - lo == 1) break;
+            few = in_range <= kList;
             shift = 0;
             while (((hi - lo - 1) >> shift) >= kBins) ++shift;
             __syncthreads();
-        }
-        if (in_range <= kList) {
-            rank_range<kMass>(kept, lo, hi, above, goal);
-            return;
         }
         // Many tokens at one distance: of one value as a rule (a bf16 row has few), which rank by id.  Distances are
         // rounded, so values far below the largest may share one: then the last value kept is found bit by bit.
@@ -609,9 +609,9 @@ struct Row {
         kept.id = S.result;
     }
 
-    // The few tokens with lo <= d < hi against one another.
+    // The tokens with lo <= d < hi against one another; false, and nothing done, if they are more than kList.
     template <bool kMass>
-    __device__ __forceinline__ void rank_range(Kept &kept, uint32_t lo, uint32_t hi, uint64_t above, uint64_t goal) {
+    __device__ __forceinline__ bool rank_range(Kept &kept, uint32_t lo, uint32_t hi, uint64_t above, uint64_t goal) {
         const int t = static_cast<int>(threadIdx.x);
         if (t == 0) S.listed = 0;
         __syncthreads();
@@ -624,8 +624,11 @@ struct Row {
         });
         cluster.sync();
         int n = 0;
+        for (int c = 0; c < ctas; ++c) n += *cluster.map_shared_rank(&S.listed, c);
+        if (n > kList) return false;
+        n = 0;
         for (int c = 0; c < ctas; ++c) {
-            const int here = min(*cluster.map_shared_rank(&S.listed, c), kList - n);
+            const int here = *cluster.map_shared_rank(&S.listed, c);
             const uint64_t *list = cluster.map_shared_rank(&S.list[0], c);
             for (int i = t; i < here; i += kSampleThreads) S.ranked[n + i] = list[i];
             n += here;
@@ -656,6 +659,7 @@ struct Row {
         kept.last = key_value(last);
         kept.id = key_id(last);
         // the next limit's histogram may use what others still read: they are past it after its own barrier
+        return true;
     }
 };
 
