@@ -8,9 +8,9 @@
 //
 // A warp takes one run (the tokens of one page, found from the slots alone: a run starts
 // where the page differs from the token before), one head, and keys or values.  Its lanes
-// hold 8 channels each, 16 bytes in and 8 bytes out, 256 / D tokens at a time; the first
-// kHold of those steps stay in registers between the search for the largest magnitude and
-// the conversion.  Bytes moved bound a prompt, the three dependent reads (slot, old scale,
+// hold 8 channels each, 16 bytes in and 8 bytes out, 256 / D tokens at a time; kHold of
+// those steps are under way together, and stay in registers between the search for the
+// largest magnitude and the conversion where the run has no more.  Bytes moved bound a prompt, the three dependent reads (slot, old scale,
 // tokens) a decoded token.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -21,7 +21,7 @@ namespace ssd {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kHold = 8;  // steps whose values stay in registers
+constexpr int kHold = 16;  // steps under way together, whose values stay in registers
 
 struct AppendParams {
     const void *x[2];  // keys, values
@@ -38,38 +38,35 @@ struct AppendParams {
 };
 
 
-template <class E, bool kVec>
-__device__ __forceinline__ void load8(const E *p, float (&v)[8]);
-
-template <>
-__device__ __forceinline__ void load8<float, true>(const float *p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16, true>(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t r[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(r[i] << 16), v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
-}
-template <>
-__device__ __forceinline__ void load8<__half, true>(const __half *p, float (&v)[8]) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t r[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r[i]));
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-    }
-}
 __device__ __forceinline__ float wide(float x) { return x; }
 __device__ __forceinline__ float wide(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float wide(__half x) { return __half2float(x); }
+
+// Eight values as they lie in memory.
+template <class E>
+struct Raw {
+    static constexpr int kWords = static_cast<int>(sizeof(E)) * 2;
+    uint32_t w[kWords];
+};
 template <class E, bool kVec>
-__device__ __forceinline__ void load8(const E *p, float (&v)[8]) {
+__device__ __forceinline__ void load8(const E *p, Raw<E> &r) {
+    if (kVec) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = wide(p[i]);
+        for (int i = 0; i < Raw<E>::kWords; i += 4) {
+            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p) + i / 4);
+            r.w[i] = a.x, r.w[i + 1] = a.y, r.w[i + 2] = a.z, r.w[i + 3] = a.w;
+        }
+    } else {
+        E *v = reinterpret_cast<E *>(r.w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = p[i];
+    }
+}
+template <class E>
+__device__ __forceinline__ void widen(const Raw<E> &r, float (&v)[8]) {
+    const E *e = reinterpret_cast<const E *>(r.w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = wide(e[i]);
 }
 
 // Largest finite magnitude; `odd` is set when a value is not finite.
@@ -80,6 +77,41 @@ __device__ __forceinline__ void magnitude(const float (&v)[8], float &amax, bool
         const bool fine = a <= 3.402823466e38f;
         odd |= !fine;
         if (fine) amax = fmaxf(amax, a);
+    }
+}
+
+// The same of values as they lie in memory.  Without their signs, halves of either kind order as whole numbers, so
+// two are compared at once; what reaches the pattern of infinity is looked at again, value by value.
+template <class E>
+__device__ __forceinline__ uint32_t infinity_bits();
+template <>
+__device__ __forceinline__ uint32_t infinity_bits<__nv_bfloat16>() {
+    return 0x7F80u;
+}
+template <>
+__device__ __forceinline__ uint32_t infinity_bits<__half>() {
+    return 0x7C00u;
+}
+template <class E, int kN>
+__device__ __forceinline__ void magnitudes(const Raw<E> (&r)[kN], float &amax, bool &odd) {
+    if constexpr (sizeof(E) == 2) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+#pragma unroll
+            for (int c = 0; c < Raw<E>::kWords; ++c) top = __vmaxu2(top, r[i].w[c] & 0x7FFF7FFFu);
+        const uint32_t most = max(top & 0xFFFFu, top >> 16);
+        if (most < infinity_bits<E>()) {
+            const uint16_t bits = static_cast<uint16_t>(most);
+            amax = fmaxf(amax, wide(*reinterpret_cast<const E *>(&bits)));
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        float v[8];
+        widen(r[i], v);
+        magnitude(v, amax, odd);
     }
 }
 
@@ -165,25 +197,26 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         uint8_t *rows = P.cache[what] + ((block << P.page_shift) * D);
         const E *xt = x + t * stride + static_cast<int64_t>(h) * D + ch;
 
-        float hold[kHold][8];
+        // kSteps steps of tokens from k0 on; those beyond the run are zero
+        constexpr int kSteps = sizeof(E) == 4 ? kHold / 2 : kHold;
+        Raw<E> hold[kSteps];
+        auto fetch = [&](int k0) {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int k = k0 + i * kStep + sub;
+                if (k < n) {
+                    load8<E, kVec>(xt + k * stride, hold[i]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < Raw<E>::kWords; ++c) hold[i].w[c] = 0u;
+                }
+            }
+        };
         float amax = 0.f;
         bool odd = false;
-#pragma unroll
-        for (int i = 0; i < kHold; ++i) {
-            const int k = i * kStep + sub;
-            if (k < n) {
-                load8<E, kVec>(xt + k * stride, hold[i]);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) hold[i][c] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kHold; ++i) magnitude(hold[i], amax, odd);
-        for (int k = kHold * kStep + sub; k < n; k += kStep) {
-            float v[8];
-            load8<E, kVec>(xt + k * stride, v);
-            magnitude(v, amax, odd);
+        for (int k0 = 0; k0 < n; k0 += kSteps * kStep) {
+            fetch(k0);
+            magnitudes(hold, amax, odd);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
@@ -210,19 +243,19 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         const bool pow2 = (__float_as_uint(scale) & 0x7FFFFFu) == 0 && scale >= 7.8e-31f;
         const float inv = pow2 ? __frcp_rn(scale) : 0.f;
         auto store = [&](int k, const float(&v)[8]) {
-            const int s = P.slots[t + k];
+            const int s = __ldg(P.slots + t + k);
             uint2 *at = reinterpret_cast<uint2 *>(rows + static_cast<int64_t>(s & page_mask) * D + ch);
             *at = pow2 ? pack8(v, inv) : pack8_div(v, scale);
         };
+        for (int k0 = 0; k0 < n; k0 += kSteps * kStep) {
+            if (n > kSteps * kStep) fetch(k0);  // else they are still there
 #pragma unroll
-        for (int i = 0; i < kHold; ++i) {
-            const int k = i * kStep + sub;
-            if (k < n) store(k, hold[i]);
-        }
-        for (int k = kHold * kStep + sub; k < n; k += kStep) {
-            float v[8];
-            load8<E, kVec>(xt + k * stride, v);
-            store(k, v);
+            for (int i = 0; i < kSteps; ++i) {
+                const int k = k0 + i * kStep + sub;
+                float v[8];
+                widen(hold[i], v);
+                if (k < n) store(k, v);
+            }
         }
         if (lane == 0 && !(scale_was == scale)) *scale_at = scale;
     }

@@ -176,28 +176,39 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             *entry = -1;
         }
     }
-    for (int t = first; t < P.cap; t += stride) {
-        int slot = -1, pos = 0;
-        if (t < tokens) {
+    // four tokens at a time, so that their searches and page reads overlap
+    constexpr int kTokens = 4;
+    bool bad_page = false;
+    for (int t0 = first; t0 < P.cap; t0 += stride * kTokens) {
+        int pos[kTokens], page[kTokens];
+        bool served[kTokens];
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+            const int t = t0 + k * stride;
+            pos[k] = 0, page[k] = -1, served[k] = false;
+            if (t >= tokens || t < t0) continue;
             const int b = first_above(cu, B, t);
-            pos = keep_sh[b] + t - (b ? cu[b - 1] : 0);
+            pos[k] = keep_sh[b] + t - (b ? cu[b - 1] : 0);
             const int held = held_sh[b];
-            if (held >= 0) {
-                const int block = pos >> P.page_shift;
-                // a page taken above is read from the ring again: its table entry may not be there yet
-                const int page =
-                    block < held ? P.block_table[static_cast<int64_t>(b) * P.max_blocks + block]
-                                 : P.ring[(static_cast<uint32_t>(head) +
-                                           static_cast<uint32_t>((b ? take[b - 1] : 0) + block - held)) % np];
-                if (page >= 0 && page < P.num_pages)
-                    slot = (page << P.page_shift) + (pos & page_mask);
-                else
-                    report(P.dev_status, SSD_DEV_BAD_PAGE);
-            }
+            if (held < 0) continue;
+            served[k] = true;
+            const int block = pos[k] >> P.page_shift;
+            // a page taken above is read from the ring again: its table entry may not be there yet
+            page[k] = block < held ? P.block_table[static_cast<int64_t>(b) * P.max_blocks + block]
+                                   : P.ring[(static_cast<uint32_t>(head) +
+                                             static_cast<uint32_t>((b ? take[b - 1] : 0) + block - held)) % np];
         }
-        P.slots[t] = slot;
-        P.positions[t] = pos;
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+            const int t = t0 + k * stride;
+            if (t >= P.cap || t < t0) continue;
+            const bool there = page[k] >= 0 && page[k] < P.num_pages;
+            bad_page |= served[k] && !there;
+            P.slots[t] = there ? (page[k] << P.page_shift) + (pos[k] & page_mask) : -1;
+            P.positions[t] = pos[k];
+        }
     }
+    if (bad_page) report(P.dev_status, SSD_DEV_BAD_PAGE);
     if (rank == 0) {
         for (int b = static_cast<int>(threadIdx.x); b < B; b += kPlanThreads) {
             P.seq_len[b] = keep_sh[b];
