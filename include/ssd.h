@@ -520,9 +520,10 @@ int ssd_kv_append(const void *k, const void *v, int dtype, int64_t k_stride, int
  * cache, NaN among them, has no effect.  A page outside the cache counts as not
  * there (SSD_DEV_BAD_PAGE).
  * Sums and the softmax are held in fp32.  The 8-bit values enter the products
- * unchanged; a query enters as the exact sum of two (bf16) or three (fp16) e4m3
- * digits next to its row's largest, and so does each softmax weight, rounded to
- * two or three of them (2^-8 and 2^-12 of the weight, as bf16 and fp16 would be).
+ * unchanged; a query enters as the sum of two (bf16) or three (fp16) e4m3 digits,
+ * exact down to 2^-9 (2^-6) of its row's largest channel and to 2^-17 of that below;
+ * a softmax weight is rounded to two or three digits (2^-8 or 2^-12 of itself, 2^-18
+ * or 2^-23 of the largest weight near it).
  * workspace: ssd_kv_workspace_size() bytes, 256-byte aligned, zero-filled before
  *   its first use and left ready by each call (not by one that reported
  *   SSD_DEV_TIMEOUT: zero it again); calls that share one must not overlap on the

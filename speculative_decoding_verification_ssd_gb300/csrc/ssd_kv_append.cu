@@ -10,8 +10,12 @@
 // where the page differs from the token before), one head, and keys or values.  Its lanes
 // hold 8 channels each, 16 bytes in and 8 bytes out, 256 / D tokens at a time; kHold of
 // those steps are under way together, and stay in registers between the search for the
-// largest magnitude and the conversion where the run has no more.  Bytes moved bound a prompt, the three dependent reads (slot, old scale,
-// tokens) a decoded token.
+// largest magnitude and the conversion where the run has no more.
+//
+// The dependent reads (slot, old scale, tokens) bound a decoded token (9 us captured into a
+// graph, LAUNCH of it an empty launch) and, with what little a warp has to do after them, a
+// prompt: 12 of 1365 tokens, 8 heads of 128 in pages of 32, take 34 us, 3.0 TB/s.  Measured:
+// 8 steps under way 54 us, 16 34; fewer registers, for more warps, gained nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -3,33 +3,48 @@
 //   s_rj = sm_scale <q_r, k8_j> ks(page j),   out_r = sum_j softmax(s_r)_j v8_j vs(page j)
 //
 // The rows r of one item are the new tokens of a sequence times the query heads that share
-// one cache head, kRows of them at most; the item's keys come in tiles of 128.
+// one cache head, 32 or 64 of them at most.
 //
-// The 8-bit values go from the cache to the tensor cores as they lie there.  What meets
-// them is made of e4m3 digits instead: x = t1 + t2 / 16 (+ t3 / 256), each digit the e4m3
-// value nearest to what is left, times 16.  Two digits hold a bf16 query exactly and three
-// an fp16 one (down to 2^-14 of the row's largest); a softmax weight is rounded to 2^-8 or
-// 2^-12 of itself, as bf16 or fp16 would round it.  The digits of a row are columns of
-// their own, so their products are summed apart in fp32 and joined with their weights.
-// So there is no conversion pass over the cache, which bounds the call.
+// The 8-bit values go from the cache to the tensor cores as they lie there: no pass converts
+// the cache, whose bytes bound the calls of few rows.  What meets them is made of e4m3
+// digits: x = t1 + t2 (+ t3), each the e4m3 value nearest to what the ones before leave.
+// * A query row is scaled by a power of two that brings its largest channel into [128, 256).
+//   Two digits then hold a bf16 channel exactly down to 2^-9 of the largest, three an fp16
+//   one down to 2^-6; smaller ones are off by 2^-17 of the largest at most.
+// * A softmax weight is scaled to 256 at most.  Two digits (bf16) round it by 2^-8 of itself,
+//   three (fp16) by 2^-12, as those types would round it; they end at 2^-18 and 2^-23 of the
+//   largest weight of the step (fp16's second and third digits are of 32 times what is left
+//   and summed apart).  A weight is taken relative to the largest of its own step of 256 (or
+//   128) keys, so that a long flat tail is not lost next to a large weight elsewhere; the
+//   steps' outputs are joined in fp32 registers under the running maximum.
 //
-// The products are taken with the long side first: S^T = K Q^T has the 128 keys as its rows
-// and rows x digits as its columns, O^T = V^T P^T the channels.  A few query rows then cost
-// a few columns, and both products read K and V in the layout that TMA leaves them in
-// (K with its channels, V with its keys as the inner index of the product).
+// The products are taken with the long side first: S^T = K Q^T has 128 keys as its rows and
+// the item's rows as its columns, O^T = V^T P^T the channels.  A few query rows then cost a
+// few columns, and both products read K and V in the layout that TMA leaves them in (K with
+// its channels, V with its keys as the inner index of the product).
 //
-// A weight is taken relative to the largest of its own tile, so that its digits' end
-// (2^-22 of that) stays below a bf16 step whatever the other tiles hold; the tiles'
-// outputs are joined in fp32 registers under the running maximum.
+// Roles of the warps of a CTA: 0-7 softmax, in two groups that take steps in turn (a thread
+// per key of each tile); 8-11 output (a thread per channel); 12 TMA; 13 MMA; 14 the queries'
+// digits; 15 the scout, which walks the items and looks up pages and scales ahead of the
+// others.  K and V pass through one ring of shared-memory slots in the order of their use;
+// S and O are double-buffered in TMEM, the weights in shared memory.  One warp issues all
+// MMAs: two warps that issued S and O apart gained 1%, and a run of them ended in a launch
+// failure that reading did not explain.
 //
-// Roles of the warps of a CTA: 0-3 softmax (a thread per key), 4-7 output (a thread per
-// channel), 8 TMA, 9 MMA, 10 the queries' digits.  K and V tiles pass through one ring of
-// shared-memory slots; S and O are double-buffered in TMEM, weights in shared memory.
+// Work split.  All steps of all items form one line, which the CTAs (one to an SM) cut into
+// equal stretches: ragged lengths and few sequences fill the GPU alike.  A CTA whose stretch
+// ends inside an item leaves a partial result (output, maximum, sum) in the workspace, and
+// the CTA that brings an item's last part joins them all.
 //
-// Work split.  All tiles of all items form one line, which the CTAs cut into equal
-// stretches: ragged lengths and few sequences fill the GPU alike.  A CTA whose stretch ends
-// inside an item leaves a partial result (output, maximum, sum) in the workspace, and the
-// CTA that brings an item's last part joins them all.
+// What bounds it (one GB300, copy rate 6764 GB/s; calls captured into graphs, L2 flushed).
+// One token a sequence: HBM (64 sequences of 8000 to 8191 keys, 8 heads of 128: 172 us, 6.2
+// TB/s; of 3 to 8191 keys 101 us, 5.3 TB/s: the shorter the items, the more of them a CTA
+// starts).  20 rows: the same (116 us, 4.7 TB/s).  36 rows and more: the softmax groups'
+// instructions (4 sequences of 90 to 131 thousand keys: 200 us, 4.5 TB/s), a sixth of them
+// for the reductions over lanes.  Measured on the way, for 64 sequences and 20 rows: loops
+// unrolled over the rows missed the instruction cache on 41% of requests (404 us, against
+// 265 rolled); a query warp that took four rows at a time held up every change of item (265,
+// against 142); 24 warps with two to each 32 keys were slower (178, against 131).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -20,10 +20,17 @@
 // on no order, a prefix and a total agree to the last bit, and the rank or id at which a
 // sum passes its limit is decided as the real numbers would, but for cases closer than
 // 2^-28 of a weight.
+//
+// Instructions bound it: some 28 for each weight, and 2 us for each cluster barrier, of
+// which a limit costs two to four.  256 rows of 128256 bf16 logits, captured into a graph with L2
+// flushed: 108 us without limits, 130 top-k, 263 top-p, 70 min-p (the tokens below the
+// limit need no weight), 126 mixed; the bytes would take 10.  Two CTAs to an SM: one loads
+// while the other computes.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <cfloat>
 
 #include "ssd_kv.h"
 #include "ssd_device.cuh"
@@ -62,8 +69,9 @@ struct SampleParams {
 struct Weigher {
     float m, c_hi, c_lo;
     uint32_t table;
-    // The weight as `value` * 2^-(27 + shift), 2^27 <= value < 2^28; false below 2^-60.
-    __device__ __forceinline__ bool parts(float z, uint32_t &value, int &shift) const {
+    // The weight as `value` * 2^-(27 + shift), 2^27 <= value < 2^28; below 2^-60, and at -inf, shift passes 59 and
+    // `value` may be anything.
+    __device__ __forceinline__ void parts(float z, uint32_t &value, int &shift) const {
         const float d = z - m;
         // what the subtraction rounded off, exact (m >= z; both finite)
         const float bb = d - z;
@@ -85,13 +93,16 @@ struct Weigher {
         const int more = __float_as_int(fmaf(rough, q, magic)) - __float_as_int(magic);
         value = base + static_cast<uint32_t>(more);
         shift = -(k >> 5);
-        return t > -60.f;
     }
+    // (value << 16) >> shift; shl and shr give 0 for counts from 32 on, so that no case is told apart.
     __device__ __forceinline__ uint64_t operator()(float z) const {
-        uint32_t value;
+        uint32_t value, high, low, small;
         int shift;
-        const bool there = parts(z, value, shift);
-        return there ? (static_cast<uint64_t>(value) << 16) >> shift : 0;
+        parts(z, value, shift);
+        asm("shr.b32 %0, %1, %2;" : "=r"(high) : "r"(value), "r"(16 + shift));
+        asm("shl.b32 %0, %1, %2;" : "=r"(low) : "r"(value), "r"(16 - shift));
+        asm("shr.b32 %0, %1, %2;" : "=r"(small) : "r"(value), "r"(shift - 16));
+        return static_cast<uint64_t>(high) << 32 | (low | small);
     }
 };
 
@@ -116,6 +127,26 @@ struct Kept {
     }
     // no value above this is left out, none below it kept
     __device__ __forceinline__ float border() const { return fmaxf(last, least); }
+};
+
+// The same for the tokens of a vector at once (and not -inf): values from `upto` on for ids up to `id`, from `after` on
+// for the rest.
+struct Bounds {
+    float upto, after;
+    int id;
+    __device__ __forceinline__ explicit Bounds(const Kept &k)
+        : upto(fmaxf(k.border(), -FLT_MAX)), after(fmaxf(fmaxf(nextafterf(k.last, INFINITY), k.least), -FLT_MAX)), id(k.id) {}
+    template <int kVec>
+    __device__ __forceinline__ uint32_t mask(const float (&z)[kVec], int first) const {
+        uint32_t a = 0, b = 0;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            a |= z[e] >= upto ? 1u << e : 0u;
+            b |= z[e] >= after ? 1u << e : 0u;
+        }
+        const uint32_t low = (1u << min(max(id - first + 1, 0), kVec)) - 1u;
+        return (a & low) | (b & ~low);
+    }
 };
 
 // Largest of a vector's values (NaN left out).
@@ -198,13 +229,18 @@ struct Row {
         const int left = P.V - first_id;
         vectors = left <= 0 ? 0 : min(P.slice, (left + kVec - 1) / kVec);
     }
+    // A vector of the slice, of -inf where it is none of the scan's.
+    __device__ __forceinline__ uint4 vector(int v, int to) const {
+        constexpr uint32_t kNone = kVec == 4 ? 0xFF800000u : 0xFF80FF80u;
+        return v < to ? slice[v] : make_uint4(kNone, kNone, kNone, kNone);
+    }
     // fn(vector, index, there) for vectors [from, to) of the slice in steps of `step`, whole warps at a time; those
     // whose largest logit is below `border` are passed over where a warp has no other.
     template <class Fn>
     __device__ __forceinline__ void scan(int from, int to, int step, int offset, float border, Fn &&fn) {
         for (int v0 = from; v0 < to; v0 += step) {
             const int v = v0 + offset;
-            const uint4 w = slice[v < to ? v : 0];
+            const uint4 w = vector(v, to);
             if (__any_sync(kAll, v < to && vector_max<D>(w) >= border)) fn(w, v, v < to);
         }
     }
@@ -227,19 +263,19 @@ struct Row {
             }
         });
     }
-    // add(z, weight, times) for the tokens of a vector that pred(z, id) takes.  Where few do, each lane goes from one
-    // of its own to the next, and the warp weighs as often as its fullest lane has any; where a warp's tokens are
-    // all one value, lane 0 adds them all at once.
-    template <class Pred, class Add>
-    __device__ __forceinline__ void weigh_vector(const uint4 &w, int v, bool in, Pred &&pred, Add &&add) {
+    // Whether a warp's tokens are all one value.
+    __device__ __forceinline__ static bool alike(const uint4 &w) {
+        const uint32_t x = __shfl_sync(kAll, w.x, 0);
+        return __all_sync(kAll, w.x == x && w.y == x && w.z == x && w.w == x && (kVec == 4 || x >> 16 == (x & 0xFFFFu)));
+    }
+    // add(z, weight, times) for the tokens of a vector in mask(z, first id), which takes none of -inf.  Where few are,
+    // each lane goes from one of its own to the next, and the warp weighs as often as its fullest lane has any; where
+    // a warp's tokens are all one value, lane 0 adds them all at once.
+    template <class Mask, class Add>
+    __device__ __forceinline__ void weigh_vector(const uint4 &w, int v, Mask &&mask_of, Add &&add) {
         float z[kVec];
         decode_vec<D>(w, z);
-        uint32_t mask = 0;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const int id = first_id + v * kVec + e;
-            mask |= (in && id < P.V && z[e] > -INFINITY && pred(z[e], id) ? 1u : 0u) << e;
-        }
+        uint32_t mask = mask_of(z, first_id + v * kVec);
         const int most = static_cast<int>(__reduce_max_sync(kAll, static_cast<uint32_t>(__popc(mask))));
         if (most == 0) return;
         if (most * 4 <= kVec * 3) {
@@ -252,19 +288,32 @@ struct Row {
             }
             return;
         }
-        const uint32_t x0 = __shfl_sync(kAll, w.x, 0);
-        const bool flat = w.x == x0 && w.y == x0 && w.z == x0 && w.w == x0 && (kVec == 4 || x0 >> 16 == (x0 & 0xFFFFu)) &&
-                          mask == (1u << kVec) - 1u;
-        if (__all_sync(kAll, flat)) {
+        if (alike(w) && __all_sync(kAll, mask == (1u << kVec) - 1u)) {
             const uint64_t weight = weigh(z[0]);
             if ((threadIdx.x & 31) == 0) add(z[0], weight * (32u * kVec), 32u * kVec);
             return;
         }
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-            const bool here = (mask >> e) & 1;
-            const uint64_t weight = weigh(here ? z[e] : m);
-            if (here) add(z[e], weight, 1u);
+            const uint64_t weight = weigh(z[e]);
+            if ((mask >> e) & 1) add(z[e], weight, 1u);
+        }
+    }
+    // add(z, weight, times) for every token of vectors [from, to): no test of any, as what lies beyond them or beyond
+    // the row is -inf, whose weight is 0.
+    template <class Add>
+    __device__ __forceinline__ void weigh_all(int from, int to, int step, int offset, Add &&add) {
+        for (int v0 = from; v0 < to; v0 += step) {
+            const uint4 w = vector(v0 + offset, to);
+            float z[kVec];
+            decode_vec<D>(w, z);
+            if (alike(w)) {
+                const uint64_t weight = weigh(z[0]);
+                if ((threadIdx.x & 31) == 0) add(z[0], weight * (32u * kVec), 32u * kVec);
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) add(z[e], weigh(z[e]), 1u);
         }
     }
     __device__ __forceinline__ uint32_t distance(float z) const { return __float_as_uint(m - z); }
@@ -302,26 +351,40 @@ struct Row {
     // The first id, in ascending order, at which the sum of weight(z, id) passes `target`; `mine` is the sum over
     // this warp's stretch of the slice (warps take consecutive stretches).  -1 in CTAs that do not hold it.
     __device__ __forceinline__ int warp_stretch() const { return (vectors + kSampleWarps - 1) / kSampleWarps; }
-    // This warp's part of the sum of weights, or (for ties) of tokens, that pred takes.
-    template <bool kWeigh, class Pred>
-    __device__ __forceinline__ uint64_t stretch_sum(float border, Pred &&pred) {
+    // This warp's part of the sum of weights that are kept.
+    __device__ __forceinline__ uint64_t kept_sum(const Kept &kept) {
+        const int n = warp_stretch(), from = static_cast<int>(threadIdx.x >> 5) * n, to = min(from + n, vectors);
+        const int lane = static_cast<int>(threadIdx.x & 31);
+        uint64_t s = 0;
+        auto add = [&](float, uint64_t weight, uint32_t) { s += weight; };
+        if (every(kept)) {
+            weigh_all(from, to, 32, lane, add);
+        } else {
+            const Bounds bounds(kept);
+            scan(from, to, 32, lane, kept.border(), [&](const uint4 &w, int v, bool) {
+                weigh_vector(w, v, [&](const float(&z)[kVec], int first) { return bounds.mask(z, first); }, add);
+            });
+        }
+        return s;
+    }
+    // This warp's part of the tokens that pred takes.
+    template <class Pred>
+    __device__ __forceinline__ uint64_t count_sum(float border, Pred &&pred) {
         const int n = warp_stretch(), from = static_cast<int>(threadIdx.x >> 5) * n, to = min(from + n, vectors);
         uint64_t s = 0;
         scan(from, to, 32, static_cast<int>(threadIdx.x & 31), border, [&](const uint4 &w, int v, bool in) {
-            if (kWeigh) {
-                weigh_vector(w, v, in, pred, [&](float, uint64_t weight, uint32_t) { s += weight; });
-            } else {
-                float z[kVec];
-                decode_vec<D>(w, z);
+            float z[kVec];
+            decode_vec<D>(w, z);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const int id = first_id + v * kVec + e;
-                    s += in && id < P.V && pred(z[e], id) ? 1 : 0;
-                }
+            for (int e = 0; e < kVec; ++e) {
+                const int id = first_id + v * kVec + e;
+                s += in && id < P.V && pred(z[e], id) ? 1 : 0;
             }
         });
         return s;
     }
+    // Whether no token is left out.
+    __device__ __forceinline__ bool every(const Kept &kept) const { return kept.border() == -INFINITY && kept.id >= P.V; }
     // Publishes the stretches' sums; returns the cluster's total, and what lies before this CTA in `before`.
     __device__ __forceinline__ uint64_t publish(uint64_t s, uint64_t &before) {
         s = warp_total(s);
@@ -467,23 +530,32 @@ struct Row {
             auto bin_of = [&](uint32_t d) { return first ? first_bin(d) : static_cast<int>((d - lo) >> shift); };
             const float from = first ? border : nearest(hi);
             if (kMass) {
-                scan(0, vectors, kSampleThreads, t, from, [&](const uint4 &w, int v, bool in) {
-                    weigh_vector(
-                        w, v, in,
-                        [&](float z, int id) {
-                            const uint32_t d = distance(z);
-                            return d >= lo && d < hi && kept(z, id);
-                        },
-                        [&](float z, uint64_t weight, uint32_t times) {
-                            const uint32_t d = distance(z);
-                            if (d >= light) {
-                                rest += weight;
-                            } else {
-                                add(bin_of(d), weight);
-                                atomicAdd(&H.count[bin_of(d)], times);
-                            }
-                        });
-                });
+                auto put = [&](float z, uint64_t weight, uint32_t times) {
+                    const uint32_t d = distance(z);
+                    if (d >= min(light, kInfinite)) {
+                        rest += weight;
+                    } else {
+                        add(bin_of(d), weight);
+                        atomicAdd(&H.count[bin_of(d)], times);
+                    }
+                };
+                if (first && every(kept)) {
+                    weigh_all(0, vectors, kSampleThreads, t, put);
+                } else {
+                    const Bounds bounds(kept);
+                    scan(0, vectors, kSampleThreads, t, from, [&](const uint4 &w, int v, bool) {
+                        weigh_vector(
+                            w, v,
+                            [&](const float(&z)[kVec], int first_of) {
+                                uint32_t mask = bounds.mask(z, first_of);
+#pragma unroll
+                                for (int e = 0; e < kVec; ++e)
+                                    if (distance(z[e]) - lo >= hi - lo) mask &= ~(1u << e);
+                                return mask;
+                            },
+                            put);
+                    });
+                }
             } else {
                 each(from, [&](float z, int, bool there) {
                     const uint32_t d = distance(z);
@@ -599,7 +671,7 @@ struct Row {
         auto is_tie = [&](float z, int id) { return z == value && (!kMass || kept(z, id)); };
         auto tie = [&](float z, int id, bool there) { return static_cast<uint64_t>(there && is_tie(z, id)); };
         uint64_t before;
-        publish(stretch_sum<false>(value, is_tie), before);
+        publish(count_sum(value, is_tie), before);
         float unused;
         const int id = locate(tie, before, ties - 1, unused);
         if (id >= 0 && (t & 31) == 0)
@@ -789,11 +861,10 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
         // w >= min_p as a least logit, rounded up to a float; the largest logit stays
         if (min_p > 0.f) kept.least = min_p >= 1.f ? m : __double2float_ru(static_cast<double>(m) + S.drop);
         // ---- the first id at which the kept weight passes u of its total ------------------------
-        const bool all = kept.border() == -INFINITY && kept.id >= P.V;
-        auto taken = [&](float z, int id) { return all || kept(z, id); };
-        auto weight = [&](float z, int id, bool there) { return R.weight_if(z, there && taken(z, id)); };
+        const bool all = R.every(kept);
+        auto weight = [&](float z, int id, bool there) { return R.weight_if(z, there && (all || kept(z, id))); };
         uint64_t before;
-        const uint64_t total = R.publish(R.template stretch_sum<true>(kept.border(), taken), before);
+        const uint64_t total = R.publish(R.kept_sum(kept), before);
         if (tid == 0) S.target = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
         __syncthreads();
         float z;

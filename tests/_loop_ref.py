@@ -151,9 +151,10 @@ def attend_bound(dtype, D, out, weight, score, largest):
     Half a step of the output's type, of the value itself.  Half a step of the softmax weights'
     (2^-8 for two e4m3 digits, 2^-12 for three), of sum p |v|.  fp32 sums of D products, whose error
     2^-24 (D + 8) of the largest sum |q k| moves a weight by as much, once for the weight and once for
-    their total.  The digits of a weight end at 2^-22 (2^-26) of the largest of its 128 keys, 128 of
-    which weigh at most 2^-15 (2^-19) of the largest value.  2^-20 of sum p |v| for the fp32 steps of
-    exp, the sums over keys and the last product."""
+    their total.  2^-15 (2^-19) of the largest value for the weights' digits that end; that is 128 digits
+    that end at 2^-22 (2^-26) of the largest weight near them, and less than the kernel's could add up to
+    (256 at 2^-18, 2^-23) if all of a step's small weights were rounded the same way.  2^-20 of sum p |v| for
+    the fp32 steps of exp, the sums over keys and the last product."""
     half, weights, floor = (2.0 ** -8, 2.0 ** -8, 2.0 ** -15) if dtype == torch.bfloat16 else \
         (2.0 ** -11, 2.0 ** -12, 2.0 ** -19)
     d = weights + 2 * (D + 8) * 2.0 ** -24 * score + 2.0 ** -20
