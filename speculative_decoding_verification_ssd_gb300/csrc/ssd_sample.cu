@@ -325,6 +325,8 @@ struct Row {
 
     // What each warp of the cluster published in word `which`, joined by op(cta, word) over the lanes of every warp:
     // no second stage in the CTA, and all the loads are under way together.
+    // Says that this thread reads no other CTA's shared memory from here on.
+    __device__ __forceinline__ void leave() { asm volatile("barrier.cluster.arrive;" ::: "memory"); }
     template <class Op>
     __device__ __forceinline__ void gather(const uint64_t *words, Op &&op) {
         const int lane = static_cast<int>(threadIdx.x & 31);
@@ -400,6 +402,8 @@ struct Row {
         before = warp_total(first);
         return warp_total(total);
     }
+    // The CTA that holds the target takes the warp's stretch that does, a vector to a thread.  The warp that finds the
+    // token returns its id, every other -1.
     template <class Weight>
     __device__ __forceinline__ int locate(Weight &&weight, uint64_t before, uint64_t target, float &value) {
         int w = 0;
@@ -409,43 +413,41 @@ struct Row {
             if (run <= target && run + s > target) break;
             run += s;
         }
-        if (w == kSampleWarps || static_cast<int>(threadIdx.x >> 5) != w) return -1;
-        const int lane = static_cast<int>(threadIdx.x & 31);
-        const int n = warp_stretch(), from = w * n, to = min(from + n, vectors);
-        for (int v0 = from; v0 < to; v0 += 32) {
-            const int v = v0 + lane;
-            float z[kVec];
-            uint64_t each_w[kVec], s = 0;
-            decode_vec<D>(slice[v < to ? v : 0], z);
+        if (w == kSampleWarps) return -1;
+        const int t = static_cast<int>(threadIdx.x), lane = t & 31;
+        const int n = warp_stretch(), v = w * n + t, to = min((w + 1) * n, vectors);
+        float z[kVec];
+        uint64_t upto = 0, x = 0;
+        if (w * n + (t & ~31) < to) {  // whole warps
+            decode_vec<D>(vector(v, to), z);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 const int id = first_id + v * kVec + e;
-                each_w[e] = weight(z[e], id, v < to && id < P.V);
-                s += each_w[e];
+                x += weight(z[e], id, v < to && id < P.V);
             }
-            uint64_t upto = s;
+            upto = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t x = __shfl_up_sync(kAll, upto, o);
-                if (lane >= o) upto += x;
+                const uint64_t y = __shfl_up_sync(kAll, upto, o);
+                if (lane >= o) upto += y;
             }
-            const uint32_t over = __ballot_sync(kAll, run + upto > target);
-            if (over) {
-                const int l = __ffs(over) - 1;
-                int id = -1;
-                float at = 0.f;
-                uint64_t x = run + upto - s;
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    x += each_w[e];
-                    if (id < 0 && x > target) id = first_id + v * kVec + e, at = z[e];
-                }
-                value = __shfl_sync(kAll, at, l);
-                return __shfl_sync(kAll, id, l);
-            }
-            run += __shfl_sync(kAll, upto, 31);
         }
-        return -1;
+        if (lane == 31) S.red[t >> 5] = upto;
+        __syncthreads();
+        for (int i = 0; i < (t >> 5); ++i) run += S.red[i];
+        const uint32_t over = __ballot_sync(kAll, run + upto > target && run + upto - x <= target);
+        if (!over) return -1;
+        int id = -1;
+        float at = 0.f;
+        x = run + upto - x;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            x += weight(z[e], first_id + v * kVec + e, v < to && first_id + v * kVec + e < P.V);
+            if (id < 0 && x > target) id = first_id + v * kVec + e, at = z[e];
+        }
+        const int l = __ffs(over) - 1;
+        value = __shfl_sync(kAll, at, l);
+        return __shfl_sync(kAll, id, l);
     }
 
     // The weight of a token that is in; all lanes of a warp call, and skip it together where none is.
@@ -510,10 +512,32 @@ struct Row {
             border = nearest(hi);
             few = k <= kList / 2;
         }
+        uint32_t low_key = 0xFFFFFFFFu, high_key = 0;  // the smallest and the largest value of the range
+        auto look_at_values = [&]() {
+            low_key = 0xFFFFFFFFu, high_key = 0;
+            each(nearest(hi), [&](float z, int id, bool there) {
+                const uint32_t d = distance(z);
+                if (there && d >= lo && d < hi && (!kMass || kept(z, id))) {
+                    const uint32_t o = ordered_bits(z);
+                    low_key = min(low_key, o), high_key = max(high_key, o);
+                }
+            });
+            low_key = __reduce_min_sync(kAll, low_key), high_key = __reduce_max_sync(kAll, high_key);
+            if ((threadIdx.x & 31) == 0) S.sums[turn][0][threadIdx.x >> 5] = low_key, S.sums[turn][1][threadIdx.x >> 5] = high_key;
+            cluster.sync();
+            gather(&S.sums[turn][0][0], [&](int, uint64_t x) { low_key = min(low_key, static_cast<uint32_t>(x)); });
+            gather(&S.sums[turn][1][0], [&](int, uint64_t x) { high_key = max(high_key, static_cast<uint32_t>(x)); });
+            low_key = __reduce_min_sync(kAll, low_key), high_key = __reduce_max_sync(kAll, high_key);
+            turn ^= 1;
+        };
         // a level divides its range by 512: three and the first end at single distances
         for (int level = 0; level < 8; ++level) {
             if (few && rank_range<kMass>(kept, lo, hi, above, goal)) return;
-            if (!first && hi - lo == 1) break;
+            // Many tokens of a narrow range: of one value as a rule (a bf16 row has few), which rank by id.
+            if (level >= 2 || (!first && hi - lo == 1)) {
+                look_at_values();
+                if (low_key == high_key || hi - lo == 1) break;
+            }
             Histogram &H = S.hist[level & 1];
             const int t = static_cast<int>(threadIdx.x);
             H.count[t] = 0;
@@ -625,24 +649,9 @@ struct Row {
             while (((hi - lo - 1) >> shift) >= kBins) ++shift;
             __syncthreads();
         }
-        // Many tokens at one distance: of one value as a rule (a bf16 row has few), which rank by id.  Distances are
-        // rounded, so values far below the largest may share one: then the last value kept is found bit by bit.
-        uint32_t low_key = 0xFFFFFFFFu, high_key = 0;
-        each(nearest(hi), [&](float z, int id, bool there) {
-            const uint32_t d = distance(z);
-            if (there && d >= lo && d < hi && (!kMass || kept(z, id))) {
-                const uint32_t o = ordered_bits(z);
-                low_key = min(low_key, o), high_key = max(high_key, o);
-            }
-        });
-        low_key = __reduce_min_sync(kAll, low_key), high_key = __reduce_max_sync(kAll, high_key);
+        // Distances are rounded, so values far below the largest may share one: then the last value kept is found bit by
+        // bit.
         const int t = static_cast<int>(threadIdx.x);
-        if ((t & 31) == 0) S.sums[turn][0][t >> 5] = low_key, S.sums[turn][1][t >> 5] = high_key;
-        cluster.sync();
-        gather(&S.sums[turn][0][0], [&](int, uint64_t x) { low_key = min(low_key, static_cast<uint32_t>(x)); });
-        gather(&S.sums[turn][1][0], [&](int, uint64_t x) { high_key = max(high_key, static_cast<uint32_t>(x)); });
-        low_key = __reduce_min_sync(kAll, low_key), high_key = __reduce_max_sync(kAll, high_key);
-        turn ^= 1;
         uint32_t key = low_key;
         if (low_key != high_key) {
             key = 0;
@@ -832,12 +841,14 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
     const Kept only{m, key_id(best), -INFINITY};
     Kept kept{-INFINITY, P.V, -INFINITY};
     if (bad) {
+        R.leave();
         if (R.rank == 0 && tid == 0) {
             report(P.dev_status, bad);
             P.tokens[row] = -1;
             if (P.prob) P.prob[row] = __int_as_float(0x7FC00000);
         }
     } else if (tau == 0.f) {
+        R.leave();
         kept = only;
         if (R.rank == 0 && tid == 0) {
             P.tokens[row] = only.id;
@@ -865,11 +876,12 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
         auto weight = [&](float z, int id, bool there) { return R.weight_if(z, there && (all || kept(z, id))); };
         uint64_t before;
         const uint64_t total = R.publish(R.kept_sum(kept), before);
+        R.leave();
         if (tid == 0) S.target = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
         __syncthreads();
         float z;
         const int token = R.locate(weight, before, S.target, z);
-        if (token >= 0) {  // one warp of the cluster
+        if (token >= 0) {
             uint32_t value;
             int shift;
             R.weigh.parts(z, value, shift);
@@ -913,7 +925,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
             }
         }
     }
-    R.cluster.sync();  // no CTA leaves while another reads its shared memory
+    asm volatile("barrier.cluster.wait;" ::: "memory");  // no CTA leaves while another reads its shared memory
 }
 
 constexpr size_t kFixedBytes = (sizeof(Shared) + 15) / 16 * 16;
