@@ -581,12 +581,16 @@ struct Row {
                     });
                 }
             } else {
-                each(from, [&](float z, int, bool there) {
-                    const uint32_t d = distance(z);
-                    const bool in = there && d >= lo && d < hi;
-                    const uint32_t d0 = __shfl_sync(kAll, d, 0);
-                    const bool alike = __all_sync(kAll, in && d == d0);  // constant rows
-                    if (alike ? (t & 31) == 0 : in) atomicAdd(&H.count[bin_of(d)], alike ? 32u : 1u);
+                // what lies beyond the row counts as -inf, and ranks behind the row's own by its ids
+                scan(0, vectors, kSampleThreads, t, from, [&](const uint4 &w, int, bool) {
+                    float z[kVec];
+                    decode_vec<D>(w, z);
+                    const bool flat = alike(w);  // constant rows
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) {
+                        const uint32_t d = distance(z[e]);
+                        if (d - lo < hi - lo && (!flat || (t & 31) == 0)) atomicAdd(&H.count[bin_of(d)], flat ? 32u : 1u);
+                    }
                 });
             }
             if (kMass && first && light != 0xFFFFFFFFu) {
