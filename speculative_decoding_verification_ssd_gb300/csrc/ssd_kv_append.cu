@@ -13,9 +13,9 @@
 // largest magnitude and the conversion where the run has no more.
 //
 // The dependent reads (slot, old scale, tokens) bound a decoded token (9 us captured into a
-// graph, LAUNCH of it an empty launch) and, with what little a warp has to do after them, a
-// prompt: 12 of 1365 tokens, 8 heads of 128 in pages of 32, take 34 us, 3.0 TB/s.  Measured:
-// 8 steps under way 54 us, 16 34; fewer registers, for more warps, gained nothing.
+// graph, 7 of it an empty launch) and, with what little a warp has to do after them, a
+// prompt: 12 of 1365 tokens, 8 heads of 128 in pages of 32, take 33 us, 3.0 TB/s.  Measured:
+// 8 steps under way 54 us, 16 33; fewer registers, for more warps, gained nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -37,9 +37,9 @@
 // the CTA that brings an item's last part joins them all.
 //
 // What bounds it (one GB300, copy rate 6764 GB/s; calls captured into graphs, L2 flushed).
-// One token a sequence: HBM (64 sequences of 8000 to 8191 keys, 8 heads of 128: 172 us, 6.2
-// TB/s; of 3 to 8191 keys 101 us, 5.3 TB/s: the shorter the items, the more of them a CTA
-// starts).  20 rows: the same (116 us, 4.7 TB/s).  36 rows and more: the softmax groups'
+// One token a sequence: HBM (64 sequences of 8000 to 8191 keys, 8 heads of 128: 171 us, 6.2
+// TB/s; of 3 to 8191 keys 99 us, 5.4 TB/s: the shorter the items, the more of them a CTA
+// starts).  20 rows: the same (115 us, 4.7 TB/s).  36 rows and more: the softmax groups'
 // instructions (4 sequences of 90 to 131 thousand keys: 200 us, 4.5 TB/s), a sixth of them
 // for the reductions over lanes.  Measured on the way, for 64 sequences and 20 rows: loops
 // unrolled over the rows missed the instruction cache on 41% of requests (404 us, against

@@ -12,7 +12,7 @@
 // search in those sums.  The bytes are few (a batch of 256 moves 20 KB), so latency
 // bounds the call: one launch, every CTA of one cluster computing the same sums from
 // shared memory instead of waiting for one that does.  Captured into a graph, 256 requests
-// of 5 tokens take 13 us and 48 of up to 2700 tokens 21, of which an empty launch is LAUNCH.
+// of 5 tokens take 13 us and 48 of up to 2700 tokens 21, of which an empty launch is 7.
 #include <cooperative_groups.h>
 
 #include "ssd_kv.h"
