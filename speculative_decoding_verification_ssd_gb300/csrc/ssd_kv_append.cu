@@ -12,10 +12,14 @@
 // those steps are under way together, and stay in registers between the search for the
 // largest magnitude and the conversion where the run has no more.
 //
-// The dependent reads (slot, old scale, tokens) bound a decoded token (9 us captured into a
-// graph, 7 of it an empty launch) and, with what little a warp has to do after them, a
-// prompt: 12 of 1365 tokens, 8 heads of 128 in pages of 32, take 33 us, 3.0 TB/s.  Measured:
-// 8 steps under way 54 us, 16 33; fewer registers, for more warps, gained nothing.
+// What bounds it is the chain of dependent reads (slots, then the old scale and the tokens
+// together), a decoded token's (8 us captured into a graph with L2 flushed, 7 of it an empty
+// launch) and, four waves of warps after one another, a prompt's: 12 of 1365 tokens, 8 heads
+// of 128 in pages of 32, take 25 us, 4.0 TB/s.  Hence one look at 32 slots by the lanes names
+// a run's start, page and, as a rule, end.  Measured, for that prompt: the end looked for
+// in a second read, before any token's, 32 us; 8 steps under way 54, 16 33; CTAs of 2, 4, 8
+// and 16 warps 35, 32, 33 and 35; CTAs that stay and take chunk after chunk 27 (54, against
+// 35, in pages of 128, where few chunks start a run).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -24,8 +28,9 @@
 namespace ssd {
 namespace {
 
-constexpr int kAppendThreads = 256;
-constexpr int kHold = 16;  // steps under way together, whose values stay in registers
+constexpr int kAppendThreads = 128;
+constexpr int kAppendCtas = 4;  // to an SM, which leaves a thread the registers of its steps
+constexpr int kHold = 16;       // steps under way together, whose values stay in registers
 
 struct AppendParams {
     const void *x[2];  // keys, values
@@ -143,58 +148,38 @@ __device__ __forceinline__ uint2 pack8_div(const float (&v)[8], float scale) {
 }
 
 template <class E, int D, bool kVec>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams P) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(const __grid_constant__ AppendParams P) {
     constexpr int kLanes = D / 8;          // lanes of one token
     constexpr int kStep = 32 / kLanes;     // tokens of one step
     const int lane = threadIdx.x & 31;
     const int sub = lane / kLanes, ch = (lane % kLanes) * 8;
+    const int chunk = 1 << P.chunk_shift;
+    const int64_t cache_rows = static_cast<int64_t>(P.num_pages) << P.page_shift;
+    const int page_mask = (1 << P.page_shift) - 1;
+
     const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
     if (unit >= P.units) return;
     const int what = static_cast<int>(unit & 1);
-    const int64_t rest = unit >> 1;
-    const int h = static_cast<int>(rest % P.H);
-    const int64_t t0 = (rest / P.H) << P.chunk_shift;
-    const int chunk = 1 << P.chunk_shift;
+    const int64_t rest = unit >> 1, at = rest / P.H;
+    const int h = static_cast<int>(rest - at * P.H);
+    const int64_t t0 = at << P.chunk_shift;
     const E *x = static_cast<const E *>(P.x[what]);
     const int64_t stride = P.stride[what];
-    const int64_t cache_rows = static_cast<int64_t>(P.num_pages) << P.page_shift;
 
-    // page of each token of the chunk (one per lane), -1 for a slot that is skipped
-    const int64_t tl = t0 + lane;
-    int page = -1, before = -2;
-    if (lane < chunk && tl < P.T) {
-        const int slot = P.slots[tl];
-        if (slot >= cache_rows) report(P.dev_status, SSD_DEV_BAD_PAGE);
-        page = slot >= 0 && slot < cache_rows ? slot >> P.page_shift : -1;
-        if (tl > 0) {
-            const int s = P.slots[tl - 1];
-            before = s >= 0 && s < cache_rows ? s >> P.page_shift : -1;
-        }
-    }
-    uint32_t starts = __ballot_sync(0xFFFFFFFFu, page >= 0 && page != before);
+    // the chunk's tokens and those after it, one per lane: the page of each, -1 for a slot that is skipped
+    auto page_of = [&](int slot) { return slot >= 0 && slot < cache_rows ? slot >> P.page_shift : -1; };
+    const int slot = t0 + lane < P.T ? P.slots[t0 + lane] : -1;
+    int before = lane == 0 && t0 > 0 ? P.slots[t0 - 1] : -1;
+    if (slot >= cache_rows) report(P.dev_status, SSD_DEV_BAD_PAGE);
+    const int page = page_of(slot), up = __shfl_up_sync(0xFFFFFFFFu, slot, 1);
+    if (lane > 0) before = up;
+    uint32_t starts = __ballot_sync(0xFFFFFFFFu, lane < chunk && page >= 0 && page != page_of(before));
     while (starts) {
         const int leader = __ffs(starts) - 1;
         starts &= starts - 1;
         const int64_t t = t0 + leader;
         const int p = __shfl_sync(0xFFFFFFFFu, page, leader);
-        // length of the run: tokens from t on with the same page
-        int n = 0;
-        for (;;) {
-            const int64_t tt = t + n + lane;
-            int same = 0;
-            if (tt < P.T) {
-                const int s = P.slots[tt];
-                same = s >= 0 && s < cache_rows && (s >> P.page_shift) == p;
-            }
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, same);
-            if (m != 0xFFFFFFFFu) {
-                n += __ffs(~m) - 1;
-                break;
-            }
-            n += 32;
-        }
-        const int page_mask = (1 << P.page_shift) - 1;
-        const int row0 = P.slots[t] & page_mask;
+        const int row0 = __shfl_sync(0xFFFFFFFFu, slot, leader) & page_mask;
         const int64_t block = static_cast<int64_t>(p) * P.H + h;
         float *scale_at = P.scale[what] + block;
         const float scale_was = *scale_at;
@@ -204,11 +189,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         // kSteps steps of tokens from k0 on; those beyond the run are zero
         constexpr int kSteps = sizeof(E) == 4 ? kHold / 2 : kHold;
         Raw<E> hold[kSteps];
-        auto fetch = [&](int k0) {
+        auto fetch = [&](int k0, int end) {
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
                 const int k = k0 + i * kStep + sub;
-                if (k < n) {
+                if (k < end) {
                     load8<E, kVec>(xt + k * stride, hold[i]);
                 } else {
 #pragma unroll
@@ -216,10 +201,31 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                 }
             }
         };
+        // Length of the run: tokens from t on with the same page.  Where it passes what the lanes see, the first steps
+        // go up to the page's last row, which ends a run whose slots ascend, and are on their way while the rest is
+        // looked up.
+        const uint32_t differ = ~(__ballot_sync(0xFFFFFFFFu, page == p) >> leader);
+        const int seen = 32 - leader;
+        int n = differ ? __ffs(differ) - 1 : 32;
+        int end = n;
+        if (n == seen) end = max(seen, static_cast<int>(min(static_cast<int64_t>(page_mask + 1 - row0), P.T - t)));
+        fetch(0, end);
+        if (n == seen) {
+            for (;;) {
+                const int64_t tt = t + n + lane;
+                const uint32_t m = __ballot_sync(0xFFFFFFFFu, tt < P.T && page_of(P.slots[tt]) == p);
+                if (m != 0xFFFFFFFFu) {
+                    n += __ffs(~m) - 1;
+                    break;
+                }
+                n += 32;
+            }
+            if (n != end && min(n, end) < kSteps * kStep) fetch(0, n);
+        }
         float amax = 0.f;
         bool odd = false;
         for (int k0 = 0; k0 < n; k0 += kSteps * kStep) {
-            fetch(k0);
+            if (k0 > 0) fetch(k0, n);
             magnitudes(hold, amax, odd);
         }
 #pragma unroll
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             *at = pow2 ? pack8(v, inv) : pack8_div(v, scale);
         };
         for (int k0 = 0; k0 < n; k0 += kSteps * kStep) {
-            if (n > kSteps * kStep) fetch(k0);  // else they are still there
+            if (n > kSteps * kStep) fetch(k0, n);  // else they are still there
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
                 const int k = k0 + i * kStep + sub;
