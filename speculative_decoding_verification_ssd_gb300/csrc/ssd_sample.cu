@@ -179,7 +179,8 @@ __device__ __forceinline__ bool vector_nan<BF16Tag>(const uint4 &w) {
 }
 
 struct Histogram {
-    uint32_t count[kBins], low[kBins], high[kBins];  // weights: 64 bits in two words
+    uint32_t count[kBins];
+    uint2 mass[kBins];  // weights: 64 bits in two words
 };
 
 struct Shared {
@@ -188,7 +189,9 @@ struct Shared {
     uint64_t ranked[kList];  // the cluster's
     uint64_t ranked_weight[kList];
     uint64_t sums[2][2][kSampleWarps];  // two words of each warp, published to the cluster in turn
+    uint64_t stretches[kSampleWarps];   // sums over the warps' stretches
     uint64_t best[kSampleWarps];
+    uint64_t inbox[2][16];  // a word from each CTA of the cluster
     int listed;
     int result;
     uint64_t red[kSampleWarps];
@@ -218,7 +221,7 @@ struct Row {
     int ctas, rank, first_id;  // id of the slice's first token
     int vectors;               // of the slice
     float top = -INFINITY;     // of this thread's vectors
-    int turn = 0, published = 0;  // which of the published words is next, and which holds the stretches' sums
+    int turn = 0;  // which of the two sets of words is next
     float m;
     Weigher weigh;
 
@@ -326,14 +329,25 @@ struct Row {
 
     // What each warp of the cluster published in word `which`, joined by op(cta, word) over the lanes of every warp:
     // no second stage in the CTA, and all the loads are under way together.
-    // Says that this thread reads no other CTA's shared memory from here on.
-    __device__ __forceinline__ void leave() { asm volatile("barrier.cluster.arrive;" ::: "memory"); }
     template <class Op>
     __device__ __forceinline__ void gather(const uint64_t *words, Op &&op) {
         const int lane = static_cast<int>(threadIdx.x & 31);
 #pragma unroll 4
         for (int i = lane; i < ctas * kSampleWarps; i += 32)
             op(i / kSampleWarps, cluster.map_shared_rank(words, i / kSampleWarps)[i % kSampleWarps]);
+    }
+    // Sends this CTA's word, join() in the threads that send it, to every CTA of the cluster, and returns CTA `lane`'s (0
+    // in lanes beyond them).  What is read afterwards is at hand, and no CTA is read after the barrier, so that none
+    // has to wait for another to leave.
+    template <class Join>
+    __device__ __forceinline__ uint64_t exchange(Join &&join) {
+        const int t = static_cast<int>(threadIdx.x), lane = t & 31;
+        __syncthreads();
+        if (t < ctas) *cluster.map_shared_rank(&S.inbox[turn][rank], t) = join();
+        cluster.sync();
+        const uint64_t x = lane < ctas ? S.inbox[turn][lane] : 0;
+        turn ^= 1;
+        return x;
     }
     __device__ __forceinline__ uint64_t warp_total(uint64_t x) {
 #pragma unroll
@@ -391,17 +405,15 @@ struct Row {
     // Publishes the stretches' sums; returns the cluster's total, and what lies before this CTA in `before`.
     __device__ __forceinline__ uint64_t publish(uint64_t s, uint64_t &before) {
         s = warp_total(s);
-        if ((threadIdx.x & 31) == 0) S.sums[turn][0][threadIdx.x >> 5] = s;
-        cluster.sync();
-        uint64_t total = 0, first = 0;
-        gather(&S.sums[turn][0][0], [&](int cta, uint64_t x) {
-            total += x;
-            if (cta < rank) first += x;
+        if ((threadIdx.x & 31) == 0) S.stretches[threadIdx.x >> 5] = s;
+        const uint64_t x = exchange([&] {
+            uint64_t all = 0;
+#pragma unroll
+            for (int w = 0; w < kSampleWarps; ++w) all += S.stretches[w];
+            return all;
         });
-        published = turn;
-        turn ^= 1;
-        before = warp_total(first);
-        return warp_total(total);
+        before = warp_total(static_cast<int>(threadIdx.x & 31) < rank ? x : 0);
+        return warp_total(x);
     }
     // The CTA that holds the target takes the warp's stretch that does, a vector to a thread.  The warp that finds the
     // token returns its id, every other -1.
@@ -410,7 +422,7 @@ struct Row {
         int w = 0;
         uint64_t run = before;
         for (; w < kSampleWarps; ++w) {
-            const uint64_t s = S.sums[published][0][w];
+            const uint64_t s = S.stretches[w];
             if (run <= target && run + s > target) break;
             run += s;
         }
@@ -459,22 +471,29 @@ struct Row {
         return in ? x : 0;
     }
 
-    __device__ __forceinline__ static int first_bin(uint32_t d) {
-        return min(max((static_cast<int>(d - kNear) >> kFirstShift) + 1, 0), kBins - 1);
-    }
-    __device__ __forceinline__ static uint32_t first_end(uint32_t bin) {
-        return bin == 0 ? kNear : (bin == kBins - 1 ? kInfinite + 1 : kNear + (bin << kFirstShift));
-    }
+    // The first histogram: `shift` bits of d to a range from `near` on, what is nearer and what is farther in one range
+    // each.
+    struct First {
+        uint32_t near = kNear, shift = kFirstShift;
+        __device__ __forceinline__ int bin(uint32_t d) const {
+            return min(max((static_cast<int>(d - near) >> shift) + 1, 0), kBins - 1);
+        }
+        __device__ __forceinline__ uint32_t start(uint32_t bin) const {  // `near` may lie below 0
+            return bin == 0 ? 0 : static_cast<uint32_t>(max(static_cast<int>(near + ((bin - 1) << shift)), 0));
+        }
+        __device__ __forceinline__ uint32_t end(uint32_t bin) const { return bin == kBins - 1 ? kInfinite + 1 : near + (bin << shift); }
+    };
     // A range of d, from 0 on, that holds the largest tokens of at least k threads (k at most the cluster's threads).
     __device__ __forceinline__ uint32_t range_of_top(int k) {
         Histogram &H = S.hist[1];
         const int t = static_cast<int>(threadIdx.x);
         H.count[t] = 0;
         __syncthreads();
-        atomicAdd(&H.count[first_bin(distance(top))], 1u);
+        const First F;
+        atomicAdd(&H.count[F.bin(distance(top))], 1u);
         cluster.sync();
         uint32_t count = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int c = 0; c < ctas; ++c) count += cluster.map_shared_rank(&H, c)->count[t];
         uint32_t upto = count;
 #pragma unroll
@@ -487,7 +506,7 @@ struct Row {
         for (int w = 0; w < (t >> 5); ++w) upto += static_cast<uint32_t>(S.red[w]);
         if (upto - count < static_cast<uint32_t>(k) && upto >= static_cast<uint32_t>(k)) S.found_bin = static_cast<uint32_t>(t);
         __syncthreads();
-        return first_end(S.found_bin);
+        return F.end(S.found_bin);
     }
 
     // Narrows `kept` to the ranks that a limit leaves.  kMass: while the weight above a rank is below `share` of
@@ -499,6 +518,7 @@ struct Row {
         uint64_t above = 0, in_range = 0;  // tokens or weight above the range; tokens in it
         uint64_t goal = static_cast<uint64_t>(k);
         float border = -INFINITY;
+        First F;
         bool few = false;  // the range may hold at most kList tokens
         uint32_t light = 0xFFFFFFFFu;  // d from which tokens only count for the total
         if (kMass) {
@@ -506,7 +526,13 @@ struct Row {
             // What lies beyond tau ln(V / (1 - share)) weighs less than 1 - share of the largest alone, so the border
             // comes before it.  (Beyond the histogram's evenly divided part nothing is left out.)
             const float d = 1.0001f / weigh.c_hi * log2f(static_cast<float>(P.V) / (1.f - share));
-            if (d < 1000.f) light = __float_as_uint(d);
+            if (d < 1000.f) {
+                light = __float_as_uint(d);
+                // 128 ranges for each power of two up to there: the tokens are many where the distances are large, and
+                // atomics on one range wait for one another
+                F.shift = kFirstShift - 2;
+                F.near = light - ((kBins - 2) << F.shift);
+            }
         } else if (k <= ctas * kSampleThreads) {
             // k threads' largest tokens are k tokens: no token beyond the k-th of those is among the k first
             hi = range_of_top(k);
@@ -542,17 +568,17 @@ struct Row {
             Histogram &H = S.hist[level & 1];
             const int t = static_cast<int>(threadIdx.x);
             H.count[t] = 0;
-            if (kMass) H.low[t] = H.high[t] = 0;
+            if (kMass) H.mass[t] = make_uint2(0, 0);
             __syncthreads();
             uint64_t rest = 0;
             auto add = [&](int bin, uint64_t w) {
                 const uint32_t part = static_cast<uint32_t>(w);
-                const uint32_t was = atomicAdd(&H.low[bin], part);
+                const uint32_t was = atomicAdd(&H.mass[bin].x, part);
                 const uint32_t carry = was + part < was ? 1u : 0u;
                 const uint32_t more = static_cast<uint32_t>(w >> 32) + carry;
-                if (more) atomicAdd(&H.high[bin], more);
+                if (more) atomicAdd(&H.mass[bin].y, more);
             };
-            auto bin_of = [&](uint32_t d) { return first ? first_bin(d) : static_cast<int>((d - lo) >> shift); };
+            auto bin_of = [&](uint32_t d) { return first ? F.bin(d) : static_cast<int>((d - lo) >> shift); };
             const float from = first ? border : nearest(hi);
             if (kMass) {
                 auto put = [&](float z, uint64_t weight, uint32_t times) {
@@ -602,11 +628,14 @@ struct Row {
             // every CTA adds up all histograms: thread t bin t
             uint32_t count = 0;
             uint64_t mass = 0;
-#pragma unroll 4
+#pragma unroll 8
             for (int c = 0; c < ctas; ++c) {
                 const Histogram *h = cluster.map_shared_rank(&H, c);
                 count += h->count[t];
-                if (kMass) mass += (static_cast<uint64_t>(h->high[t]) << 32) + h->low[t];
+                if (kMass) {
+                    const uint2 w = h->mass[t];
+                    mass += (static_cast<uint64_t>(w.y) << 32) + w.x;
+                }
             }
             const uint64_t mine = kMass ? mass : count;
             uint64_t upto = mine;
@@ -641,8 +670,8 @@ struct Row {
             above = S.found_above;
             in_range = S.found_in;
             if (first) {
-                lo = bin == 0 ? 0 : kNear + ((bin - 1) << kFirstShift);
-                hi = min(min(hi, first_end(bin)), light);
+                lo = F.start(bin);
+                hi = min(min(hi, F.end(bin)), light);
                 first = false;
                 light = 0xFFFFFFFFu;
             } else {
@@ -708,17 +737,20 @@ struct Row {
                 if (at < kList) S.list[at] = make_key(z, id);
             }
         });
-        cluster.sync();
-        int n = 0;
-        for (int c = 0; c < ctas; ++c) n += *cluster.map_shared_rank(&S.listed, c);
-        if (n > kList) return false;
-        n = 0;
-        for (int c = 0; c < ctas; ++c) {
-            const int here = *cluster.map_shared_rank(&S.listed, c);
-            const uint64_t *list = cluster.map_shared_rank(&S.list[0], c);
-            for (int i = t; i < here; i += kSampleThreads) S.ranked[n + i] = list[i];
-            n += here;
+        // how many each CTA has, and how many the CTAs before it
+        const uint32_t here = static_cast<uint32_t>(exchange([&] { return static_cast<uint64_t>(S.listed); }));
+        uint32_t upto = here;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(kAll, upto, o);
+            if ((t & 31) >= o) upto += x;
         }
+        const int n = static_cast<int>(__shfl_sync(kAll, upto, 31));
+        if (n > kList) return false;
+        int cta = 0;  // that holds number t
+        for (int c = 0; c < ctas; ++c) cta += t >= static_cast<int>(__shfl_sync(kAll, upto, c)) ? 1 : 0;
+        const int at = t - static_cast<int>(__shfl_sync(kAll, upto - here, cta & 31));
+        if (t < n) S.ranked[t] = cluster.map_shared_rank(&S.list[0], cta)[at];
         __syncthreads();
         const uint64_t own = t < n ? S.ranked[t] : 0;
         if (kMass && t < kList) {
@@ -756,6 +788,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
     uint4 *slice = reinterpret_cast<uint4 *>(raw + (sizeof(Shared) + 15) / 16 * 16);
     constexpr int kVec = D::kVec;
     Row<D> R(P, S, slice);
+    asm volatile("barrier.cluster.arrive;" ::: "memory");
     const int row = static_cast<int>(blockIdx.x) / R.ctas, tid = threadIdx.x, lane = tid & 31;
     const int64_t at = static_cast<int64_t>(row) * P.ld;
 
@@ -825,8 +858,13 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
         const float least = P.min_p[row];
         if (least > 0.f) S.drop = static_cast<double>(P.tau[row]) * log(static_cast<double>(least));
     }
-    R.cluster.sync();
-    R.gather(&S.best[0], [&](int, uint64_t x) { best = x > best ? x : best; });
+    asm volatile("barrier.cluster.wait;" ::: "memory");  // every CTA has started: it can be written to
+    best = R.exchange([&] {
+        uint64_t most = 0;
+#pragma unroll
+        for (int w = 0; w < kSampleWarps; ++w) most = S.best[w] > most ? S.best[w] : most;
+        return most;
+    });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const uint64_t t = __shfl_xor_sync(kAll, best, o);
@@ -846,14 +884,12 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
     const Kept only{m, key_id(best), -INFINITY};
     Kept kept{-INFINITY, P.V, -INFINITY};
     if (bad) {
-        R.leave();
         if (R.rank == 0 && tid == 0) {
             report(P.dev_status, bad);
             P.tokens[row] = -1;
             if (P.prob) P.prob[row] = __int_as_float(0x7FC00000);
         }
     } else if (tau == 0.f) {
-        R.leave();
         kept = only;
         if (R.rank == 0 && tid == 0) {
             P.tokens[row] = only.id;
@@ -881,7 +917,6 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
         auto weight = [&](float z, int id, bool there) { return R.weight_if(z, there && (all || kept(z, id))); };
         uint64_t before;
         const uint64_t total = R.publish(R.kept_sum(kept), before);
-        R.leave();
         if (tid == 0) S.target = static_cast<uint64_t>(static_cast<double>(u) * static_cast<double>(total));
         __syncthreads();
         float z;
@@ -930,7 +965,6 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
             }
         }
     }
-    asm volatile("barrier.cluster.wait;" ::: "memory");  // no CTA leaves while another reads its shared memory
 }
 
 constexpr size_t kFixedBytes = (sizeof(Shared) + 15) / 16 * 16;
