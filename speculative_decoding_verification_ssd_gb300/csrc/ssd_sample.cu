@@ -23,8 +23,8 @@
 //
 // What bounds it: some 35 instructions for each weight, and 1 to 2 us for each cluster
 // barrier, of which a limit takes two to four.  256 rows of 128256 bf16 logits, captured into
-// a graph with L2 flushed: 94 us without limits, 112 top-k, 210 top-p, 66 min-p (the tokens
-// below the limit need no weight), 113 mixed; the bytes would take 10.  Two CTAs to an SM: one
+// a graph with L2 flushed: 93 us without limits, 107 top-k, 198 top-p, 65 min-p (the tokens
+// below the limit need no weight), 109 mixed; the bytes would take 10.  Two CTAs to an SM: one
 // computes while the other waits.  Clusters of 8, three CTAs to an SM and CTAs of 1024
 // threads were all slower.
 #include <cooperative_groups.h>
