@@ -14,7 +14,7 @@
 //
 // Weights.  w = exp((z - m) / tau) = 2^t, t = d * c with d = z - m and c = log2(e) / tau
 // both carried as two floats, so that t is exact to about 2^-45 of itself.  t is split
-// into k / 32 + g: a 32-entry table of 2^(i/32) (one entry per lane, read by shuffle) times
+// into k / 32 + g, g to 2^-31: a 32-entry table of 2^(i/32) (one entry per lane, read by shuffle) times
 // a polynomial of 2^g - 1, |g| <= 1/64, gives 28 significant bits, which are shifted into
 // 64-bit fixed point with 43 bits after the point.  Sums of those are exact: they depend
 // on no order, a prefix and a total agree to the last bit, and the rank or id at which a
@@ -23,8 +23,8 @@
 //
 // What bounds it: some 35 instructions for each weight, and 1 to 2 us for each cluster
 // barrier, of which a limit takes two to four.  256 rows of 128256 bf16 logits, captured into
-// a graph with L2 flushed: 93 us without limits, 107 top-k, 198 top-p, 65 min-p (the tokens
-// below the limit need no weight), 109 mixed; the bytes would take 10.  Two CTAs to an SM: one
+// a graph with L2 flushed: 88 us without limits, 106 top-k, 196 top-p, 65 min-p (the tokens
+// below the limit need no weight), 106 mixed; the bytes would take 10.  Two CTAs to an SM: one
 // computes while the other waits.  Clusters of 8, three CTAs to an SM and CTAs of 1024
 // threads were all slower.
 #include <cooperative_groups.h>
@@ -77,13 +77,12 @@ struct Weigher {
         // what the subtraction rounded off, exact (m >= z; both finite)
         const float bb = d - z;
         const float err = (z - (d - bb)) + (-m - bb);
-        float t = d * c_hi;
-        const float t_lo = fmaf(d, c_lo, fmaf(d, c_hi, -t)) + err * c_hi;
-        t = fmaxf(t, -64.f);
-        const float magic = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the rounded value
-        const float km = fmaf(t, 32.f, magic);
-        const int k = __float_as_int(km) - __float_as_int(magic);
-        const float g = fmaf(km - magic, -0.03125f, t) + t_lo;
+        // t rounded to 1/32: `near` is so large that its last bit stands for that
+        const float near = 393216.f;  // 1.5 * 2^18
+        const float kn = fmaxf(fmaf(d, c_hi, near), near - 64.f);
+        const int k = __float_as_int(kn) - __float_as_int(near);
+        // what that leaves of t, from the product itself
+        const float g = fmaf(err, c_hi, fmaf(d, c_lo, fmaf(d, c_hi, near - kn)));
         // (2^g - 1) = g (ln2 + g (ln2^2/2 + g (ln2^3/6 + g ln2^4/24)))
         float q = fmaf(g, 0.0096181291f, 0.0555041087f);
         q = fmaf(g, q, 0.2402265070f);
@@ -91,6 +90,7 @@ struct Weigher {
         const uint32_t base = __shfl_sync(0xFFFFFFFFu, table, k & 31);
         // base as a float, cut off at 24 bits: its part of the product ends 2^-29 below
         const float rough = __uint_as_float((base >> 4) + 0x4C800000u);
+        const float magic = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the rounded value
         const int more = __float_as_int(fmaf(rough, q, magic)) - __float_as_int(magic);
         value = base + static_cast<uint32_t>(more);
         shift = -(k >> 5);
