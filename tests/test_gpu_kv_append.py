@@ -84,6 +84,16 @@ def test_append_matches_plain_form(ssd, H, P, D, runs, dtype):
     _compare(ssd, rng, N, H, P, D, _runs(rng, N, P, runs), dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [31, 32, 33, 50, 64, 65, 100])
+def test_runs_that_end_before_their_page(ssd, n, D, dtype):
+    """Runs longer than the slots looked at at once, other sequences' tokens right behind them."""
+    rng = np.random.default_rng(900 + n)
+    slots = _runs(rng, 12, 128, [(0, n), (3, n), (128 - n, n), (0, 128), (17, n), (0, 1)])
+    _compare(ssd, rng, 12, 2, 128, D, slots, dtype)
+
+
 @pytest.mark.parametrize("pad", [8, 3])  # 3: rows that no 16-byte load can take
 def test_strided_tokens(ssd, pad):
     rng = np.random.default_rng(pad)
