@@ -631,7 +631,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 if (lane % 4 == 0) sum_sh[(r0 + lane / 4) * 4 + quad] = sums[0];
 #pragma unroll
                 for (int u = 0; u < kSub; ++u) {
-                    if (odd && !plain) {  // 0 times a scale that is not finite
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[u][i] *= f[u];
+                    if (odd && !plain) {  // 0 times a scale that is not finite, for rows that do not attend to the key
 #pragma unroll 1
                         for (int i = 0; i < 8; ++i) {
                             if (there[u] && attends(P, S.row_last[item][r0 + i], key0 + u * kTile)) continue;
@@ -642,12 +644,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     }
                     uint32_t words[kDigits][2];
                     if (F::kBoth) {
-                        // Two digits hold 2^-8 of a weight, so halves (2^-11) do between: the product with the value
-                        // scale, and what is left after the first digit, which is exact.
-                        const __half2 f2 = __float2half2_rn(f[u]);
+                        // Two digits hold 2^-8 of a weight, so a half (2^-11) does for the product with the value scale,
+                        // rounded once; what is left of it after the first digit is exact.
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
-                            const __half2 w = __hmul2(__floats2half2_rn(s[u][2 * h], s[u][2 * h + 1]), f2);
+                            const __half2 w = __floats2half2_rn(s[u][2 * h], s[u][2 * h + 1]);
                             const uint32_t a = e4m3x2_of_halves(w);
                             const uint32_t back = halves_of_e4m3x2(a);
                             const uint32_t b = e4m3x2_of_halves(__hsub2(w, *reinterpret_cast<const __half2 *>(&back)));
@@ -655,8 +656,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                             words[1][h / 2] = h % 2 == 0 ? b : words[1][h / 2] | (b << 16);
                         }
                     } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) s[u][i] *= f[u];
 #pragma unroll
                         for (int g = 0; g < kDigits; ++g)
 #pragma unroll

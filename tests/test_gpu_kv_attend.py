@@ -234,3 +234,23 @@ def test_in_a_graph_and_on_another_stream(ssd):
     c.kv[0] = 700
     torch.cuda.synchronize()
     assert torch.equal(out, c.run(ssd))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("window,page", [(0, 18), (10, 17)])
+def test_a_value_scale_that_is_not_finite_stays_with_those_that_see_it(ssd, dtype, bad, window, page):
+    """Of tokens at 285 to 290 the last three see the page of positions 288 on; of those at 294 to 299, with a window of 10,
+    the first three that of 272 to 287."""
+    pairs = [(291, 6)] if window == 0 else [(300, 6)]
+    c = Case(12, pairs, 4, 2, 64, 16, dtype)
+    c.vs[c.table[0, page], 1] = bad
+    got = c.run(ssd, window=window).double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        want = ref.attend(c.q.double().numpy(), VALUES[c.k], VALUES[c.v], c.ks.astype(np.float64), c.vs.astype(np.float64),
+                          c.table, c.cu, c.kv, c.P, c.scale, window)
+        bound = ref.attend_bound(dtype, c.D, *want)
+    sees = ~np.isfinite(want[0])
+    assert sees[:, 2:].any() and not sees[:, 2:].all() and not sees[:, :2].any()
+    np.testing.assert_array_equal(~np.isfinite(got), sees)
+    assert (np.abs(got - want[0])[~sees] <= bound[~sees]).all()
