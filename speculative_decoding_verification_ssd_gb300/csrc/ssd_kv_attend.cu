@@ -1002,7 +1002,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     } else if (warp == 14) {
 // ---- the queries' digits: eight rows at a time, four lanes to a row ------------------
         constexpr int kPer = D / 4;  // channels per lane
-        const float sign = P.scale < 0.f ? -1.f : 1.f, size = fabsf(P.scale);
+        // scores of scale 0 are those of digits that are all 0
+        const float sign = P.scale < 0.f ? -1.f : (P.scale > 0.f ? 1.f : 0.f), size = P.scale == 0.f ? 1.f : fabsf(P.scale);
+        const int most = min(126, 126 + ilogbf(size));
         const int sub = lane >> 2, part_of_row = lane & 3;
         int items = 0;
         for (int it = 0;; ++it) {
@@ -1039,9 +1041,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
                     odd = (__ballot_sync(kAll, odd) >> (lane & 28)) & 15;
-                    // the largest is brought into [128, 256): k = 7 - its exponent
+                    // The largest is brought into [128, 256): k = 7 - its exponent.  Not so far that the factor of the
+                    // scores, |scale| 2^-k, falls below the normal range: masked scores are -inf before it, and have to
+                    // be so after it.
                     const int e = static_cast<int>(__float_as_uint(top) >> 23);
-                    const int k = top == 0.f ? 0 : min(134 - e, 126);
+                    const int k = top == 0.f ? 0 : min(134 - e, most);
                     const float up = sign * __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 #pragma unroll
                     for (int c0 = 0; c0 < kPer; c0 += 16) {  // one 16-byte chunk of each digit

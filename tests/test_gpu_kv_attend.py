@@ -254,3 +254,13 @@ def test_a_value_scale_that_is_not_finite_stays_with_those_that_see_it(ssd, dtyp
     assert sees[:, 2:].any() and not sees[:, 2:].all() and not sees[:, :2].any()
     np.testing.assert_array_equal(~np.isfinite(got), sees)
     assert (np.abs(got - want[0])[~sees] <= bound[~sees]).all()
+
+
+@pytest.mark.parametrize("dtype,scale,spread", [(BF, 0.0, 1.0), (FP, 0.0, 1.0), (BF, -0.0, 1.0), (BF, 1e-30, 1e-30), (BF, -1e-44, 1.0),
+                                                (FP, 1e-38, 1.0), (FP, 3e-41, 1e-3)])
+def test_scale_of_zero_and_scales_that_vanish(ssd, dtype, scale, spread):
+    """Scores of 0, or too small to matter: the mean of the values that a token attends to."""
+    c = Case(13, [(300, 6), (17, 17), (700, 1), (3, 5)], 4, 2, 64, 16, dtype, spread=spread)
+    c.scale = scale
+    c.check(ssd)
+    c.check(ssd, window=37)
