@@ -510,7 +510,7 @@ int ssd_kv_append(const void *k, const void *v, int dtype, int64_t k_stride, int
  * n attends to the positions j <= kv_len[b] - n + i, and with window > 0 only to
  * the last `window` of those.
  *   score = sm_scale * <q, k8> * k_scale,  out = sum softmax(score) * v8 * v_scale
- * sm_scale is any finite number, 0 and negative ones among them.
+ * sm_scale is any number, 0 and negative ones among them, with sm_scale * log2(e) finite.
  * q [T, Hq, D] of `dtype` (SSD_BF16 or SSD_F16), tokens q_stride elements apart,
  *   16-byte aligned with q_stride a multiple of 8; query head h reads head
  *   h / (Hq / Hkv) of the cache (Hq a multiple of Hkv).  out [T, Hq, D] dense.

@@ -1245,7 +1245,8 @@ extern "C" int ssd_kv_attend(const void *q, int dtype, int64_t q_stride, const v
     if (B < 1 || T < 0 || max_new < 1 || num_pages < 1 || max_blocks < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 ||
         window < 0 || !kv_page_size_ok(page_size) || (D != 64 && D != 128))
         return SSD_ERR_INVALID_ARG;
-    if (!(sm_scale == sm_scale) || sm_scale - sm_scale != 0.f) return SSD_ERR_INVALID_ARG;
+    const float scale = sm_scale * kLog2e;
+    if (!(scale - scale == 0.f)) return SSD_ERR_INVALID_ARG;
     if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !cu_new || !kv_len || (T > 0 && (!q || !out)))
         return SSD_ERR_INVALID_ARG;
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return SSD_ERR_INVALID_ARG;
@@ -1273,7 +1274,7 @@ extern "C" int ssd_kv_attend(const void *q, int dtype, int64_t q_stride, const v
     P.max_blocks = max_blocks;
     P.cu = cu_new, P.kv_len = kv_len;
     P.B = B, P.T = T, P.max_new = max_new < T ? max_new : T;
-    P.scale = sm_scale * kLog2e;
+    P.scale = scale;
     P.window = window;
     P.out = out;
     P.ws = static_cast<Workspace *>(workspace);

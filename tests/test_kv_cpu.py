@@ -132,3 +132,10 @@ def test_plain_sample_keeps_prefixes():
     assert ref.sample(z, 0.0, 0, 1.0, 0.0, 0.9)[0] == 1
     token, prob, _, _ = ref.sample(z, 1.0, 2, 1.0, 0.0, 0.99)
     assert token == 3 and abs(prob - 3 / 7) < 1e-12
+
+
+@pytest.mark.parametrize("scale", [2.5e38, -3e38, float("nan"), -float("inf")])
+def test_attend_refuses_a_scale_that_is_not_finite_in_base_2(ssd, scale):
+    n = ssd.lib().ssd_kv_workspace_size()
+    assert ssd.lib().ssd_kv_attend(P, ssd.SSD_BF16, 4096, P, P, P, P, 10, 16, 32, 8, 128, P, 4, P, P, 2, 3, 2, ctypes.c_float(scale), 0, P,
+                                   P, n, None, None) == ssd.SSD_ERR_INVALID_ARG
