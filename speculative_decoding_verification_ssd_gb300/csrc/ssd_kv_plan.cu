@@ -15,6 +15,8 @@
 // of 5 tokens take 13 us and 48 of up to 2700 tokens 21, of which an empty launch is 7.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "ssd_kv.h"
 
 namespace ssd {
@@ -24,6 +26,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kSumsBytes = 6 * sizeof(int32_t);  // of shared memory for each request
 
 struct PlanParams {
     int32_t *seq_len;
@@ -241,11 +244,23 @@ extern "C" int ssd_kv_plan(int32_t *seq_len, const int32_t *accept_len, const in
     const PlanParams P{seq_len,   accept_len,         new_len,     held, B,      block_table, max_blocks, ring,
                        ring_state, num_pages,          log2_of(page_size), cap,  cu_new, kv_len,      slots,      positions,
                        dev_status};
-    const size_t dyn = static_cast<size_t>(B) * 6 * sizeof(int32_t);
-    if (dyn > 48 * 1024 && cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                static_cast<int>(dyn)) != cudaSuccess) {
+    // More than 48 KB of shared memory, what the kernel has of its own among it, has to be asked for: once for each
+    // device, for the largest batch, so that no call lowers what another is about to launch with.
+    const size_t dyn = static_cast<size_t>(B) * kSumsBytes;
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
         return SSD_ERR_CUDA;
+    }
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SSD_KV_MAX_B * kSumsBytes) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return SSD_ERR_CUDA;
+        }
+        ready.fetch_or(bit, std::memory_order_relaxed);
     }
     // one CTA writes 2048 tokens in about the time that a cluster takes to meet twice
     int ctas = 1;

@@ -1,5 +1,8 @@
 """ssd_kv_plan against a plain form, request by request: whole numbers, so exact equality."""
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 
@@ -129,3 +132,21 @@ def test_a_broken_ring_serves_nobody(ssd):
                           dev_status=dev)
     assert out["slots"].tolist() == [-1, -1, -1] and st["held"].tolist() == [0, 0]
     assert int(dev) & ssd.SSD_DEV_BAD_PAGE
+
+
+def _batch(ssd, B):
+    rng = random.Random(B)
+    lens, acc, held, table, ring, head, count = _random_state(rng, B, 64, 300, B, True)
+    new = [rng.randint(0, 5) for _ in range(B)]
+    _check(ssd, lens, acc, new, held, table, ring, head, count, 64, sum(new))
+
+
+def test_batches_around_48_kb_of_sums_in_a_fresh_process(ssd):
+    """The sums of 2043 requests and the kernel's fixed shared memory pass 48 KB together: no larger batch has raised
+    the limit before."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import test_gpu_kv_plan as t, speculative_decoding_verification_ssd_gb300 as ssd\n"
+            "for B in (2042, 2043, 2048, 2049): t._batch(ssd, B)")
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([os.path.dirname(here), here]))
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
