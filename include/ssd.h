@@ -476,7 +476,7 @@ int ssd_round_host(const void *tgt, const void *drf, int dtype, int B, int K, in
  *   int32: keep + new_len, or keep when refused; slots [cap], positions [cap]
  *   int32: token i of sequence b at cu_new[b] + i has position keep + i and the
  *   slot of that position, -1 when refused; entries from cu_new[B] on are -1 and 0.
- * seq_len becomes keep.  Requires 1 <= B <= SSD_KV_MAX_B, cap >= 0,
+ * seq_len becomes keep.  Requires 1 <= B <= SSD_KV_MAX_B, 0 <= cap < 2^31 - 2^14,
  * B * max_blocks < 2^31 and num_pages * page_size < 2^31.
  */
 int ssd_kv_plan(int32_t *seq_len, const int32_t *accept_len, const int32_t *new_len, int32_t *held, int B,

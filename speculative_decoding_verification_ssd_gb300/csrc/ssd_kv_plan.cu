@@ -27,6 +27,10 @@ namespace cg = cooperative_groups;
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kSumsBytes = 6 * sizeof(int32_t);  // of shared memory for each request
+constexpr int kPlanCtas = 8;                     // at most, of one cluster
+constexpr int kTokens = 4;                       // that a thread looks up at once
+// the tokens of one turn of the whole cluster: a token's index stays in 32 bits for caps that leave room for one
+constexpr int kTurn = kPlanCtas * kPlanThreads * kTokens;
 
 struct PlanParams {
     int32_t *seq_len;
@@ -181,7 +185,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         }
     }
     // four tokens at a time, so that their searches and page reads overlap
-    constexpr int kTokens = 4;
     bool bad_page = false;
     for (int t0 = first; t0 < P.cap; t0 += stride * kTokens) {
         int pos[kTokens], page[kTokens];
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         for (int k = 0; k < kTokens; ++k) {
             const int t = t0 + k * stride;
             pos[k] = 0, page[k] = -1, served[k] = false;
-            if (t >= tokens || t < t0) continue;
+            if (t >= tokens) continue;
             const int b = first_above(cu, B, t);
             pos[k] = keep_sh[b] + t - (b ? cu[b - 1] : 0);
             const int held = held_sh[b];
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) {
             const int t = t0 + k * stride;
-            if (t >= P.cap || t < t0) continue;
+            if (t >= P.cap) continue;
             const bool there = page[k] >= 0 && page[k] < P.num_pages;
             bad_page |= served[k] && !there;
             P.slots[t] = there ? (page[k] << P.page_shift) + (pos[k] & page_mask) : -1;
@@ -237,7 +240,7 @@ extern "C" int ssd_kv_plan(int32_t *seq_len, const int32_t *accept_len, const in
         (cap > 0 && (!slots || !positions)))
         return SSD_ERR_INVALID_ARG;
     if (B < 1 || max_blocks < 1 || num_pages < 1 || cap < 0 || !kv_page_size_ok(page_size)) return SSD_ERR_INVALID_ARG;
-    if (B > SSD_KV_MAX_B || static_cast<int64_t>(B) * max_blocks > 0x7FFFFFFF ||
+    if (B > SSD_KV_MAX_B || cap > 0x7FFFFFFF - kTurn || static_cast<int64_t>(B) * max_blocks > 0x7FFFFFFF ||
         static_cast<int64_t>(num_pages) * page_size > 0x7FFFFFFF ||
         static_cast<int64_t>(max_blocks) * page_size > 0x7FFFFFFF)
         return SSD_ERR_UNSUPPORTED;
@@ -264,7 +267,7 @@ extern "C" int ssd_kv_plan(int32_t *seq_len, const int32_t *accept_len, const in
     }
     // one CTA writes 2048 tokens in about the time that a cluster takes to meet twice
     int ctas = 1;
-    while (ctas < 8 && cap > ctas * 2048) ctas *= 2;
+    while (ctas < kPlanCtas && cap > ctas * 2048) ctas *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kPlanThreads);

@@ -139,3 +139,17 @@ def test_attend_refuses_a_scale_that_is_not_finite_in_base_2(ssd, scale):
     n = ssd.lib().ssd_kv_workspace_size()
     assert ssd.lib().ssd_kv_attend(P, ssd.SSD_BF16, 4096, P, P, P, P, 10, 16, 32, 8, 128, P, 4, P, P, 2, 3, 2, ctypes.c_float(scale), 0, P,
                                    P, n, None, None) == ssd.SSD_ERR_INVALID_ARG
+
+
+def test_plan_refuses_a_cap_whose_indexes_pass_32_bits(ssd):
+    """Of a turn of 2^14 tokens a thread's index starts among the first 2^12, and goes on while it is below the cap."""
+    turn = 8 * 512 * 4
+
+    def index_at_the_end(cap):
+        last = cap - 1
+        return last - max(0, last % turn - (turn // 4 - 1)) + turn
+
+    assert index_at_the_end(2 ** 31 - turn - 1) < 2 ** 31
+    for cap in (2 ** 31 - turn + 1, 2 ** 31 - 1):
+        assert index_at_the_end(cap) >= 2 ** 31
+        assert ssd.lib().ssd_kv_plan(P, None, P, P, 4, P, 8, P, P, 100, 16, cap, P, P, P, P, None, None) == ssd.SSD_ERR_UNSUPPORTED
