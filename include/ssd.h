@@ -515,8 +515,11 @@ int ssd_kv_append(const void *k, const void *v, int dtype, int64_t k_stride, int
  *   16-byte aligned with q_stride a multiple of 8; query head h reads head
  *   h / (Hq / Hkv) of the cache (Hq a multiple of Hkv).  out [T, Hq, D] dense.
  * cu_new [B+1], kv_len [B] int32 as from ssd_kv_plan; max_new: a bound on the
- *   tokens of one sequence (a longer one counts SSD_DEV_BAD_LENGTH, its tokens
- *   beyond max_new get zeros, as does every token from cu_new[B] on).
+ *   tokens of one sequence: a longer one's tokens beyond max_new get zeros, as does
+ *   every token from cu_new[B] on.  SSD_DEV_BAD_LENGTH counts a sequence of more than
+ *   max_new tokens, a cu_new that falls, is negative or passes T (it is cut to what is
+ *   there), and a kv_len of a sequence with tokens that is negative or beyond
+ *   max_blocks pages (whose keys beyond them are left out).
  * A token that attends to nothing gets zeros.  What lies in masked places of the
  * cache, NaN among them, has no effect.  A page outside the cache counts as not
  * there (SSD_DEV_BAD_PAGE).

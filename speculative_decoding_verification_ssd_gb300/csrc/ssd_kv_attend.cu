@@ -467,9 +467,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         for (int64_t i = served * width + static_cast<int64_t>(cta) * kAttendThreads + tid; i < P.T * width; i += stride)
             out[i] = narrow<E>(0.f);
         for (int b = cta; b < P.B; b += gridDim.x) {
-            const int from = min(max(P.cu[b], 0), P.T), to = min(max(P.cu[b + 1], from), P.T);
-            if (to - from <= P.max_new) continue;
-            if (tid == 0) report(P.dev_status, SSD_DEV_BAD_LENGTH);
+            const int first = P.cu[b], next = P.cu[b + 1], keys = P.kv_len[b];
+            const int from = min(max(first, 0), P.T), to = min(max(next, from), P.T);
+            // a length counts where tokens are there to attend over it
+            const bool fits = first >= 0 && next >= first && next <= P.T &&
+                              (to == from || (keys >= 0 && keys <= P.max_blocks << P.page_shift));
+            if (tid == 0 && (!fits || to - from > P.max_new)) report(P.dev_status, SSD_DEV_BAD_LENGTH);
             for (int64_t i = (from + P.max_new) * width + tid; i < to * width; i += kAttendThreads) out[i] = narrow<E>(0.f);
         }
     }

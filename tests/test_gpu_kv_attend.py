@@ -264,3 +264,39 @@ def test_scale_of_zero_and_scales_that_vanish(ssd, dtype, scale, spread):
     c.scale = scale
     c.check(ssd)
     c.check(ssd, window=37)
+
+
+def _status(ssd, c, **kw):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.check(ssd, dev_status=status, **kw)
+    return int(status)
+
+
+@pytest.mark.parametrize("kv", [65, 70, 10 ** 9, -1, -5])
+def test_a_length_that_the_table_cannot_hold_is_reported(ssd, kv):
+    c = Case(6, [(64, 4), (50, 3)], 2, 2, 64, 16, BF)
+    assert _status(ssd, c) == 0
+    c.kv[0] = kv
+    assert _status(ssd, c) == ssd.SSD_DEV_BAD_LENGTH
+
+
+def test_the_length_of_a_sequence_without_tokens_does_not_matter(ssd):
+    c = Case(6, [(64, 4), (50, 0)], 2, 2, 64, 16, BF)
+    c.kv[1] = -7
+    assert _status(ssd, c) == 0
+
+
+def test_more_tokens_than_the_bound_are_reported(ssd):
+    assert _status(ssd, Case(6, [(64, 4), (50, 9)], 2, 2, 64, 16, BF), max_new=5) == ssd.SSD_DEV_BAD_LENGTH
+
+
+def test_token_counts_that_pass_the_queries_are_reported(ssd):
+    """cu_new beyond the T tokens of q is cut there."""
+    c = Case(6, [(64, 4), (50, 3)], 2, 2, 64, 16, BF)
+    want = c.run(ssd)
+    c.cu[2] = 9
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.kv[1] = 52          # of five tokens; three are there, and attend from the end all the same
+    got = c.run(ssd, max_new=5, dev_status=status)
+    assert int(status) == ssd.SSD_DEV_BAD_LENGTH
+    assert torch.equal(got[:4], want[:4])
