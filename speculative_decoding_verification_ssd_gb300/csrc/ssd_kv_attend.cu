@@ -1099,10 +1099,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const int common_to = low, common_from = P.window > 0 ? max(0, high + 1 - P.window) : 0;
             const int32_t *table = P.table + static_cast<int64_t>(part.b) * P.max_blocks;
             const int key0 = part.step * F::kStep;
-            auto look_up = [&](int t) {  // page of this lane's place in the steps from t on
+            // page of this lane's place in the steps from t on; -1 for what is no page, less for what is no place
+            constexpr int kNoPlace = -2;
+            auto look_up = [&](int t) {
                 const int j = key0 + (t + my_step) * F::kStep + (my_page << P.page_shift);
                 const bool in = t + my_step < part.steps && j < part.stop && j + (1 << P.page_shift) > part.start;
-                return in ? __ldg(table + (j >> P.page_shift)) : -2;
+                return in ? max(__ldg(table + (j >> P.page_shift)), -1) : kNoPlace;
             };
             int next = look_up(0);
             for (int t0 = 0; t0 < part.steps; t0 += at_once) {
@@ -1114,7 +1116,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     ks = __ldg(P.ks + block);
                     vs = __ldg(P.vs + block);
                 }
-                if (page != -2 && !there) report(P.dev_status, SSD_DEV_BAD_PAGE);
+                if (page != kNoPlace && !there) report(P.dev_status, SSD_DEV_BAD_PAGE);
                 if (t0 + at_once < part.steps) next = look_up(t0 + at_once);
                 // Value scales are divided by a power of two above the step's largest, times 256: the weights'
                 // digits start at e4m3's upper end.

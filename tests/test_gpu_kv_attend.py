@@ -300,3 +300,14 @@ def test_token_counts_that_pass_the_queries_are_reported(ssd):
     got = c.run(ssd, max_new=5, dev_status=status)
     assert int(status) == ssd.SSD_DEV_BAD_LENGTH
     assert torch.equal(got[:4], want[:4])
+
+
+@pytest.mark.parametrize("entry", [-1, -2, -3, -2 ** 31, 2 ** 31 - 1])
+def test_every_entry_outside_the_cache_is_reported(ssd, entry):
+    c = Case(5, [(200, 3)], 4, 2, 64, 16, BF)
+    c.table[0, 2] = entry
+    assert _status(ssd, c) == ssd.SSD_DEV_BAD_PAGE
+    # behind the end of the sequence it is nobody's
+    c = Case(5, [(200, 3), (300, 3)], 4, 2, 64, 16, BF)
+    c.table[0, 13:] = entry
+    assert _status(ssd, c) == 0
