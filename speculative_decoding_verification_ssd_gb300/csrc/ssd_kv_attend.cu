@@ -91,6 +91,7 @@ struct AttendParams {
     int step_shift;  // log2 of the keys of one step
     int item_cost;   // what starting an item counts in the split, in steps
     int inside;  // the schedule is made by every CTA in shared memory
+    int most_pairs;  // (sequence, row block) pairs that T tokens of B sequences can make: what the host's limits are of
     void *out;
     Workspace *ws;
     int32_t *dev_status;
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kScheduleThreads) schedule_kernel(const __grid
         if (b < P.B) blocks[b + 1] = sum;
     }
     __syncthreads();
-    const int pairs = min(carry, kMaxPairs);
+    const int pairs = min(carry, P.most_pairs);  // more only of a cu_new that falls
     Workspace &W = *P.ws;
     carry = 0;
     if (tid == 0) W.sums[0] = 0, W.pairs = pairs;
@@ -1219,7 +1220,9 @@ int attend_launch(AttendParams P, const CUtensorMap &k_map, const CUtensorMap &v
     int ctas = dev.sms;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     if (!P.inside) {
-        if (static_cast<int64_t>(P.T) * P.G / F::R + P.B > kMaxPairs) return SSD_ERR_UNSUPPORTED;
+        const int64_t most = static_cast<int64_t>(P.T) * P.G / F::R + P.B;
+        if (most > kMaxPairs) return SSD_ERR_UNSUPPORTED;
+        P.most_pairs = static_cast<int>(most);
         schedule_kernel<<<1, kScheduleThreads, 0, stream>>>(P, ctas);
         if (launched() != SSD_OK) return SSD_ERR_CUDA;
     }

@@ -311,3 +311,18 @@ def test_every_entry_outside_the_cache_is_reported(ssd, entry):
     c = Case(5, [(200, 3), (300, 3)], 4, 2, 64, 16, BF)
     c.table[0, 13:] = entry
     assert _status(ssd, c) == 0
+
+
+def test_token_counts_that_fall_are_reported_and_bounded(ssd):
+    """cu_new going back and forth would make 13 row blocks for each of 20 sequences, of tokens that make 13 in all."""
+    ws = ssd.kv_workspace()
+    good = Case(14, [(300, 200), (90, 70)], 8, 2, 64, 16, BF)
+    want = good.run(ssd, workspace=ws)
+    c = Case(14, [(300, 200)] + [(20, 0)] * 39, 8, 2, 64, 16, BF)
+    c.cu = np.array([0, 200] * 20 + [0], np.int32)
+    c.kv[:] = 300
+    c.table[:] = c.table[0]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.run(ssd, workspace=ws, dev_status=status)
+    assert int(status) == ssd.SSD_DEV_BAD_LENGTH
+    assert torch.equal(good.run(ssd, workspace=ws), want)
