@@ -1266,9 +1266,10 @@ extern "C" int ssd_kv_attend(const void *q, int dtype, int64_t q_stride, const v
         static_cast<int64_t>(B) * max_blocks > 0x7FFFFFFF || static_cast<int64_t>(max_blocks) * page_size > 0x7FFFFFFF / 2 ||
         B > SSD_KV_MAX_B)
         return SSD_ERR_UNSUPPORTED;
-    // tiles of all items, which the schedule counts in 32 bits
+    // Units of all items, which the schedule counts in 32 bits: steps of 128 or 256 keys, the last one begun, and up to
+    // two for an item's start.
     const int64_t row_blocks = static_cast<int64_t>(T < 1 ? 1 : T) * (Hq / Hkv) / 8 + B;
-    if (row_blocks * Hkv > 0x7FFFFFFF / (static_cast<int64_t>(max_blocks) * page_size / kTile + 2)) return SSD_ERR_UNSUPPORTED;
+    if (row_blocks * Hkv > 0x7FFFFFFF / (static_cast<int64_t>(max_blocks) * page_size / kTile + 3)) return SSD_ERR_UNSUPPORTED;
     if (T == 0) return SSD_OK;
     AttendParams P{};
     P.q = q;

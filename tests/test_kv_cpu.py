@@ -153,3 +153,13 @@ def test_plan_refuses_a_cap_whose_indexes_pass_32_bits(ssd):
     for cap in (2 ** 31 - turn + 1, 2 ** 31 - 1):
         assert index_at_the_end(cap) >= 2 ** 31
         assert ssd.lib().ssd_kv_plan(P, None, P, P, 4, P, 8, P, P, 100, 16, cap, P, P, P, P, None, None) == ssd.SSD_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("T,B,Hkv,blocks,page", [(8, 8, 119000000, 1, 16), (8, 8, 119000000, 1, 128), (16, 16, 70000000, 9, 16)])
+def test_attend_refuses_more_steps_than_32_bits(ssd, T, B, Hkv, blocks, page):
+    """One token each of B sequences: ceil(keys / 256) steps and two for the start, for every head."""
+    keys, n = blocks * page, ssd.lib().ssd_kv_workspace_size()
+    assert B * Hkv * (-(-keys // 256) + 2) >= 2 ** 31
+    got = ssd.lib().ssd_kv_attend(P, ssd.SSD_BF16, Hkv * 64, P, P, P, P, 1, 16, Hkv, Hkv, 64, P, blocks * page // 16, P, P, B, T, 1,
+                                  ctypes.c_float(1.0), 0, P, P, n, None, None)
+    assert got == ssd.SSD_ERR_UNSUPPORTED
