@@ -351,6 +351,7 @@ struct Shared {
     uint32_t tmem;
     int nan_met;
     int gave_up;
+    int highest;  // place in the ring of the last copy issued
     int last_part;
     int red[kAttendWarps];
 };
@@ -359,14 +360,15 @@ struct Shared {
 // more than any step takes).  When one runs out, `gave_up` is set and every role leaves its loop without
 // waiting for the others; barriers that a whole group shares are met by all of it or by none.
 constexpr int kPolls = 1 << 22;
-__device__ __forceinline__ void wait_phase(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
     int polls = 0;
     while (!mbar_try_wait(bar, parity)) {
         if (*gave_up || ++polls == kPolls) {
             *gave_up = 1;
-            break;
+            return false;
         }
     }
+    return true;
 }
 // The same for what has to end whether or not a wait ran out.
 __device__ __forceinline__ void drain_phase(uint64_t *bar, uint32_t parity) {
@@ -502,11 +504,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     if (!busy) return;
     const uint32_t tmem = S.tmem;
 
-    auto wait = [&](uint64_t *bar, int parity) { wait_phase(bar, static_cast<uint32_t>(parity), &S.gave_up); };
+    auto wait = [&](uint64_t *bar, int parity) { return wait_phase(bar, static_cast<uint32_t>(parity), &S.gave_up); };
     auto gave_up = [&] { return *static_cast<volatile int *>(&S.gave_up) != 0; };
-    auto open_step = [&](int s) -> const Step & {
-        wait(&S.step_full[s % kSteps], (s / kSteps) & 1);
-        return S.step[s % kSteps];
+    // Whether step s is there and not the end, the same for a warp's lanes.  After a wait that ran out its fields may be
+    // anything, and are not used.
+    auto open_step = [&](int s) {
+        const bool came = wait(&S.step_full[s % kSteps], (s / kSteps) & 1);
+        return !__any_sync(kAll, !came || !S.step[s % kSteps].live);
     };
     auto close_step = [&](int s) {
         __syncwarp();
@@ -528,8 +532,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const int phase = (it >> 1) & 1;
             float(&max_sh)[4][R] = S.step_max[it & 3];
             float *sum_sh = reinterpret_cast<float *>(S.step_sum[group]);
-            const Step &st = open_step(it);
-            const bool stop = !st.live;
+            const bool stop = !open_step(it);
+            const Step &st = S.step[it % kSteps];
             const int item = stop ? 0 : st.item, chunks = (st.rows + 7) >> 3;
             const float *q_factor = S.q_factor[item];
             const bool plain = st.plain, odd = st.odd;
@@ -737,8 +741,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         for (int r = 0; r < R; ++r) acc[r] = 0.f;
         for (int it = 0;; ++it) {
             const int buf = it & 1, phase = (it >> 1) & 1;
-            const Step &st = open_step(it);
-            const bool stop = !st.live;
+            const bool stop = !open_step(it);
+            const Step &st = S.step[it % kSteps];
             if (!stop) wait(&S.p_full[buf], phase);
             if (!stop && ch < st.rows) {
                 const float(&ms)[4][R] = S.step_max[it & 3];
@@ -914,8 +918,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         };
         int n = 0;
         for (;; ++n) {
-            const Step &st = open_step(n);
-            if (!st.live || __any_sync(kAll, gave_up())) break;
+            if (!open_step(n)) break;
+            const Step &st = S.step[n % kSteps];
             load(n, place_of_k(n), &k_map);
             if (n >= 2) {
                 load(n - 2, place_of_v(n - 2), &v_map);
@@ -926,9 +930,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             load(s, place_of_v(s), &v_map);
             close_step(s);
         }
-        if (gave_up())  // the copies under way still have to land before the CTA ends
-            for (int x = max(0, highest - slots + 1); x <= highest; ++x)
-                drain_phase(&S.full[x % slots], (x / slots) & 1);
+        if (lane == 0) S.highest = highest;
     } else if (warp == 13) {
         // ---- MMA ------------------------------------------------------------------------
         const uint64_t ring_k = tc::matrix_desc(ring, D), q_desc = tc::matrix_desc(q_sh, D);
@@ -963,8 +965,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         int n = 0, items = 0, subs_1 = 0, subs_2 = 0, columns_1 = 0, columns_2 = 0;
         for (;; ++n) {
             const int buf = n & 1, phase = (n >> 1) & 1;
-            const Step &st = open_step(n);
-            if (!st.live || __any_sync(kAll, gave_up())) break;
+            if (!open_step(n)) break;
+            const Step &st = S.step[n % kSteps];
             const int subs = st.subs, first = st.first, last = st.last, rows = st.rows;
             const uint32_t shape = tc::mma_shape((rows + 15) & ~15, false, false);
             const int columns = F::kBoth ? 2 * ((rows + 7) & ~7) : (rows + 15) & ~15;  // of O
@@ -998,11 +1000,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (n >= 2) output_of(n - 2, subs_2, columns_2);
             if (n >= 1) output_of(n - 1, subs_1, columns_1);
         }
-        if (__any_sync(kAll, gave_up())) {  // what was issued still has to end before the CTA does
-            if (tc::elect_one()) tc::mma_commit(&S.drained);
-            __syncwarp();
-            drain_phase(&S.drained, 0);
-        }
     } else if (warp == 14) {
 // ---- the queries' digits: eight rows at a time, four lanes to a row ------------------
         constexpr int kPer = D / 4;  // channels per lane
@@ -1012,8 +1009,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const int sub = lane >> 2, part_of_row = lane & 3;
         int items = 0;
         for (int it = 0;; ++it) {
-            const Step &st = open_step(it);
-            if (!st.live || __any_sync(kAll, gave_up())) break;
+            if (!open_step(it)) break;
+            const Step &st = S.step[it % kSteps];
             if (st.first) {
                 const int rows = st.rows, row0 = st.row0, token0 = st.token0, head0 = st.head * P.G, pos0 = st.pos0;
                 uint4 x[kPer / 8];
@@ -1181,6 +1178,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    if (gave_up()) {
+        // Some role left early, perhaps after the ones that issue copies and products had left: what they issued still
+        // has to end before the CTA does.
+        if (warp == 12) {
+            const int highest = S.highest;
+#pragma unroll 1
+            for (int x = max(0, highest - slots + 1); x <= highest; ++x) drain_phase(&S.full[x % slots], (x / slots) & 1);
+        }
+        if (warp == 13) {
+            if (tc::elect_one()) tc::mma_commit(&S.drained);
+            __syncwarp();
+            drain_phase(&S.drained, 0);
+        }
+    }
     if (warp == 13) tc::tmem_free(tmem, F::kColumns);
 }
 
