@@ -88,6 +88,7 @@ extern "C" {
 #define SSD_DEV_NO_PAGES 32   /* a request got no pages: too few are free */
 #define SSD_DEV_BAD_LENGTH 64 /* a negative length, or one beyond the table or the token buffers */
 #define SSD_DEV_BAD_PARAM 128 /* a sampling parameter or a uniform that is not a number in its range */
+#define SSD_DEV_LOW_LOGITS 256 /* a row too low for filtered logits (SSD_DROPPED_LOGIT) */
 
 /* Limits. */
 #define SSD_MAX_K 32
@@ -100,7 +101,8 @@ extern "C" {
  * logits' type).  Finite and of moderate size, so that ssd_verify and ssd_round
  * take rows that hold little else: their running sums start from such a value,
  * and its rounding has to stay far below the exponent range (temperatures from
- * 1e-4).  Its weight is 0 next to any larger logit up to temperatures of 900. */
+ * 1e-4).  Its weight is 0 next to a logit that is more than 104 temperatures above it:
+ * in rows whose largest logit is -6000 or more, up to temperatures of 900. */
 #define SSD_DROPPED_LOGIT (-1e5f)
 
 /*
@@ -559,6 +561,9 @@ int ssd_kv_attend(const void *q, int dtype, int64_t q_stride, const void *k_cach
  * temperature (SSD_DEV_BAD_TEMPERATURE), a top_p or min_p that is NaN or a uniform
  * outside [0, 1) (SSD_DEV_BAD_PARAM) gets token -1 and prob NaN; its filtered row
  * is a copy of the logits.  A -inf logit is a token of weight 0, dropped in `filtered`.
+ * A row with a token to drop whose largest logit is not more than 104 temperatures above
+ * SSD_DROPPED_LOGIT (temperatures above 900, which the filtered rows are not for, count as
+ * 900) sets SSD_DEV_LOW_LOGITS: its token is drawn as ever, its filtered row is a copy.
  * Weights are summed in 64-bit fixed point (2^-43 of the largest weight; each is
  * exact to about 2^-28 of itself), so the sums do not depend on their order.
  * Requires rows >= 1, 2 <= V <= SSD_MAX_V_F32 / SSD_MAX_V_BF16.

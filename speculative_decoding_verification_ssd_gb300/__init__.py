@@ -37,6 +37,7 @@ SSD_DEV_BAD_PAGE = 16
 SSD_DEV_NO_PAGES = 32
 SSD_DEV_BAD_LENGTH = 64
 SSD_DEV_BAD_PARAM = 128
+SSD_DEV_LOW_LOGITS = 256
 
 SSD_MAX_K = 32
 SSD_MAX_F = 256
@@ -821,7 +822,7 @@ def ssd_sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=N
     """One token per row of logits [rows, V] (rows may be a [..., :V] view of longer ones)
     under temperature, top-k, top-p and min-p: returns dict(tokens, prob[, filtered]).
     filtered: True, or a tensor of the logits' shape and strides, for the logits with every
-    dropped token at SSD_DROPPED_LOGIT."""
+    dropped token at SSD_DROPPED_LOGIT (rows too low for that are copied: SSD_DEV_LOW_LOGITS)."""
     R, V = _cuda(logits, "logits", 2)
     dt = _logit_dtype(logits)
     ld, step = logits.stride()

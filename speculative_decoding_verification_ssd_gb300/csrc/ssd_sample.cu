@@ -937,6 +937,11 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
     if (P.filtered) {
         const uint32_t dropped = kVec == 4 ? __float_as_uint(SSD_DROPPED_LOGIT)
                                            : static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16(SSD_DROPPED_LOGIT)));
+        // e^-104 is 0 in fp32: next to a largest logit that is 104 tau above it, a dropped token weighs nothing.  A row that
+        // lies lower is left as it is, and reported if a token of it had to be dropped.  (Temperatures count up to 900,
+        // where that is 93600 and any row from -6000 on fits.)
+        const bool low = !bad && !(m - __uint_as_float(kVec == 4 ? dropped : dropped << 16) > 104.f * fminf(tau, 900.f));
+        bool kept_back = false;
         for (int v = tid; v < R.vectors; v += kSampleThreads) {
             uint4 w = slice[v];
             uint32_t *words = &w.x;
@@ -946,6 +951,10 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) {
                     if (kept(z[e], R.first_id + v * kVec + e) && z[e] > -INFINITY) continue;
+                    if (low) {
+                        kept_back |= R.first_id + v * kVec + e < P.V;
+                        continue;
+                    }
                     if (kVec == 4)
                         words[e % 4] = dropped;
                     else
@@ -964,6 +973,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_con
                 }
             }
         }
+        if (kept_back) report(P.dev_status, SSD_DEV_LOW_LOGITS);
     }
 }
 

@@ -188,3 +188,39 @@ def test_filtered_rows_verify_as_the_truncated_distributions(ssd, B, V):
         n = min(a + 1, K)
         np.testing.assert_allclose(out["q_tok"].cpu().numpy()[b, :n], q[b, :n], rtol=1e-5)
         assert float(tgt[b, a, int(want["bonus"][b])]) != ssd.SSD_DROPPED_LOGIT
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_rows_too_low_for_filtered_logits_are_reported(ssd, dtype):
+    """A dropped logit has weight 0 next to one that is 104 tau above it.  Rows that lie lower keep their logits, and the status
+    says so; their tokens are drawn as ever."""
+    V = 500
+    z, rng = _rows(8, 8, V, dtype)
+    drop = float(torch.tensor(ssd.SSD_DROPPED_LOGIT).to(dtype))
+    low = (z.float() - z.float().max(dim=1, keepdim=True).values).clamp_min(-20.0) * 512 + drop    # the largest is `drop`
+    low = low.to(dtype)
+
+    def run(x, tau, k):
+        n = x.shape[0]
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        u = rng.random(n).astype(np.float32)
+        out = ssd.ssd_sample(x.cuda(), _t([tau] * n), _t(u), top_k=_t([k] * n, torch.int32), filtered=True, dev_status=status)
+        want = [ref.sample(r.double().numpy(), float(np.float32(tau)), k, 1.0, 0.0, float(v)) for r, v in zip(x, u)]
+        for t, w in zip(out["tokens"].tolist(), want):
+            assert w[3] < MARGIN or t == w[0]
+        return out["filtered"].cpu(), int(status)
+
+    for shift, tau, k in ((0.0, 300.0, 7), (-2e5, 300.0, 7), (0.0, 0.0, 0), (-1024.0, 0.0, 0), (1024.0, 20.0, 7)):
+        x = (low.float() + shift).to(dtype)
+        got, status = run(x, tau, k)
+        assert status == ssd.SSD_DEV_LOW_LOGITS, (shift, tau)
+        assert torch.equal(got, x)
+    # nothing dropped, or the largest far enough above
+    x = (low.float() - 2e5).to(dtype)
+    got, status = run(x, 300.0, 0)
+    assert status == 0 and torch.equal(got, x)
+    for shift, tau, k in ((1024.0, 0.0, 0), (1024.0, 2.0, 7), (1e5, 900.0, 7)):
+        x = (low.float() + shift).to(dtype)
+        got, status = run(x, tau, k)
+        assert status == 0, (shift, tau)
+        assert ((got == drop).sum(dim=1) >= V - max(k, 1) - 1).all()
