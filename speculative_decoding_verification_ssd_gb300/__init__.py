@@ -645,16 +645,33 @@ except AttributeError:
         return torch.cuda.current_stream(device).cuda_stream
 
 
+try:
+    _current_device = torch._C._cuda_getDevice
+except AttributeError:
+    _current_device = torch.cuda.current_device
+
+
 def _stream_at(stream, t) -> int:
     if stream is None:
         return _current_stream(t.get_device())
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        return int(stream)
+    if stream.device_index != _current_device():
+        raise ValueError(f"stream is of cuda:{stream.device_index}, the current device is cuda:{_current_device()}")
+    return stream.cuda_stream
+
+
+def _here(t, name: str):
+    """A CUDA tensor of the current device, on which the call launches."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{_current_device()}")
 
 
 def _at(t, name: str, dtype, shape) -> int:
     """Address of a contiguous CUDA tensor of that dtype and shape."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    _here(t, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -665,8 +682,7 @@ def _at(t, name: str, dtype, shape) -> int:
 
 
 def _cuda(t, name: str, dim: int):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    _here(t, name)
     if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, got {list(t.shape)}")
     return t.shape
@@ -843,7 +859,8 @@ def ssd_sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=N
     elif filtered is False:
         filtered = None
     if filtered is not None:
-        if not isinstance(filtered, torch.Tensor) or not filtered.is_cuda or filtered.dtype is not logits.dtype:
+        _here(filtered, "filtered")
+        if filtered.dtype is not logits.dtype:
             raise TypeError("filtered must be a CUDA tensor of the logits' dtype")
         if filtered.shape != logits.shape or filtered.stride(1) != 1 or (R > 1 and filtered.stride(0) != ld):
             raise ValueError("filtered must have the logits' shape and strides")

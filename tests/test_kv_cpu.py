@@ -163,3 +163,83 @@ def test_attend_refuses_more_steps_than_32_bits(ssd, T, B, Hkv, blocks, page):
     got = ssd.lib().ssd_kv_attend(P, ssd.SSD_BF16, Hkv * 64, P, P, P, P, 1, 16, Hkv, Hkv, 64, P, blocks * page // 16, P, P, B, T, 1,
                                   ctypes.c_float(1.0), 0, P, P, n, None, None)
     assert got == ssd.SSD_ERR_UNSUPPORTED
+
+
+class Somewhere(torch.Tensor):
+    """A host tensor that says it is on a GPU."""
+    __torch_function__ = torch._C._disabled_torch_function_impl
+    where = 0
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.where
+
+
+def _calls(ssd, where):
+    """(call, names of its tensors) for the four operators; where: the device of each tensor by name."""
+    def t(name, shape, dtype=torch.int32):
+        x = torch.zeros(shape, dtype=dtype).as_subclass(Somewhere)
+        x.where = where.get(name, where.get("*", 0))
+        return x
+    f32, bf16, u8 = torch.float32, torch.bfloat16, torch.uint8
+
+    def cache():
+        return (t("k_cache", (3, 2, 16, 64), u8), t("v_cache", (3, 2, 16, 64), u8), t("k_scale", (3, 2), f32), t("v_scale", (3, 2), f32))
+
+    def plan():
+        out = {"cu_new": t("cu_new", 3), "kv_len": t("kv_len", 2), "slots": t("slots", 5), "positions": t("positions", 5)}
+        ssd.ssd_kv_plan(t("seq_len", 2), t("new_len", 2), t("held", 2), t("block_table", (2, 4)), t("ring", 3), t("ring_state", 2), 16, 5,
+                        accept_len=t("accept_len", 2), out=out, dev_status=t("dev_status", 1))
+
+    def append():
+        ssd.ssd_kv_append(t("k", (5, 2, 64), bf16), t("v", (5, 2, 64), bf16), t("slots", 5), *cache(), dev_status=t("dev_status", 1))
+
+    def attend():
+        ssd.ssd_kv_attend(t("q", (5, 4, 64), bf16), *cache(), t("block_table", (2, 4)), t("cu_new", 3), t("kv_len", 2), 5, 1.0,
+                          out=t("out", (5, 4, 64), bf16), workspace=t("workspace", 256, u8), dev_status=t("dev_status", 1))
+
+    def sample():
+        ssd.ssd_sample(t("logits", (2, 9), f32), t("temperature", 2, f32), t("uniforms", 2, f32), top_k=t("top_k", 2),
+                       top_p=t("top_p", 2, f32), min_p=t("min_p", 2, f32), filtered=t("filtered", (2, 9), f32), tokens=t("tokens", 2),
+                       prob=t("prob", 2, f32), dev_status=t("dev_status", 1))
+
+    c = ["k_cache", "v_cache", "k_scale", "v_scale"]
+    return [(plan, ["seq_len", "new_len", "held", "block_table", "ring", "ring_state", "accept_len", "cu_new", "kv_len", "slots",
+                    "positions", "dev_status"]),
+            (append, ["k", "v", "slots", "dev_status"] + c),
+            (attend, ["q", "block_table", "cu_new", "kv_len", "out", "workspace", "dev_status"] + c),
+            (sample, ["logits", "temperature", "uniforms", "top_k", "top_p", "min_p", "filtered", "tokens", "prob", "dev_status"])]
+
+
+def test_binding_refuses_tensors_of_another_device(ssd, monkeypatch):
+    """The kernels launch on the current device and would read another one's addresses."""
+    launched = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: launched.append(name) or 0
+
+    monkeypatch.setattr(ssd, "lib", Lib)
+    monkeypatch.setattr(ssd, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(ssd, "_current_stream", lambda device: 0)
+    for i in range(4):
+        call, names = _calls(ssd, {})[i]
+        call()
+        assert len(launched) == 1
+        launched.clear()
+        for name in names + ["*"]:
+            with pytest.raises(ValueError, match="current device"):
+                _calls(ssd, {name: 1})[i][0]()
+            assert not launched, name
+
+
+def test_binding_refuses_a_stream_of_another_device(ssd, monkeypatch):
+    class Stream:
+        device_index = 1
+        cuda_stream = 5
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(ssd, "_current_device", lambda: 0, raising=False)
+    with pytest.raises(ValueError, match="current device"):
+        ssd._stream_at(Stream(), None)
+    Stream.device_index = 0
+    assert ssd._stream_at(Stream(), None) == 5 and ssd._stream_at(7, None) == 7
