@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const int key0 = st.key0 + key;
             auto fetch = [&](int r0, float(&s)[kSub][8]) {
 #pragma unroll
-                for (int u = 0; u < kSub; ++u) tc::tmem_load<8>(s[u], s_at + u * N + r0);
+                for (int u = 0; u < kSub; ++u) tc::tmem_load(s[u], s_at + u * N + r0);
             };
             // Scores of eight rows, without the rows' own factors; `next` holds what was fetched of them and then
             // gets the following rows under way.
@@ -764,8 +764,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             for (int r0 = 0; r0 < R; r0 += 8) {
                 if (r0 < rows) {
                     float o[2][8];
-                    tc::tmem_load<8>(o[0], at + r0);
-                    tc::tmem_load<8>(o[1], at + second + r0);
+                    tc::tmem_load(o[0], at + r0);
+                    tc::tmem_load(o[1], at + second + r0);
                     tc::tmem_wait_load(o);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
