@@ -349,7 +349,7 @@ struct Shared {
     float final[R];
     int64_t out_at[R];
     uint32_t tmem;
-    int nan_met;
+    int nan_met[kItems];  // NaN among an item's values that only some rows attend to, cleared by the output warps
     int gave_up;
     int highest;  // place in the ring of the last copy issued
     int last_part;
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         mbar_init(&S.q_full, 1);
         mbar_init(&S.q_free, 1);
         mbar_init(&S.drained, 1);
-        S.nan_met = 0;
+        for (int i = 0; i < kItems; ++i) S.nan_met[i] = 0;
         S.gave_up = 0;
         fence_mbar_init();
     }
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                             }
                             if (here) row[c] = w4, met = true;
                         }
-                        if (met) atomicExch(&S.nan_met, 1);
+                        if (met) atomicExch(&S.nan_met[item], 1);
                     }
                 }
             }
@@ -778,7 +778,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.o_free[buf]);
             if (st.last) {
-                if (*static_cast<volatile int *>(&S.nan_met) && ch < D) {
+                const bool nan_met = *static_cast<volatile int *>(&S.nan_met[st.item]) != 0;
+                if (nan_met && ch < D) {
                     // rare: NaN among values that only some rows attend to, read again from the cache
                     const int from = max(st.start, st.part_key0), to = min(st.stop, st.key0 + F::kStep);
                     for (int j = from; j < to; ++j) {
@@ -893,6 +894,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         tc::named_barrier(3, 128);
                     }
                 }
+                // all four warps have read it, at a barrier since; the next item of this number starts after this step is closed
+                if (nan_met && ch == 0) S.nan_met[st.item] = 0;
 #pragma unroll
                 for (int r = 0; r < R; ++r) acc[r] = 0.f;
                 m_run = -INFINITY, l_run = 0.f;

@@ -326,3 +326,22 @@ def test_token_counts_that_fall_are_reported_and_bounded(ssd):
     c.run(ssd, workspace=ws, dev_status=status)
     assert int(status) == ssd.SSD_DEV_BAD_LENGTH
     assert torch.equal(good.run(ssd, workspace=ws), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_nan_in_some_of_many_items(ssd, dtype):
+    """Several items to a CTA, some with NaN that only the later tokens see: it stays in its own item."""
+    rng = np.random.default_rng(16)
+    c = Case(16, [(int(rng.integers(5, 600)), 4) for _ in range(330)], 4, 2, 64, 16, dtype)
+    for b in rng.choice(330, 40, replace=False):
+        j = int(c.kv[b]) - int(rng.integers(1, 4))
+        c.v[c.table[b, j // 16], rng.integers(2), j % 16, rng.integers(64)] = 0xFF
+    got = c.run(ssd).double().cpu().numpy()
+    want = ref.attend(c.q.double().numpy(), VALUES[c.k], VALUES[c.v], c.ks.astype(np.float64), c.vs.astype(np.float64), c.table,
+                      c.cu, c.kv, c.P, c.scale, 0)
+    nan = np.isnan(want[0])
+    assert 40 < nan.sum() < 40 * 2 * 3 + 1
+    np.testing.assert_array_equal(np.isnan(got), nan)
+    want[3][:] = np.nanmax(np.abs(VALUES[c.v]) * c.vs[:, :, None, None])   # the largest |v| of a row is NaN with it
+    bound = ref.attend_bound(dtype, c.D, *want)
+    assert (np.abs(got - want[0])[~nan] <= bound[~nan]).all()
