@@ -345,3 +345,21 @@ def test_nan_in_some_of_many_items(ssd, dtype):
     want[3][:] = np.nanmax(np.abs(VALUES[c.v]) * c.vs[:, :, None, None])   # the largest |v| of a row is NaN with it
     bound = ref.attend_bound(dtype, c.D, *want)
     assert (np.abs(got - want[0])[~nan] <= bound[~nan]).all()
+
+
+@pytest.mark.parametrize("times", [30.0, 1000.0])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_queries_with_one_large_channel(ssd, dtype, times):
+    """Digits end at 2^-17 of a row's largest channel: what that can move a score by, 2^-17 |scale| max |q| sum |k|, moves a
+    weight by as much and their total once more, next to the bound of the other roundings."""
+    c = Case(17, [(700, 5), (40, 40)], 8, 2, 128, 32, dtype)
+    c.q[:, :, 5] *= times
+    c.k[..., 5] = 1                        # 2^-9: the scores are those of the small channels
+    got = c.run(ssd).double().cpu().numpy()
+    want = ref.attend(c.q.double().numpy(), VALUES[c.k], VALUES[c.v], c.ks.astype(np.float64), c.vs.astype(np.float64), c.table,
+                      c.cu, c.kv, c.P, c.scale, 0)
+    held = np.unique(c.table[c.table >= 0])
+    k = np.nansum(np.abs(VALUES[c.k[held]]) * c.ks[held][:, :, None, None], axis=3).max()
+    moved = 2.0 ** -17 * c.scale * np.abs(c.q.double().numpy()).max(axis=2, keepdims=True) * k
+    bound = ref.attend_bound(dtype, c.D, *want) + 2 * moved * want[1]
+    assert (np.abs(got - want[0]) <= bound).all()
