@@ -661,17 +661,26 @@ def _stream_at(stream, t) -> int:
     return stream.cuda_stream
 
 
-def _here(t, name: str):
-    """A CUDA tensor of the current device, on which the call launches."""
+def _device_of(t, name: str) -> int:
+    """The device of a call's first tensor: the current one, on which the call launches."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.get_device() != _current_device():
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{_current_device()}")
+    dev = t.get_device()
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev
 
 
-def _at(t, name: str, dtype, shape) -> int:
-    """Address of a contiguous CUDA tensor of that dtype and shape."""
-    _here(t, name)
+def _not_here(t, name: str, dev: int):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _at(t, name: str, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of that dtype, shape and device."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _not_here(t, name, dev)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -681,15 +690,16 @@ def _at(t, name: str, dtype, shape) -> int:
     return t.data_ptr()
 
 
-def _cuda(t, name: str, dim: int):
-    _here(t, name)
+def _cuda(t, name: str, dim: int, dev: int):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _not_here(t, name, dev)
     if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, got {list(t.shape)}")
     return t.shape
 
 
-def _status_at(dev_status):
-    return None if dev_status is None else _at(dev_status, "dev_status", torch.int32, dev_status.shape)
+def _status_at(dev_status, dev: int):
+    return None if dev_status is None else _at(dev_status, "dev_status", torch.int32, dev_status.shape, dev)
 
 
 def _on(stream, *made):
@@ -721,10 +731,10 @@ def ssd_kv_plan(seq_len, new_len, held, block_table, ring, ring_state, page_size
     """Commits accept_len, and gives each sequence's new_len next tokens their pages and
     slots: updates seq_len, held, block_table, ring and ring_state in place and returns
     dict(cu_new [B+1], kv_len [B], slots [cap], positions [cap]), all int32."""
-    i32 = torch.int32
-    B, = _cuda(seq_len, "seq_len", 1)
-    rows, max_blocks = _cuda(block_table, "block_table", 2)
-    num_pages, = _cuda(ring, "ring", 1)
+    i32, dev = torch.int32, _device_of(seq_len, "seq_len")
+    B, = _cuda(seq_len, "seq_len", 1, dev)
+    rows, max_blocks = _cuda(block_table, "block_table", 2, dev)
+    num_pages, = _cuda(ring, "ring", 1, dev)
     cap, of_b = int(cap), (B,)
     if rows != B:
         raise ValueError("block_table must be [B, max_blocks]")
@@ -738,12 +748,13 @@ def ssd_kv_plan(seq_len, new_len, held, block_table, ring, ring_state, page_size
             made.append(t)
             at.append(t.data_ptr())
         else:
-            at.append(_at(t, name, i32, (n,)))
+            at.append(_at(t, name, i32, (n,), dev))
     _check(lib().ssd_kv_plan(
-        _at(seq_len, "seq_len", i32, of_b), None if accept_len is None else _at(accept_len, "accept_len", i32, of_b),
-        _at(new_len, "new_len", i32, of_b), _at(held, "held", i32, of_b), B,
-        _at(block_table, "block_table", i32, (B, max_blocks)), max_blocks, _at(ring, "ring", i32, (num_pages,)),
-        _at(ring_state, "ring_state", i32, (2,)), num_pages, int(page_size), cap, *at, _status_at(dev_status),
+        _at(seq_len, "seq_len", i32, of_b, dev),
+        None if accept_len is None else _at(accept_len, "accept_len", i32, of_b, dev),
+        _at(new_len, "new_len", i32, of_b, dev), _at(held, "held", i32, of_b, dev), B,
+        _at(block_table, "block_table", i32, (B, max_blocks), dev), max_blocks, _at(ring, "ring", i32, (num_pages,), dev),
+        _at(ring_state, "ring_state", i32, (2,), dev), num_pages, int(page_size), cap, *at, _status_at(dev_status, dev),
         _stream_at(stream, seq_len)), "ssd_kv_plan")
     if stream is not None:
         _on(stream, *made)
@@ -756,20 +767,20 @@ _KV_DTYPES = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16, torch.float16: S
 _BYTES = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _kv_cache(k_cache, v_cache, k_scale, v_scale):
+def _kv_cache(k_cache, v_cache, k_scale, v_scale, dev):
     """(num_pages, Hkv, page_size, D) and the four addresses."""
-    shape = _cuda(k_cache, "k_cache", 4)
+    shape = _cuda(k_cache, "k_cache", 4, dev)
     kind = k_cache.dtype
     if kind not in _BYTES:
         raise TypeError(f"k_cache must be float8_e4m3fn or uint8, got {kind}")
     blocks = shape[:2]
-    return shape, (_at(k_cache, "k_cache", kind, shape), _at(v_cache, "v_cache", kind, shape),
-                   _at(k_scale, "k_scale", torch.float32, blocks), _at(v_scale, "v_scale", torch.float32, blocks))
+    return shape, (_at(k_cache, "k_cache", kind, shape, dev), _at(v_cache, "v_cache", kind, shape, dev),
+                   _at(k_scale, "k_scale", torch.float32, blocks, dev), _at(v_scale, "v_scale", torch.float32, blocks, dev))
 
 
-def _tokens(t, name, H, D):
+def _tokens(t, name, H, D, dev):
     """(T, heads, token stride) of a [T, H, D] tensor whose heads and channels are contiguous."""
-    T, heads, width = _cuda(t, name, 3)
+    T, heads, width = _cuda(t, name, 3, dev)
     if t.dtype not in _KV_DTYPES:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if width != D or (H is not None and heads != H):
@@ -787,13 +798,14 @@ def _tokens(t, name, H, D):
 def ssd_kv_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, *, dev_status=None, stream=None):
     """Stores keys and values [T, Hkv, D] (views with a longer token stride are fine) at
     `slots` of the e4m3 cache, growing the touched pages' power-of-two scales in place."""
-    (N, H, P, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    (T, _, ks), (Tv, _, vs) = _tokens(k, "k", H, D), _tokens(v, "v", H, D)
+    dev = _device_of(k, "k")
+    (N, H, P, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    (T, _, ks), (Tv, _, vs) = _tokens(k, "k", H, D, dev), _tokens(v, "v", H, D, dev)
     if T != Tv or v.dtype is not k.dtype:
         raise ValueError("k and v must match in shape and dtype")
     _check(lib().ssd_kv_append(
-        k.data_ptr(), v.data_ptr(), _KV_DTYPES[k.dtype], ks, vs, _at(slots, "slots", torch.int32, (T,)), T, H, D,
-        *cache, N, P, _status_at(dev_status), _stream_at(stream, k)), "ssd_kv_append")
+        k.data_ptr(), v.data_ptr(), _KV_DTYPES[k.dtype], ks, vs, _at(slots, "slots", torch.int32, (T,), dev), T, H, D,
+        *cache, N, P, _status_at(dev_status, dev), _stream_at(stream, k)), "ssd_kv_append")
 
 
 def kv_workspace(device=None) -> torch.Tensor:
@@ -805,10 +817,11 @@ def ssd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, kv
                   sm_scale: float, *, window: int = 0, out=None, workspace=None, dev_status=None, stream=None):
     """Causal attention of q [T, Hq, D] (bf16 or fp16) over the paged e4m3 cache: returns
     out [T, Hq, D].  cu_new and kv_len as from ssd_kv_plan."""
-    (N, Hkv, P, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    T, Hq, ld = _tokens(q, "q", None, D)
-    B, = _cuda(kv_len, "kv_len", 1)
-    rows, max_blocks = _cuda(block_table, "block_table", 2)
+    dev = _device_of(q, "q")
+    (N, Hkv, P, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    T, Hq, ld = _tokens(q, "q", None, D, dev)
+    B, = _cuda(kv_len, "kv_len", 1, dev)
+    rows, max_blocks = _cuda(block_table, "block_table", 2, dev)
     if rows != B:
         raise ValueError("block_table must be [B, max_blocks]")
     i32, made = torch.int32, []
@@ -824,10 +837,10 @@ def ssd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, kv
             s.wait_stream(torch.cuda.current_stream())
     _check(lib().ssd_kv_attend(
         q.data_ptr(), _KV_DTYPES[q.dtype], ld, *cache, N, P, Hq, Hkv, D,
-        _at(block_table, "block_table", i32, (B, max_blocks)), max_blocks, _at(cu_new, "cu_new", i32, (B + 1,)),
-        _at(kv_len, "kv_len", i32, (B,)), B, T, int(max_new), float(sm_scale), int(window),
-        _at(out, "out", q.dtype, (T, Hq, D)), _at(workspace, "workspace", torch.uint8, workspace.shape),
-        workspace.numel(), _status_at(dev_status), _stream_at(stream, q)), "ssd_kv_attend")
+        _at(block_table, "block_table", i32, (B, max_blocks), dev), max_blocks, _at(cu_new, "cu_new", i32, (B + 1,), dev),
+        _at(kv_len, "kv_len", i32, (B,), dev), B, T, int(max_new), float(sm_scale), int(window),
+        _at(out, "out", q.dtype, (T, Hq, D), dev), _at(workspace, "workspace", torch.uint8, workspace.shape, dev),
+        workspace.numel(), _status_at(dev_status, dev), _stream_at(stream, q)), "ssd_kv_attend")
     if stream is not None:
         _on(stream, *made)
     return out
@@ -839,7 +852,8 @@ def ssd_sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=N
     under temperature, top-k, top-p and min-p: returns dict(tokens, prob[, filtered]).
     filtered: True, or a tensor of the logits' shape and strides, for the logits with every
     dropped token at SSD_DROPPED_LOGIT (rows too low for that are copied: SSD_DEV_LOW_LOGITS)."""
-    R, V = _cuda(logits, "logits", 2)
+    dev = _device_of(logits, "logits")
+    R, V = _cuda(logits, "logits", 2, dev)
     dt = _logit_dtype(logits)
     ld, step = logits.stride()
     if R <= 1:
@@ -859,17 +873,18 @@ def ssd_sample(logits, temperature, uniforms, *, top_k=None, top_p=None, min_p=N
     elif filtered is False:
         filtered = None
     if filtered is not None:
-        _here(filtered, "filtered")
+        if not isinstance(filtered, torch.Tensor) or filtered.get_device() != dev:
+            _not_here(filtered, "filtered", dev)
         if filtered.dtype is not logits.dtype:
             raise TypeError("filtered must be a CUDA tensor of the logits' dtype")
         if filtered.shape != logits.shape or filtered.stride(1) != 1 or (R > 1 and filtered.stride(0) != ld):
             raise ValueError("filtered must have the logits' shape and strides")
     _check(lib().ssd_sample(
-        logits.data_ptr(), dt, R, V, ld, _at(temperature, "temperature", f32, of_r),
-        None if top_k is None else _at(top_k, "top_k", i32, of_r), None if top_p is None else _at(top_p, "top_p", f32, of_r),
-        None if min_p is None else _at(min_p, "min_p", f32, of_r), _at(uniforms, "uniforms", f32, of_r),
-        _at(tokens, "tokens", i32, of_r), _at(prob, "prob", f32, of_r), None if filtered is None else filtered.data_ptr(),
-        _status_at(dev_status), _stream_at(stream, logits)), "ssd_sample")
+        logits.data_ptr(), dt, R, V, ld, _at(temperature, "temperature", f32, of_r, dev),
+        None if top_k is None else _at(top_k, "top_k", i32, of_r, dev), None if top_p is None else _at(top_p, "top_p", f32, of_r, dev),
+        None if min_p is None else _at(min_p, "min_p", f32, of_r, dev), _at(uniforms, "uniforms", f32, of_r, dev),
+        _at(tokens, "tokens", i32, of_r, dev), _at(prob, "prob", f32, of_r, dev), None if filtered is None else filtered.data_ptr(),
+        _status_at(dev_status, dev), _stream_at(stream, logits)), "ssd_sample")
     if stream is not None:
         _on(stream, *made)
     out = {"tokens": tokens, "prob": prob}
