@@ -11,9 +11,9 @@
 // * A query row is scaled by a power of two that brings its largest channel into [128, 256).
 //   Two digits then hold a bf16 channel exactly down to 2^-9 of the largest, three an fp16
 //   one down to 2^-6; smaller ones are off by 2^-17 of the largest at most.
-// * A softmax weight is scaled to 256 at most.  Two digits (bf16) round it by 2^-8 of itself,
-//   three (fp16) by 2^-12, as those types would round it; they end at 2^-18 and 2^-23 of the
-//   largest weight of the step (fp16's second and third digits are of 32 times what is left
+// * A softmax weight is scaled to 256 at most.  Two digits (bf16) round it by 2^-9 of itself
+//   (after a half, by 2^-11), three (fp16) by 2^-14, less than half a step of those types; they
+//   end at 2^-18 and 2^-23 of the largest weight of the step (fp16's second and third digits are of 32 times what is left
 //   and summed apart).  A weight is taken relative to the largest of its own step of 256 (or
 //   128) keys, so that a long flat tail is not lost next to a large weight elsewhere; the
 //   steps' outputs are joined in fp32 registers under the running maximum.
@@ -38,10 +38,11 @@
 //
 // What bounds it (one GB300, copy rate 6764 GB/s; calls captured into graphs, L2 flushed).
 // One token a sequence: HBM (64 sequences of 8000 to 8191 keys, 8 heads of 128: 171 us, 6.2
-// TB/s; of 3 to 8191 keys 99 us, 5.4 TB/s: the shorter the items, the more of them a CTA
-// starts).  20 rows: the same (115 us, 4.7 TB/s).  36 rows and more: the softmax groups'
-// instructions (4 sequences of 90 to 131 thousand keys: 200 us, 4.5 TB/s), a sixth of them
-// for the reductions over lanes.  Measured on the way, for 64 sequences and 20 rows: loops
+// TB/s; of 3 to 8191 keys 101 us, 5.3 TB/s: the shorter the items, the more of them a CTA
+// starts).  20 rows: the same (117 us, 4.6 TB/s; fp16 140 us).  36 rows and more: the softmax
+// groups (4 sequences of 90 to 131 thousand keys: 201 us, 4.5 TB/s), whose chains of TMEM
+// reads, conversions and stores leave half the issue cycles empty and DRAM at 57%.  Prompts the
+// same, with next to no bytes (202 us).  Measured on the way, for 64 sequences and 20 rows: loops
 // unrolled over the rows missed the instruction cache on 41% of requests (404 us, against
 // 265 rolled); a query warp that took four rows at a time held up every change of item (265,
 // against 142); 24 warps with two to each 32 keys were slower (178, against 131).

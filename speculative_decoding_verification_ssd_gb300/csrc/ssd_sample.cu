@@ -23,7 +23,7 @@
 //
 // What bounds it: some 35 instructions for each weight, and 1 to 2 us for each cluster
 // barrier, of which a limit takes two to four.  256 rows of 128256 bf16 logits, captured into
-// a graph with L2 flushed: 88 us without limits, 106 top-k, 196 top-p, 65 min-p (the tokens
+// a graph with L2 flushed: 89 us without limits, 106 top-k, 194 top-p, 64 min-p (the tokens
 // below the limit need no weight), 106 mixed; the bytes would take 10.  Two CTAs to an SM: one
 // computes while the other waits.  Clusters of 8, three CTAs to an SM and CTAs of 1024
 // threads were all slower.
