@@ -491,7 +491,8 @@ int ssd_kv_plan(int32_t *seq_len, const int32_t *accept_len, const int32_t *new_
  * k, v: [T, Hkv, D] of `dtype` (SSD_F32, SSD_BF16 or SSD_F16), heads and
  *   channels contiguous, tokens k_stride / v_stride elements apart.
  * slots [T] int32 (ssd_kv_plan): a negative slot is skipped; tokens of one page
- *   are consecutive and in order, and no page is met twice in a call.
+ *   are consecutive and in order, with no skipped one between them, and no page is met
+ *   twice in a call (two runs of one page would be stored at the same time).
  * For every page written and head: with amax the largest finite magnitude of the
  * new tokens there, need = the smallest power of two 2^k, k >= -100, with
  * amax <= 448 * 2^k.  A page whose first new token has row 0 takes scale = need;
