@@ -12,9 +12,10 @@
 // * A thread has a row of S: its maximum and sum cross no lanes, and a mask is 32 keys to a word.
 // * The weights go back to TMEM as halves, over the scores they are made of, and are the A operand
 //   of O = P V from there; V is turned into halves (exactly) once for all rows.  A weight is rounded
-//   by 2^-11 of itself; it is held as 2^5 2^(s - m) vs / v, with m and v a maximum of the scores and a
-//   power of two above the value scales that may lag by 2^8 and 2^2: at most 2^15, and normal down to
-//   2^-19 of the largest.  O stays in TMEM from step to step, and is scaled there when m or v has to move on.
+//   by 2^-11 of itself; it is held as 2^5 2^s vs / 2^m, with 2^m the largest 2^s vs of the keys that the row has
+//   attended to, which may lag by 2^10: at most 2^15, and normal down to 2^-19 of the largest.  O stays in TMEM
+//   from step to step, and is scaled there when m has to move on.  (Relative to a step's largest value scale, which a row need not attend to or which its largest
+//   scores need not meet, weights lost bits that count.)
 //
 // Two streams of work pass through the tensor cores in turns, each with its S, O and four softmax
 // warps: the two tiles of 128 rows of an item of more than 128, else every other step of its keys.
@@ -73,8 +74,14 @@ constexpr int kItemCost = 5;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMost = 3.402823466e38f;
 constexpr float kNothing = -2e30f;  // the maximum of a row that has attended to nothing
-// Powers of two by which a row's maximum, and the values' unit, may be passed; weights are 2^(kUnit - 126) times theirs.
-constexpr int kLag = 8, kLagValues = 2, kUnit = 126 + 15 - kLag - kLagValues;
+// Weights are 2^kUp times those relative to a row's largest, which may be passed by 2^kLag.
+constexpr float kLag = 10.f, kUp = 15.f - kLag, kUnit = 32.f;  // (2^kUp)
+// A pass takes the short form of the weights, relative to one number for their sum and for O, where value scales are from
+// 2^-kMostUnit to 2^kMostUnit, so that the sum's terms down to 2^-(2 kMostUnit) are normal in fp32.
+constexpr float kMostUnit = 50.f;
+// In the long form the sum is relative to the scores' maximum, and what the weights are relative to is not below 2^kLow
+// (and kLag less) of that, so that it stays a normal number whatever the value scales.
+constexpr float kLow = -109.f;
 
 struct Workspace {
     float o[2 * kMaxCtas][kMaxHead][kMaxRows];
@@ -329,6 +336,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// Of numbers below the normal range, too.
+__device__ __forceinline__ float lg2_of_any(float x) {
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ void prefetch(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // 2^(e - 127)
 __device__ __forceinline__ float power(int e) { return __uint_as_float(static_cast<uint32_t>(e) << 23); }
@@ -374,9 +387,8 @@ struct Step {
     int32_t first_cta, parts;  // of the item
     int32_t seq, head, row0, rows, token0, pos0;
     int32_t part_key0;    // first key of the part
-    int32_t v_exp;        // exponent of the largest value scale, biased
     int32_t page[kGroups];
-    // of the keys, and of the values (NaN if not finite); the logarithm (base 2) of the latter and its reciprocal
+    // of the keys, and of the values (NaN if not finite); the logarithm (base 2) of the latter's size, and its reciprocal
     alignas(16) float4 scale[kGroups];
 };
 
@@ -389,7 +401,7 @@ struct Shared {
     Step step[kSteps];
     float q_factor[kItems][kMaxRows];
     float2 stat[2][2][kTile];  // maxima and sums of the streams, of every other item
-    int32_t v_unit[2][2];
+    float unit[2][2][kTile];   // what their weights are relative to
     uint32_t tmem;
     int nan_met[kItems];  // NaN among an item's values that only some rows attend to
     int gave_up;
@@ -603,10 +615,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t s_at = tmem + group * kTile + lanes, o_at = tmem + F::kO + group * D + lanes;
         int ended[2] = {0, 0}, meets = 0, shared = 0;  // items whose output a stream has finished; meetings of the two groups; items of one tile
         Row row{};
-        float m = 0.f, l = 0.f, qf = 0.f;
-        int v_unit = 0;
+        // what the row's sum is relative to, the sum, and what the weights in O are relative to that (0 but in the long form)
+        float m = 0.f, l = 0.f, u = 0.f, qf = 0.f;
         int passes = 0, r = 0, k_slot = 0;  // of the stream; this thread's row of the item; of the step's keys
         bool any = false, some = false;  // the warp has rows; the row has attended to a key
+        bool far = false;  // a row of the warp is one that only the long form serves
         for (int it = 0;; ++it) {
             const int flags = open_step(it);
             if (!(flags & kLive)) break;
@@ -617,7 +630,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 r = at_row + (pair && other ? kTile : 0);
                 any = __any_sync(kAll, r < rows);
                 row = load_row(P, st.token0, st.pos0, st.row0 + r, r < rows);
-                m = -1e30f, l = 0.f, v_unit = 0, some = false;
+                m = kNothing, l = 0.f, u = 0.f, some = false, far = false;
             }
             if (pair || !other) {
                 const bool first = flags & kFirst;
@@ -628,6 +641,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) sees[c] &= ((there >> (2 * c)) & 1 ? 0xFFFFu : 0u) | ((there >> (2 * c)) & 2 ? 0xFFFF0000u : 0u);
                 }
+                const bool ordinary = (flags & kOrdinary) && !far;
                 if (!wait(&S.s_full[group], passes++ & 1)) break;
                 tc::fence_after();
                 if (pair == other) tc::warp_arrive(&S.k_empty[k_slot]);  // the step's last scores are there
@@ -638,20 +652,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         const float f = ks * qf;
                         return f <= 1.2e-38f ? 1.2e-38f : f;
                     };
-                    // What the weights are relative to moves on where it is passed by 2^kLag, and O follows.
-                    auto follow = [&](float top) {
-                        if (first) {
-                            m = fmaxf(top, -1e30f);
-                            v_unit = st.v_exp;
-                            return;
-                        }
-                        const bool move = top > m + kLag, unit = st.v_exp > v_unit + kLagValues;
-                        if (!__any_sync(kAll, move || unit)) return;
-                        const float to = move ? top : m;
-                        float f = ex2(m - to);
-                        l *= f;
-                        m = to;
-                        if (unit) f *= ex2(static_cast<float>(v_unit - st.v_exp)), v_unit = st.v_exp;
+                    some |= (sees[0] | sees[1] | sees[2] | sees[3]) != 0;
+                    auto scale_output = [&](float f) {
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             uint32_t o[16];
@@ -662,10 +664,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             tc::tmem_store(o_at + c, o);
                         }
                     };
-                    some |= (sees[0] | sees[1] | sees[2] | sees[3]) != 0;
                     // Loops of few instructions: straight-line code for a whole row of scores passes through the instruction
                     // caches each time, and the other roles' code with it.
-                    if (flags & kOrdinary) {
+                    if (ordinary) {
                         float x[4][16], top = -INFINITY;
                         auto fetch = [&](int c) {
 #pragma unroll
@@ -685,25 +686,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         fetch(0);
 #pragma unroll 1
                         for (int c = 0; c < 2; ++c) {
-                            float f[4];
+                            float f[4], e[4];
 #pragma unroll
-                            for (int h = 0; h < 4; ++h) f[h] = factor(st.scale[4 * c + h].x);
+                            for (int h = 0; h < 4; ++h) f[h] = factor(st.scale[4 * c + h].x), e[h] = st.scale[4 * c + h].z;
                             arrived(c);
-                            float u[4];
+                            float w[4];
 #pragma unroll
                             for (int h = 0; h < 4; ++h) {
                                 float t = max3(x[h][0], x[h][1], x[h][2]), v = max3(x[h][3], x[h][4], x[h][5]);
 #pragma unroll
                                 for (int i = 6; i < 14; i += 4) t = max3(t, x[h][i], x[h][i + 1]), v = max3(v, x[h][i + 2], x[h][i + 3]);
-                                u[h] = max3(fmaxf(t, v), x[h][14], x[h][15]) * f[h];
+                                w[h] = fmaf(max3(fmaxf(t, v), x[h][14], x[h][15]), f[h], e[h]);
                             }
                             fetch(1 - c);
-                            top = fmaxf(top, fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])));
+                            top = fmaxf(top, fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])));
                         }
-                        follow(top);
-                        // With value scales that are ordinary numbers 2^(s - m) vs is one power, and the sum over 16 keys is
-                        // divided by vs.
-                        const float unit = static_cast<float>(kUnit - v_unit) - m;
+                        // What the weights are relative to moves on where it is passed by 2^kLag, and O and the sum follow.
+                        if (first) {
+                            m = fmaxf(top, kNothing);
+                        } else if (const bool move = top > m + kLag; __any_sync(kAll, move)) {
+                            const float to = move ? top : m, by = ex2(m - to);
+                            l *= by;
+                            m = to;
+                            scale_output(by);
+                        }
+                        // 2^s vs / 2^m is one power here, and the sum over 16 keys is divided by vs.
+                        const float unit = kUp - m;
                         float sums = 0.f;
                         // (the first 64 scores' weights lie over themselves: the second 64 follow them)
 #pragma unroll 1
@@ -732,38 +740,63 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                             for (int h = 0; h < 4; ++h) tc::tmem_store(s_at + 32 * c + 8 * h, w[h]);
                         }
-                        l = fmaf(sums, power(v_unit + 127 - kUnit), l);
+                        l = fmaf(sums, 1.f / kUnit, l);
                     } else {
-                        float x[16], top = -INFINITY;
+                        float x[16], to = m, largest = -INFINITY;
 #pragma unroll 1
-                        for (int c = 0; c < 2 * kGroups; ++c) {  // the largest score, then the weights
+                        for (int c = 0; c < 2 * kGroups; ++c) {  // the largest score and weight, then the weights
                             const int g = c & (kGroups - 1);
                             const float4 sc = st.scale[g];
                             const uint32_t bits = (g < 4 ? (g < 2 ? sees[0] : sees[1]) : (g < 6 ? sees[2] : sees[3])) >> (16 * (g & 1));
                             const float f = sc.x * qf;
-                            if (c == kGroups) follow(top);
+                            if (c == kGroups) {
+                                largest = fmaxf(largest, kLow);
+                                if (first) {
+                                    m = to, u = largest;
+                                } else {
+                                    const float up = to - m;
+                                    l *= ex2(-up);
+                                    m = to, u -= up;
+                                    const bool move = largest > u + kLag;
+                                    if (__any_sync(kAll, move)) {
+                                        scale_output(move ? ex2(u - largest) : 1.f);
+                                        if (move) u = largest;
+                                    }
+                                }
+                            }
                             tc::tmem_load(x, s_at + 16 * g);
                             tc::tmem_wait_load(x);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) x[i] = (bits >> i) & 1 ? x[i] * f : -INFINITY;
                             if (c < kGroups) {
+                                float top = x[0];
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) top = fmaxf(top, x[i]);
+                                for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+                                const float before = to;
+                                to = fmaxf(to, top);
+                                largest = fmaxf(largest - (to - before), (top - to) + sc.z);
                                 continue;
                             }
-                            const float up = sc.y * power(kUnit + 127 - v_unit);
+                            const float e = sc.z + (kUp - u);
                             uint32_t w[8];
                             float sum = 0.f;
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                float y = ex2(x[i] - m), z = ex2(x[i + 1] - m);
-                                sum += y + z;
+                                float y = x[i] - m, z = x[i + 1] - m;
+                                sum += ex2(y) + ex2(z);
                                 // (not 0 times a scale that is not finite, of keys that the row does not attend to)
-                                y = (bits >> i) & 1 ? y * up : 0.f, z = (bits >> i) & 2 ? z * up : 0.f;
+                                y = (bits >> i) & 1 ? copysignf(ex2(y + e), sc.y) : 0.f, z = (bits >> i) & 2 ? copysignf(ex2(z + e), sc.y) : 0.f;
                                 w[i / 2] = two_of(__half(), y, z);
                             }
                             l += sum;
                             tc::tmem_store(s_at + 8 * g, w);
+                        }
+                        // back to one number for both, where that is in range
+                        const bool none = m == kNothing;
+                        far = __any_sync(kAll, !none && fabsf(u) > kMostUnit);
+                        if (!far) {
+                            if (!none) m += u, l *= ex2(-u);
+                            u = 0.f;
                         }
                     }
                     tc::tmem_wait_store();
@@ -775,17 +808,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 // ---- the item's output, or this part's share of it ----
                 const int took = pair || !(flags & kSingle) ? 3 : (flags & kStream ? 2 : 1);
                 const int ch0 = pair ? 0 : group * (D / 2), chs = pair ? D : D / 2;  // the two groups share a single tile
-                if (!some) m = kNothing, l = 0.f;
+                if (!some) m = kNothing, l = 0.f, u = 0.f;
                 float mul_0 = 0.f, mul_1 = 0.f, total = l, top = m;
                 bool fine = true;
                 if (pair) {
-                    (group ? mul_1 : mul_0) = power(v_unit + 127 - kUnit);
+                    (group ? mul_1 : mul_0) = ex2(u - kUp);
                     fine = wait(&S.o_full[group], ended[group] & 1);
                 } else {
                     // (the other group may still read what the item before left)
                     const int buf = shared++ & 1;
                     S.stat[buf][group][at_row] = make_float2(m, l);
-                    if (at_row == 0) S.v_unit[buf][group] = v_unit;
+                    S.unit[buf][group][at_row] = u;
                     arrive(&S.meet);
                     fine = wait(&S.meet, meets++ & 1);
                     float2 both[2];
@@ -796,9 +829,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         if (!((took >> g) & 1)) continue;
-                        const float f = ex2(both[g].x - top);
-                        total = fmaf(both[g].y, f, total);
-                        (g ? mul_1 : mul_0) = f * power(S.v_unit[buf][g] + 127 - kUnit);
+                        const float down = both[g].x - top;
+                        total = fmaf(both[g].y, ex2(down), total);
+                        (g ? mul_1 : mul_0) = ex2(down + (S.unit[buf][g][at_row] - kUp));
                         fine &= wait(&S.o_full[g], ended[g] & 1);
                     }
                 }
@@ -1217,13 +1250,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (page != kNoPlace && !there) report(P.dev_status, SSD_DEV_BAD_PAGE);
                 if (t0 + kAtOnce < part.steps) next = look_up(t0 + kAtOnce);
                 const bool finite = fabsf(vs) <= kMost;
-                float top = finite ? fabsf(vs) : 0.f;
-#pragma unroll
-                for (int o = 1; o < kGroups; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-                const int v_exp = min(max(static_cast<int>(__float_as_uint(top) >> 23), 8), 254);
+                const float lv = finite ? lg2_of_any(fabsf(vs)) : __int_as_float(0x7FC00000);
                 const uint32_t there_all = __ballot_sync(kAll, there);
-                // between 2^-100 and 2^100
-                const uint32_t fast_all = __ballot_sync(kAll, !there || (ks >= 7.9e-31f && ks <= 1.2e30f && vs >= 7.9e-31f && vs <= 1.2e30f));
+                // between 2^-100 and 2^100, and between 2^-kMostUnit and 2^kMostUnit
+                const uint32_t fast_all = __ballot_sync(kAll, !there || (ks >= 7.9e-31f && ks <= 1.2e30f && fabsf(lv) <= kMostUnit && vs > 0.f));
                 const int n = min(kAtOnce, part.steps - t0);
                 for (int i = 0; i < n; ++i, ++s) {
                     const int slot = s % kSteps;
@@ -1232,7 +1262,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     Step &st = S.step[slot];
                     if (my_step == i) {
                         st.page[my_group] = page;
-                        st.scale[my_group] = there ? make_float4(ks, finite ? vs : __int_as_float(0x7FC00000), lg2(vs), __frcp_rn(vs))
+                        st.scale[my_group] = there ? make_float4(ks, finite ? vs : __int_as_float(0x7FC00000), lv, __frcp_rn(vs))
                                                       : make_float4(1.f, 1.f, 0.f, 1.f);
                         if (my_group == 0) {
                             const int k0 = key0 + (t0 + i) * kTile;
@@ -1252,7 +1282,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             st.seq = part.b, st.head = part.head, st.row0 = part.row0, st.rows = part.rows;
                             st.token0 = part.first, st.pos0 = part.pos0;
                             st.part_key0 = key0;
-                            st.v_exp = v_exp;
                         }
                     }
                     event += passes;

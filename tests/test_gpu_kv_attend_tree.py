@@ -453,3 +453,61 @@ def test_queries_with_one_large_channel(ssd, dtype, times):
     moved = 2.0 ** -17 * c.scale * np.abs(c.q.double().numpy()).max(axis=2, keepdims=True) * k
     bound = ref.attend_bound(dtype, c.D, *want) + 2 * moved * want[1]
     assert (np.abs(got - want[0]) <= bound).all()
+
+
+def check_seen(c, got, window=0, rows=slice(None)):
+    """Against the bound that is relative to what each token attends to, and to nothing else."""
+    args = (c.table, c.cu, c.kv, c.sees, c.P, c.scale, window)
+    ks, vs = c.ks.astype(np.float64), c.vs.astype(np.float64)
+    out, weight, score, _, count = c.want(window)
+    floor = ref.seen_floor(c.q.double().numpy(), VALUES[c.k], ks, vs, *args)
+    bound = ref.seen_bound(c.dtype, c.D, out, weight, score, floor, count)
+    over = (np.abs(got.double().cpu().numpy() - out) - bound)[rows]
+    assert over.max() <= 0, (over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("times", [30, 60, 100])
+@pytest.mark.parametrize("n,window", [(40, 0), (40, 40), (150, 0)])
+def test_a_large_value_scale_concerns_those_alone_that_see_it(ssd, dtype, times, n, window):
+    """Nodes 12 to 27 lie in a page of far larger scale, and every other token attends to none of them."""
+    c = Case(31, [(260 + n, n), (300, 3)], 4, 2, 64, 16, dtype, "chain")
+    hidden = set(range(12, 28))
+    for t in range(0, n, 2):
+        c.sees[t] -= hidden
+    want = c.run(ssd, window=window)
+    check_seen(c, want, window)
+    c.vs[c.table[0, 17]] *= np.float32(2.0 ** times)
+    got = c.run(ssd, window=window)
+    check_seen(c, got, window, slice(None) if dtype == BF else slice(0, n, 2))      # (what fp16 does not hold is left out)
+    if times == 30:
+        assert torch.equal(got[0:n:2], want[0:n:2])
+
+
+@pytest.mark.parametrize("times", [30, 60])
+@pytest.mark.parametrize("page", [0, 5, 17])
+def test_the_largest_score_next_to_the_largest_value_scale(ssd, times, page):
+    """A page of far larger value scale, whose keys all score 2^-(times + 20) of the others: what it adds is little, and
+    the others' weights keep their bits."""
+    for dtype in (BF, FP):
+        c = Case(32, [(300, 20), (77, 7)], 4, 2, 64, 16, dtype)
+        p = c.table[0, page]
+        c.q[:, :, 5] = 4.0
+        c.k[..., 5] = 0
+        c.k[p, ..., 5] = 0xFE                                    # -448
+        c.ks[p] = 0.02
+        c.scale = (times + 20) * float(np.log(2.0)) / (4 * 448 * 0.02)
+        c.vs[p] = 0.02 * 2.0 ** times
+        check_seen(c, c.run(ssd))
+
+
+def test_value_scales_of_all_sizes(ssd):
+    """From 2^-120 to 2^100, none and negative ones among them, with a mask that shows each token some pages."""
+    for seed, dtype in ((33, BF), (34, BF)):
+        c = Case(seed, [(400, 60), (200, 9)], 4, 2, 64, 16, dtype, spread=8.0)
+        c.vs *= (2.0 ** c.rng.uniform(-115, 105, c.vs.shape)).astype(np.float32)
+        c.vs[c.table[0, 3]] = 0.0
+        c.vs[c.table[0, 5]] *= -1
+        c.sees = [{j for j in s if c.rng.random() < 0.7} for s in c.sees]
+        for window in (0, 23):
+            check_seen(c, c.run(ssd, window=window), window)
