@@ -73,12 +73,15 @@ constexpr int kMaxPairs = 1 << 18;  // such pairs of a call
 constexpr int kItemCost = 5;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMost = 3.402823466e38f;
-constexpr float kNothing = -2e30f;  // the maximum of a row that has attended to nothing
+constexpr float kNothing = -3e38f;  // the maximum of a row that has attended to nothing
 // Weights are 2^kUp times those relative to a row's largest, which may be passed by 2^kLag.
 constexpr float kLag = 10.f, kUp = 15.f - kLag, kUnit = 32.f;  // (2^kUp)
 // A pass takes the short form of the weights, relative to one number for their sum and for O, where value scales are from
-// 2^-kMostUnit to 2^kMostUnit, so that the sum's terms down to 2^-(2 kMostUnit) are normal in fp32.
-constexpr float kMostUnit = 50.f;
+// 2^-kMostUnit to 2^kMostUnit, so that the sum's terms down to 2^-(2 kMostUnit) are normal in fp32, and no score can
+// be above 2^21, so that exponents are exact to 1/8: a product of digits is at most 2^8 448 kMostHead = 2^23.8 (and mostly
+// 2^8 less, which leaves 2^-12).  The long form's exponents are differences of scores, exact whatever their size, and a warp
+// goes back to the short one while that is so to 2^-12.
+constexpr float kMostUnit = 50.f, kMostFactor = 0.125f, kMostScore = 8192.f;
 // In the long form the sum is relative to the scores' maximum, and what the weights are relative to is not below 2^kLow
 // (and kLag less) of that, so that it stays a normal number whatever the value scales.
 constexpr float kLow = -109.f;
@@ -387,6 +390,7 @@ struct Step {
     int32_t first_cta, parts;  // of the item
     int32_t seq, head, row0, rows, token0, pos0;
     int32_t part_key0;    // first key of the part
+    float k_most;         // the largest scale of its keys, where all are ordinary
     int32_t page[kGroups];
     // of the keys, and of the values (NaN if not finite); the logarithm (base 2) of the latter's size, and its reciprocal
     alignas(16) float4 scale[kGroups];
@@ -630,7 +634,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 r = at_row + (pair && other ? kTile : 0);
                 any = __any_sync(kAll, r < rows);
                 row = load_row(P, st.token0, st.pos0, st.row0 + r, r < rows);
-                m = kNothing, l = 0.f, u = 0.f, some = false, far = false;
+                m = kNothing, l = 0.f, u = 0.f, qf = 0.f, some = false, far = false;
             }
             if (pair || !other) {
                 const bool first = flags & kFirst;
@@ -641,12 +645,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) sees[c] &= ((there >> (2 * c)) & 1 ? 0xFFFFu : 0u) | ((there >> (2 * c)) & 2 ? 0xFFFF0000u : 0u);
                 }
-                const bool ordinary = (flags & kOrdinary) && !far;
+                // (qf is 0 before the first scores, whose factors are there with them)
+                bool ordinary = (flags & kOrdinary) && !far && !__any_sync(kAll, qf * st.k_most > kMostFactor);
                 if (!wait(&S.s_full[group], passes++ & 1)) break;
                 tc::fence_after();
                 if (pair == other) tc::warp_arrive(&S.k_empty[k_slot]);  // the step's last scores are there
                 if (any) {
-                    if (first) qf = r < st.rows ? S.q_factor[st.item][r] : 0.f;
+                    if (first) {
+                        qf = r < st.rows ? S.q_factor[st.item][r] : 0.f;
+                        ordinary = ordinary && !__any_sync(kAll, qf * st.k_most > kMostFactor);
+                    }
                     // Of the scores.  Not 0 where it is small, so that a masked one stays below all others.
                     auto factor = [&](float ks) {
                         const float f = ks * qf;
@@ -793,7 +801,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         }
                         // back to one number for both, where that is in range
                         const bool none = m == kNothing;
-                        far = __any_sync(kAll, !none && fabsf(u) > kMostUnit);
+                        far = __any_sync(kAll, !none && (fabsf(u) > kMostUnit || fabsf(m) > kMostScore));
                         if (!far) {
                             if (!none) m += u, l *= ex2(-u);
                             u = 0.f;
@@ -1251,6 +1259,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (t0 + kAtOnce < part.steps) next = look_up(t0 + kAtOnce);
                 const bool finite = fabsf(vs) <= kMost;
                 const float lv = finite ? lg2_of_any(fabsf(vs)) : __int_as_float(0x7FC00000);
+                float k_most = ks;
+#pragma unroll
+                for (int o = 1; o < kGroups; o <<= 1) k_most = fmaxf(k_most, __shfl_xor_sync(kAll, k_most, o));
                 const uint32_t there_all = __ballot_sync(kAll, there);
                 // between 2^-100 and 2^100, and between 2^-kMostUnit and 2^kMostUnit
                 const uint32_t fast_all = __ballot_sync(kAll, !there || (ks >= 7.9e-31f && ks <= 1.2e30f && fabsf(lv) <= kMostUnit && vs > 0.f));
@@ -1282,6 +1293,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             st.seq = part.b, st.head = part.head, st.row0 = part.row0, st.rows = part.rows;
                             st.token0 = part.first, st.pos0 = part.pos0;
                             st.part_key0 = key0;
+                            st.k_most = k_most;
                         }
                     }
                     event += passes;

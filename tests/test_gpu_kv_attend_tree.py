@@ -511,3 +511,31 @@ def test_value_scales_of_all_sizes(ssd):
         c.sees = [{j for j in s if c.rng.random() < 0.7} for s in c.sees]
         for window in (0, 23):
             check_seen(c, c.run(ssd, window=window), window)
+
+
+@pytest.mark.parametrize("size", [64.0, 2.0 ** 13, 2.0 ** 20, 2.0 ** 27, 1e15, 1e28, 1e31])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_scores_of_any_size(ssd, dtype, size, sign):
+    """Scores are whole multiples of `size`, so that the keys of the largest share all: a weight's half, the sums of equal
+    numbers and half a step of the output are what is rounded, and exponents up to 8192 twice (half a step of fp32, 2^-24 of
+    the score), for a weight and for their total; larger scores enter as their differences."""
+    for seed, (kv, n) in enumerate(((500, 30), (40, 30), (1300, 90))):
+        c = Case(seed, [(kv, n)], 4, 2, 64, 64, dtype, "chain")
+        level = c.rng.integers(2, 9, c.k.shape[:3])
+        at = [(c.table[0, j // 64], j % 64) for j in (3, kv - n // 2)]
+        for page, row in at:
+            level[page, :, row] = 1 if sign < 0 else 9
+        if kv > 500:                                             # one that only some see is by itself
+            level[at[0][0], :, at[0][1]] = 5
+        c.k[:] = 0
+        c.k[..., 0] = np.array([loop.e4m3_values().tolist().index(float(v)) for v in range(10)])[level]
+        c.ks[:], c.q[:], c.scale = 1.0, 0, size
+        c.q[..., 0] = float(sign)
+        got = c.run(ssd).double().cpu().numpy()
+        out, weight, score, _, count = c.want()
+        half = torch.finfo(dtype).eps / 2
+        d = 2.0 ** -11 + 2.0 ** -20 + 2 * count * 2.0 ** -23 + 4 * 2.0 ** -24 * np.minimum(score, 8192 * np.log(2))
+        bound = half * np.abs(out) + (1 + half) * d * weight + 2.0 ** -24
+        over = np.abs(got - out) - bound
+        assert over.max() <= 0, (over.max(), np.unravel_index(over.argmax(), over.shape))
