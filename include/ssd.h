@@ -614,8 +614,9 @@ int ssd_qk_rope(const void *q, const void *k, int dtype, int64_t q_stride, int64
  *   above it.  Tokens from cu_new[B] on get 0 in both.
  * A parent that is not before its node counts as -1 (SSD_DEV_BAD_TREE).
  *   SSD_DEV_BAD_LENGTH counts a sequence of more than max_new tokens (those beyond get 0 in
- *   both), a cu_new that falls, is negative or passes T (cut to what is there), and a seq_len
- *   that is negative or within SSD_TREE_MAX of 2^31 (it counts as 0).
+ *   both), a cu_new that falls (the batch ends there: sequences from it on have no tokens), is
+ *   negative or passes T (cut to what is there), and a seq_len that is negative or within
+ *   SSD_TREE_MAX of 2^31 (it counts as 0).
  * Requires 1 <= B <= SSD_KV_MAX_B, 1 <= max_new <= SSD_TREE_MAX.
  */
 int ssd_tree_plan(const int32_t *parent, const int32_t *cu_new, const int32_t *seq_len, int B, int T, int max_new,
@@ -626,7 +627,8 @@ int ssd_tree_plan(const int32_t *parent, const int32_t *cu_new, const int32_t *s
  * attends to every position below kv_len[b] - n, and of the new tokens j <= i (at position
  * kv_len[b] - n + j) to those whose bit is set in its row of mask [T, W], W = ceil(max_new /
  * 32) (ssd_tree_plan, or any mask); with window > 0 only to the last `window` of those.
- * A mask whose bits j <= i are all set gives ssd_kv_attend's function.
+ * A mask whose bits j <= i are all set gives ssd_kv_attend's function.  A cu_new that falls ends
+ * the batch as in ssd_tree_plan.
  * Everything else (layouts, scales, lengths, reports) as ssd_kv_attend, with max_new <=
  * SSD_TREE_MAX.
  * workspace: ssd_kv_tree_workspace_size() bytes, used as ssd_kv_attend's.

@@ -28,6 +28,24 @@ inline bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_
 // Status of the launch just made.
 inline int launched() { return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
 
+// Sequences of a batch: those before the first whose tokens, cu[b] to cu[b + 1], would end before they begin.  What follows
+// would name tokens of sequences before it.  For a whole block, room [1] for its use.
+template <int kThreads>
+__device__ __forceinline__ int sequences(const int32_t *cu, int B, int *room) {
+    int fall = B;
+#pragma unroll 8
+    for (int b = threadIdx.x; b < B; b += kThreads)
+        if (cu[b + 1] < cu[b]) fall = min(fall, b);
+    if (!__syncthreads_or(fall < B)) return B;
+    if (threadIdx.x == 0) *room = B;
+    __syncthreads();
+    if (fall < B) atomicMin(room, fall);
+    __syncthreads();
+    fall = *room;
+    __syncthreads();
+    return fall;
+}
+
 // Two values as e4m3, `lo` in the low byte: nearest, ties to even, magnitudes beyond
 // 448 become 448, NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {

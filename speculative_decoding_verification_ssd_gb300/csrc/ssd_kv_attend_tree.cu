@@ -90,7 +90,7 @@ struct Workspace {
     float o[2 * kMaxCtas][kMaxHead][kMaxRows];
     float2 ml[2 * kMaxCtas][kMaxRows];
     int32_t arrived[kMaxCtas];  // parts of the item that starts in each CTA; left at 0
-    int32_t pairs;              // of the schedule below
+    int32_t pairs, seqs;        // of the schedule below, and sequences in it
     int32_t sums[kMaxPairs + 1];  // steps before each pair
     int32_t seq[kMaxPairs];
     int32_t row0[kMaxPairs];
@@ -245,29 +245,33 @@ __device__ __forceinline__ int last_not_above(const int32_t *sums, int n, int x)
 }
 
 // The schedule: the (sequence, row block) pairs, and the units before each in sums [pairs + 1], of which the total is
-// returned.  blocks [B + 1] is for the block's own use.
+// returned.  seqs: the sequences() in it.  blocks [B + 1] is for the block's own use.
 template <int kN>
 __device__ __forceinline__ int make_schedule(const TreeParams &P, int32_t *blocks, int32_t *sums, int32_t *seq, int32_t *row0,
-                                             int *red, int &pairs) {
+                                             int *red, int &pairs, int &seqs) {
     const int tid = threadIdx.x;
     int carry = 0;
     if (tid == 0) blocks[0] = 0;
-    for (int base = 0; base < P.B; base += kN) {
-        const int b = base + tid;
-        int v = 0;
-        if (b < P.B) v = (load_seq(P, b).n * P.G + kMaxRows - 1) / kMaxRows;
-        const int sum = block_sums<kN>(v, carry, red);
-        if (b < P.B) blocks[b + 1] = sum;
+    for (seqs = P.B;; seqs = sequences<kN>(P.cu, P.B, red)) {  // (counted once where cu_new does not fall)
+        bool falls = false;
+        carry = 0;
+        for (int base = 0; base < seqs; base += kN) {
+            const int b = base + tid;
+            int v = 0;
+            if (b < seqs) v = (load_seq(P, b).n * P.G + kMaxRows - 1) / kMaxRows, falls |= P.cu[b + 1] < P.cu[b];
+            const int sum = block_sums<kN>(v, carry, red);
+            if (b < seqs) blocks[b + 1] = sum;
+        }
+        if (!__syncthreads_or(falls)) break;
     }
-    __syncthreads();
-    pairs = min(carry, P.most_pairs);  // more only of a cu_new that falls
+    pairs = min(carry, P.most_pairs);  // (what the tokens of that many sequences can make)
     carry = 0;
     if (tid == 0) sums[0] = 0;
     for (int base = 0; base < pairs; base += kN) {
         const int p = base + tid;
         int v = 0;
         if (p < pairs) {
-            const int b = last_not_above(blocks, P.B, p);
+            const int b = last_not_above(blocks, seqs, p);
             const int first = (p - blocks[b]) * kMaxRows;
             const Seq s = load_seq(P, b);
             v = (key_span(P, s, min(first + kMaxRows, s.n * P.G)).steps + kItemCost) * P.Hkv;
@@ -287,9 +291,9 @@ __global__ void __launch_bounds__(kScheduleThreads) schedule_kernel(const __grid
     __shared__ int32_t blocks[SSD_KV_MAX_B + 1];
     __shared__ int red[kScheduleThreads / 32];
     Workspace &W = *P.ws;
-    int pairs;
-    const int units = make_schedule<kScheduleThreads>(P, blocks, W.sums, W.seq, W.row0, red, pairs), used = ctas_of(ctas, units);
-    if (threadIdx.x == 0) W.pairs = pairs;
+    int pairs, seqs;
+    const int units = make_schedule<kScheduleThreads>(P, blocks, W.sums, W.seq, W.row0, red, pairs, seqs), used = ctas_of(ctas, units);
+    if (threadIdx.x == 0) W.pairs = pairs, W.seqs = seqs;
     for (int c = threadIdx.x; c < used; c += kScheduleThreads)
         W.start[c] = last_not_above(W.sums, pairs, first_unit(c, units, used));
 }
@@ -514,31 +518,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (tid == 0) tc::prefetch_map(&k_map), tc::prefetch_map(&v_map);
     // ---- schedule -------------------------------------------------------------------
     Walk walk;
-    int pairs = P.B;
+    int pairs, seqs = P.B;
     if constexpr (kOwn) {
         int32_t *blocks = sums_sh + kInside + 1, *seq = blocks + kInside + 1, *row0 = seq + kInside;
-        walk.units = make_schedule<kTreeThreads>(P, blocks, sums_sh, seq, row0, S.red, pairs);
+        walk.units = make_schedule<kTreeThreads>(P, blocks, sums_sh, seq, row0, S.red, pairs, seqs);
         walk.sums = sums_sh, walk.seq = seq, walk.row0 = row0;
     } else if (P.inside) {
         int carry = 0;
         if (tid == 0) sums_sh[0] = 0;
-        for (int b0 = 0; b0 < P.B; b0 += kTreeThreads) {
-            const int b = b0 + tid;
+        for (;; seqs = sequences<kTreeThreads>(P.cu, P.B, S.red)) {
+            static_assert(kInside <= kTreeThreads);
             int v = 0;
-            if (b < P.B) {
-                const Seq s = load_seq(P, b);
+            bool falls = false;
+            if (tid < seqs) {
+                const Seq s = load_seq(P, tid);
                 if (s.n > 0) v = (key_span(P, s, s.n * P.G).steps + kItemCost) * P.Hkv;
+                falls = P.cu[tid + 1] < P.cu[tid];
             }
+            carry = 0;
             const int sum = block_sums<kTreeThreads>(v, carry, S.red);
-            if (b < P.B) sums_sh[b + 1] = sum;
+            if (tid < seqs) sums_sh[tid + 1] = sum;
+            if (!__syncthreads_or(falls)) break;
         }
-        __syncthreads();
+        pairs = seqs;
         walk.sums = sums_sh;
         walk.units = carry;
         walk.seq = walk.row0 = nullptr;
     } else {
         walk.sums = P.ws->sums, walk.seq = P.ws->seq, walk.row0 = P.ws->row0;
-        walk.units = P.ws->sums[P.ws->pairs];
+        pairs = P.ws->pairs, seqs = P.ws->seqs;
+        walk.units = P.ws->sums[pairs];
     }
     walk.ctas = ctas_of(static_cast<int>(gridDim.x), walk.units);
     walk.cta = cta;
@@ -552,7 +561,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int64_t width = static_cast<int64_t>(P.Hq) * D;
         E *out = static_cast<E *>(P.out);
         const int64_t stride = static_cast<int64_t>(gridDim.x) * kTreeThreads;
-        const int served = min(max(P.cu[P.B], 0), P.T);
+        const int served = min(max(P.cu[seqs], 0), P.T);
         for (int64_t i = served * width + static_cast<int64_t>(cta) * kTreeThreads + tid; i < P.T * width; i += stride)
             out[i] = narrow<E>(0.f);
         for (int b = cta; b < P.B; b += gridDim.x) {
@@ -562,6 +571,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const bool fits = first >= 0 && next >= first && next <= P.T &&
                               (to == from || (keys >= 0 && keys <= P.max_blocks << P.page_shift));
             if (tid == 0 && (!fits || to - from > P.max_new)) report(P.dev_status, SSD_DEV_BAD_LENGTH);
+            if (b >= seqs) continue;
             for (int64_t i = (from + P.max_new) * width + tid; i < to * width; i += kTreeThreads) out[i] = narrow<E>(0.f);
         }
     }

@@ -40,9 +40,12 @@ struct TreePlanParams {
 // us).
 __global__ void __launch_bounds__(kTreeThreads) tree_plan_kernel(const __grid_constant__ TreePlanParams P) {
     __shared__ int32_t up[SSD_TREE_MAX];
+    __shared__ int room;
     const int b = blockIdx.x;
-    const TreeSeq s = tree_seq(P.cu, b, P.T, P.max_new);
+    TreeSeq s = tree_seq(P.cu, b, P.T, P.max_new);
     int bad = s.fits ? 0 : SSD_DEV_BAD_LENGTH;
+    const int seqs = sequences<kTreeThreads>(P.cu, P.B, &room);
+    if (b >= seqs) s.n = 0, s.to = s.first;
     int base = P.seq_len[b];
     if (base < 0 || base > 0x7FFFFFFF - SSD_TREE_MAX) base = 0, bad |= SSD_DEV_BAD_LENGTH;
     const int from = static_cast<int>(blockIdx.y) * kTreeThreads;
@@ -71,7 +74,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_plan_kernel(const __grid_co
         P.positions[t] = depth < 0 ? 0 : base + depth;
     }
     // entries behind the last sequence
-    const int end = min(max(P.cu[P.B], 0), P.T), block = static_cast<int>(blockIdx.y * gridDim.x) + b;
+    const int end = min(max(P.cu[seqs], 0), P.T), block = static_cast<int>(blockIdx.y * gridDim.x) + b;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * gridDim.y * kTreeThreads;
     for (int64_t t = static_cast<int64_t>(end) + static_cast<int64_t>(block) * kTreeThreads + threadIdx.x; t < P.T; t += stride) {
         P.positions[t] = 0;

@@ -539,3 +539,22 @@ def test_scores_of_any_size(ssd, dtype, size, sign):
         bound = half * np.abs(out) + (1 + half) * d * weight + 2.0 ** -24
         over = np.abs(got - out) - bound
         assert over.max() <= 0, (over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+@pytest.mark.parametrize("rest", [[40], [40, 60], [40, 60, 0, 90, 300], [0] * 300, [40, 90] * 200])
+@pytest.mark.parametrize("n", [50, 150])
+def test_a_batch_ends_where_its_token_counts_fall(ssd, n, rest):
+    """Sequences before the fall are what they are without the rest, and no other token has an owner."""
+    c = Case(41, [(400 + n, n)] + [(90, 0)] * len(rest), 8, 2, 64, 16, BF)
+    c.q = torch.cat([c.q, c.q])
+    c.sees = c.sees * 2
+    c.kv[:] = 400 + n
+    c.table[:] = c.table[0]
+    want = c.run(ssd)
+    assert want[:n].abs().sum() > 0 and not want[n:].any()
+    c.cu[2:] = rest[:len(c.cu) - 2]
+    c.cu[2] = min(c.cu[2], n - 1)
+    for _ in range(10):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        assert torch.equal(c.run(ssd, dev_status=status), want)
+        assert int(status) == ssd.SSD_DEV_BAD_LENGTH

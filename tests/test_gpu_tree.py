@@ -74,6 +74,23 @@ def test_plan_reports_lengths(ssd):
         assert int(status) & ssd.SSD_DEV_BAD_LENGTH, cu
 
 
+@pytest.mark.parametrize("rest", [[4], [4, 12], [4, 12, 0, 20, 90], [0] * 300, [7, 60] * 200])
+@pytest.mark.parametrize("n", [9, 140])
+def test_plan_of_a_batch_ends_where_its_token_counts_fall(ssd, n, rest):
+    """Sequences before the fall are what they are without the rest, and no other token has an owner."""
+    cu, parent, _ = trees(13, [n, 60])
+    seq = [5] + [1000] * len(rest)
+    want = ref.tree_plan(parent[:n], [0, n], [5], n + 60, n)
+    for _ in range(10):
+        out = {"positions": torch.full((n + 60,), 77, dtype=torch.int32, device="cuda"),
+               "mask": torch.full((n + 60, -(-n // 32)), 77, dtype=torch.int32, device="cuda")}
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ssd.ssd_tree_plan(dev(parent), dev([0, n] + rest), dev(seq), n, out=out, dev_status=status)
+        assert out["positions"].tolist() == want[0]
+        np.testing.assert_array_equal(out["mask"].cpu().numpy(), ref.words(want[1], -(-n // 32)))
+        assert int(status) & ssd.SSD_DEV_BAD_LENGTH
+
+
 # ---- accept -------------------------------------------------------------------------------
 
 def check_accept(ssd, cu, parent, tokens, sampled, max_new, max_path):
