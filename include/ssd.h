@@ -522,9 +522,10 @@ int ssd_kv_append(const void *k, const void *v, int dtype, int64_t k_stride, int
  * cu_new [B+1], kv_len [B] int32 as from ssd_kv_plan; max_new: a bound on the
  *   tokens of one sequence: a longer one's tokens beyond max_new get zeros, as does
  *   every token from cu_new[B] on.  SSD_DEV_BAD_LENGTH counts a sequence of more than
- *   max_new tokens, a cu_new that falls, is negative or passes T (it is cut to what is
- *   there), and a kv_len of a sequence with tokens that is negative or beyond
- *   max_blocks pages (whose keys beyond them are left out).
+ *   max_new tokens, a cu_new that falls (the batch ends there: sequences from it on have
+ *   no tokens), is negative or passes T (it is cut to what is there), and a kv_len of a
+ *   sequence with tokens that is negative or beyond max_blocks pages (whose keys beyond
+ *   them are left out).
  * A token that attends to nothing gets zeros.  What lies in masked places of the
  * cache, NaN among them, has no effect.  A page outside the cache counts as not
  * there (SSD_DEV_BAD_PAGE).
@@ -627,8 +628,7 @@ int ssd_tree_plan(const int32_t *parent, const int32_t *cu_new, const int32_t *s
  * attends to every position below kv_len[b] - n, and of the new tokens j <= i (at position
  * kv_len[b] - n + j) to those whose bit is set in its row of mask [T, W], W = ceil(max_new /
  * 32) (ssd_tree_plan, or any mask); with window > 0 only to the last `window` of those.
- * A mask whose bits j <= i are all set gives ssd_kv_attend's function.  A cu_new that falls ends
- * the batch as in ssd_tree_plan.
+ * A mask whose bits j <= i are all set gives ssd_kv_attend's function.
  * Everything else (layouts, scales, lengths, reports) as ssd_kv_attend, with max_new <=
  * SSD_TREE_MAX.
  * workspace: ssd_kv_tree_workspace_size() bytes, used as ssd_kv_attend's.

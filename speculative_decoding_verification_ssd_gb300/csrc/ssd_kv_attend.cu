@@ -69,7 +69,7 @@ struct Workspace {
     float o[2 * kMaxCtas][kMaxRows][kMaxHead];
     float2 ml[2 * kMaxCtas][kMaxRows];
     int32_t arrived[kMaxCtas];  // parts of the item that starts in each CTA; left at 0
-    int32_t pairs;              // of the schedule below
+    int32_t pairs, seqs;        // of the schedule below, and sequences in it
     int32_t sums[kMaxPairs + 1];  // steps before each pair
     int32_t seq[kMaxPairs];
     int32_t row0[kMaxPairs];
@@ -220,25 +220,29 @@ __global__ void __launch_bounds__(kScheduleThreads) schedule_kernel(const __grid
     __shared__ int32_t blocks[SSD_KV_MAX_B + 1];
     __shared__ int red[kScheduleThreads / 32];
     const int tid = threadIdx.x;
-    int carry = 0;
+    int carry = 0, seqs = P.B;
     if (tid == 0) blocks[0] = 0;
-    for (int base = 0; base < P.B; base += kScheduleThreads) {
-        const int b = base + tid;
-        int v = 0;
-        if (b < P.B) v = (load_seq(P, b).n * P.G + P.rows_per_item - 1) / P.rows_per_item;
-        const int sum = block_sums<kScheduleThreads>(v, carry, red);
-        if (b < P.B) blocks[b + 1] = sum;
+    for (;; seqs = sequences<kScheduleThreads>(P.cu, P.B, red)) {  // (counted once where cu_new does not fall)
+        bool falls = false;
+        carry = 0;
+        for (int base = 0; base < seqs; base += kScheduleThreads) {
+            const int b = base + tid;
+            int v = 0;
+            if (b < seqs) v = (load_seq(P, b).n * P.G + P.rows_per_item - 1) / P.rows_per_item, falls |= P.cu[b + 1] < P.cu[b];
+            const int sum = block_sums<kScheduleThreads>(v, carry, red);
+            if (b < seqs) blocks[b + 1] = sum;
+        }
+        if (!__syncthreads_or(falls)) break;
     }
-    __syncthreads();
-    const int pairs = min(carry, P.most_pairs);  // more only of a cu_new that falls
+    const int pairs = min(carry, P.most_pairs);  // (what the tokens of that many sequences can make)
     Workspace &W = *P.ws;
     carry = 0;
-    if (tid == 0) W.sums[0] = 0, W.pairs = pairs;
+    if (tid == 0) W.sums[0] = 0, W.pairs = pairs, W.seqs = seqs;
     for (int base = 0; base < pairs; base += kScheduleThreads) {
         const int p = base + tid;
         int v = 0;
         if (p < pairs) {
-            const int b = last_not_above(blocks, P.B, p);
+            const int b = last_not_above(blocks, seqs, p);
             const int row0 = (p - blocks[b]) * P.rows_per_item;
             const Seq s = load_seq(P, b);
             v = (key_span(P, s, row0, min(row0 + P.rows_per_item, s.n * P.G)).steps + P.item_cost) * P.Hkv;
@@ -435,39 +439,44 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     if (tid == 0) tc::prefetch_map(&k_map), tc::prefetch_map(&v_map);
     // ---- schedule -------------------------------------------------------------------
     Walk walk;
+    int seqs = P.B;
     if (P.inside) {
         int carry = 0;
         if (tid == 0) sums_sh[0] = 0;
-        for (int b0 = 0; b0 < P.B; b0 += kAttendThreads) {
-            const int b = b0 + tid;
+        for (;; seqs = sequences<kAttendThreads>(P.cu, P.B, S.red)) {
+            static_assert(kSeqsInside <= kAttendThreads, "");
             int v = 0;
-            if (b < P.B) {
-                const Seq s = load_seq(P, b);
+            bool falls = false;
+            if (tid < seqs) {
+                const Seq s = load_seq(P, tid);
                 if (s.n > 0) v = (key_span(P, s, 0, s.n * P.G).steps + P.item_cost) * P.Hkv;
+                falls = P.cu[tid + 1] < P.cu[tid];
             }
+            carry = 0;
             const int sum = block_sums<kAttendThreads>(v, carry, S.red);
-            if (b < P.B) sums_sh[b + 1] = sum;
+            if (tid < seqs) sums_sh[tid + 1] = sum;
+            if (!__syncthreads_or(falls)) break;
         }
-        __syncthreads();
         walk.sums = sums_sh;
         walk.units = carry;
         walk.seq = walk.row0 = nullptr;
     } else {
         walk.sums = P.ws->sums, walk.seq = P.ws->seq, walk.row0 = P.ws->row0;
+        seqs = P.ws->seqs;
         walk.units = P.ws->sums[P.ws->pairs];
     }
     walk.ctas = min(static_cast<int>(gridDim.x), walk.units);
     const bool busy = cta < walk.ctas;
     walk.unit = busy ? first_unit(cta, walk.units, walk.ctas) : 0;
     walk.end = busy ? first_unit(cta + 1, walk.units, walk.ctas) : 0;
-    walk.pair = !busy ? 0 : (P.inside ? last_not_above(sums_sh, P.B, walk.unit) : P.ws->start[cta]);
+    walk.pair = !busy ? 0 : (P.inside ? last_not_above(sums_sh, seqs, walk.unit) : P.ws->start[cta]);
 
     // Tokens that no item serves get zeros: those behind the last sequence's, and those beyond max_new.
     {
         const int64_t width = static_cast<int64_t>(P.Hq) * D;
         E *out = static_cast<E *>(P.out);
         const int64_t stride = static_cast<int64_t>(gridDim.x) * kAttendThreads;
-        const int served = min(max(P.cu[P.B], 0), P.T);
+        const int served = min(max(P.cu[seqs], 0), P.T);
         for (int64_t i = served * width + static_cast<int64_t>(cta) * kAttendThreads + tid; i < P.T * width; i += stride)
             out[i] = narrow<E>(0.f);
         for (int b = cta; b < P.B; b += gridDim.x) {
@@ -477,6 +486,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const bool fits = first >= 0 && next >= first && next <= P.T &&
                               (to == from || (keys >= 0 && keys <= P.max_blocks << P.page_shift));
             if (tid == 0 && (!fits || to - from > P.max_new)) report(P.dev_status, SSD_DEV_BAD_LENGTH);
+            if (b >= seqs) continue;
             for (int64_t i = (from + P.max_new) * width + tid; i < to * width; i += kAttendThreads) out[i] = narrow<E>(0.f);
         }
     }

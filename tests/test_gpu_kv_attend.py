@@ -363,3 +363,21 @@ def test_queries_with_one_large_channel(ssd, dtype, times):
     moved = 2.0 ** -17 * c.scale * np.abs(c.q.double().numpy()).max(axis=2, keepdims=True) * k
     bound = ref.attend_bound(dtype, c.D, *want) + 2 * moved * want[1]
     assert (np.abs(got - want[0]) <= bound).all()
+
+
+@pytest.mark.parametrize("rest", [[40], [40, 60], [40, 60, 0, 90, 300], [0] * 300, [40, 90] * 200])
+@pytest.mark.parametrize("n", [13, 150])
+def test_a_batch_ends_where_its_token_counts_fall(ssd, n, rest):
+    """Sequences before the fall are what they are without the rest, and no other token has an owner."""
+    c = Case(41, [(400 + n, n)] + [(90, 0)] * len(rest), 8, 2, 64, 16, BF)
+    c.q = torch.cat([c.q, c.q])
+    c.kv[:] = 400 + n
+    c.table[:] = c.table[0]
+    want = c.run(ssd)
+    assert want[:n].abs().sum() > 0 and not want[n:].any()
+    c.cu[2:] = rest
+    c.cu[2] = min(c.cu[2], n - 1)
+    for _ in range(10):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        assert torch.equal(c.run(ssd, dev_status=status), want)
+        assert int(status) == ssd.SSD_DEV_BAD_LENGTH
