@@ -100,6 +100,121 @@ __device__ __forceinline__ void store8(E *p, const float2 (&v)[4]) {
     }
 }
 
+// Cosines and sines of a lane's pairs, and the sines' negatives.
+struct Turns {
+    float2 c[4], s[4], n[4];
+};
+__device__ __forceinline__ Turns turns_of(const RopeParams &P, int t, int u) {
+    Turns r;
+    const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(P.positions[t]));
+    auto one = [&](int i, float &sine, float &cosine) {
+        const int f = P.interleaved ? (i < 4 ? 4 * u + i : P.R / 2 + 4 * u + i - 4) : 8 * u + i;
+        const int32_t left = static_cast<int32_t>((pos * __ldg(P.turns + f)) >> 32);
+        sincospif(static_cast<float>(left) * 4.656612873077393e-10f, &sine, &cosine);  // 2^-31: half turns
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        one(2 * i, r.s[i].x, r.c[i].x), one(2 * i + 1, r.s[i].y, r.c[i].y);
+        r.n[i] = make_float2(-r.s[i].x, -r.s[i].y);
+    }
+    return r;
+}
+__device__ __forceinline__ void turn(const RopeParams &P, const Turns &t, float2 (&v)[4], float2 (&z)[4]) {
+    if (P.interleaved) {
+        auto rotate = [](float2 &p, float cosine, float sine) {
+            p = make_float2(p.x * cosine - p.y * sine, p.x * sine + p.y * cosine);
+        };
+        rotate(v[0], t.c[0].x, t.s[0].x), rotate(v[1], t.c[0].y, t.s[0].y), rotate(v[2], t.c[1].x, t.s[1].x), rotate(v[3], t.c[1].y, t.s[1].y);
+        rotate(z[0], t.c[2].x, t.s[2].x), rotate(z[1], t.c[2].y, t.s[2].y), rotate(z[2], t.c[3].x, t.s[3].x), rotate(z[3], t.c[3].y, t.s[3].y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v0 = v[i], z0 = z[i];
+            v[i] = fma2(v0, t.c[i], mul2(z0, t.n[i]));
+            z[i] = fma2(v0, t.s[i], mul2(z0, t.c[i]));
+        }
+    }
+}
+
+// The lane's two runs of channels, and whether they are turned.
+struct Runs {
+    bool turned;
+    int a, b;
+};
+template <int D>
+__device__ __forceinline__ Runs runs_of(const RopeParams &P, int u) {
+    const bool turned = u < P.R / 8;
+    return {turned, turned ? 8 * u : P.R + 8 * u, turned ? P.R + 8 * u : D / 2 + 8 * u};
+}
+// A lane's head in a pass.
+template <int D>
+__device__ __forceinline__ bool head_of(const RopeParams &P, int pass, int sub, int &what, int &head) {
+    constexpr int kHeads = 512 / D;
+    const int passes_q = (P.Hq + kHeads - 1) / kHeads;
+    what = pass >= passes_q, head = (pass - (what ? passes_q : 0)) * kHeads + sub;
+    return head < (what ? P.H - P.Hq : P.Hq);
+}
+
+constexpr int kMostPasses = 32;  // of a warp
+
+// The heads that a warp has left out since fp32 may not hold their squares: brought to where the larger of their largest
+// channel and the root of eps is between 1 and 2, by a power of two that drops out of y.  Rare, and behind the kernel's loop,
+// whose registers it would take: 9472 tokens 41.1 us a call as a part of the loop, 39.4 here, 39.1 without.
+template <class E, int D, bool kVec>
+__device__ __noinline__ void odd_heads(const RopeParams &P, int t, int pass, uint32_t odd_passes, const float (*weights)[D]) {
+    constexpr int kLanes = D / 16;
+    const int lane = threadIdx.x & 31, u = lane % kLanes;
+    const Runs run = runs_of<D>(P, u);
+    for (; __any_sync(0xFFFFFFFFu, odd_passes != 0); pass += P.slices, odd_passes >>= 1) {
+        if (!__any_sync(0xFFFFFFFFu, odd_passes & 1)) continue;
+        const bool odd = odd_passes & 1;
+        int what, head;
+        head_of<D>(P, pass, lane / kLanes, what, head);
+        const int64_t at = static_cast<int64_t>(head) * D;
+        Raw<E> x, y;
+        if (odd) {
+            const E *p = static_cast<const E *>(P.x[what]) + t * P.x_stride[what] + at;
+            load8<E, kVec>(p + run.a, x);
+            load8<E, kVec>(p + run.b, y);
+        }
+        float2 v[4], z[4];
+        float top = sqrtf(P.eps);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = odd ? make_float2(wide(x.e[2 * i]), wide(x.e[2 * i + 1])) : make_float2(0.f, 0.f);
+            z[i] = odd ? make_float2(wide(y.e[2 * i]), wide(y.e[2 * i + 1])) : make_float2(0.f, 0.f);
+            top = fmaxf(fmaxf(top, fmaxf(fabsf(v[i].x), fabsf(v[i].y))), fmaxf(fabsf(z[i].x), fabsf(z[i].y)));
+        }
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        // (127 + the exponent of 1 / top, so that this is a normal number)
+        const int e = min(max(254 - static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
+        const float by = __uint_as_float(static_cast<uint32_t>(e) << 23);
+        const float2 by2 = make_float2(by, by);
+        float2 sum2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = mul2(v[i], by2), z[i] = mul2(z[i], by2);
+            sum2 = fma2(v[i], v[i], fma2(z[i], z[i], sum2));
+        }
+        float sum = sum2.x + sum2.y;
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float r = rsqrtf(sum * (1.f / D) + P.eps * by * by);
+        const float *w = weights[what];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = mul2(v[i], make_float2(r * w[run.a + 2 * i], r * w[run.a + 2 * i + 1]));
+            z[i] = mul2(z[i], make_float2(r * w[run.b + 2 * i], r * w[run.b + 2 * i + 1]));
+        }
+        if (!odd) continue;
+        if (run.turned) turn(P, turns_of(P, t, u), v, z);
+        E *p = static_cast<E *>(P.y[what]) + t * P.y_stride[what] + at;
+        store8<E, kVec>(p + run.a, v);
+        store8<E, kVec>(p + run.b, z);
+    }
+}
+
 template <class E, int D, bool kVec>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const __grid_constant__ RopeParams P) {
     constexpr int kLanes = D / 16;       // of a head
@@ -114,11 +229,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const _
     if (unit >= P.units) return;
     const int t = static_cast<int>(unit / P.slices), slice = static_cast<int>(unit - static_cast<int64_t>(t) * P.slices);
 
-    // the lane's two runs of channels
-    const bool turned = u < P.R / 8;
-    const int a = turned ? 8 * u : P.R + 8 * u;
-    const int b = turned ? P.R + 8 * u : D / 2 + 8 * u;
+    const Runs run = runs_of<D>(P, u);
+    const bool turned = run.turned;
+    const int a = run.a, b = run.b;
     const int passes_q = (P.Hq + kHeads - 1) / kHeads, passes = passes_q + (P.H - P.Hq + kHeads - 1) / kHeads;
+    uint32_t odd_passes = 0, this_pass = 1;  // passes in which the lane's head is one for odd_heads; at most kMostPasses
     struct {
         Raw<E> x, y;
     } next;  // the next pass, on its way
@@ -131,20 +246,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const _
         }
     };
     fetch(slice);
-    float2 c[4], s[4], n[4];  // cosines, sines and their negatives
-    if (turned) {
-        const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(P.positions[t]));
-        auto turn = [&](int i, float &sine, float &cosine) {
-            const int f = P.interleaved ? (i < 4 ? 4 * u + i : P.R / 2 + 4 * u + i - 4) : 8 * u + i;
-            const int32_t left = static_cast<int32_t>((pos * __ldg(P.turns + f)) >> 32);
-            sincospif(static_cast<float>(left) * 4.656612873077393e-10f, &sine, &cosine);  // 2^-31: half turns
-        };
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            turn(2 * i, s[i].x, c[i].x), turn(2 * i + 1, s[i].y, c[i].y);
-            n[i] = make_float2(-s[i].x, -s[i].y);
-        }
-    }
+    Turns turns;
+    if (turned) turns = turns_of(P, t, u);
 #pragma unroll 1
     for (int pass = slice; pass < passes; pass += P.slices) {
         const int what = pass >= passes_q, head = (pass - (what ? passes_q : 0)) * kHeads + sub;
@@ -156,6 +259,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const _
             z[i] = there ? make_float2(wide(next.y.e[2 * i]), wide(next.y.e[2 * i + 1])) : make_float2(0.f, 0.f);
         }
         fetch(pass + P.slices);
+        bool odd = false;  // squares that fp32 may not hold
         if (P.w[0]) {
             float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -163,7 +267,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const _
             float sum = sum2.x + sum2.y;
 #pragma unroll
             for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-            const float r = rsqrtf(sum * (1.f / D) + P.eps);
+            const float mean = sum * (1.f / D) + P.eps;  // (next to a larger eps small squares do not count)
+            odd = there && !(mean >= 0x1p-80f && mean <= 0x1p120f);
+            odd_passes |= odd ? this_pass : 0u;
+            this_pass <<= 1;
+            const float r = rsqrtf(mean);
             const float2 r2 = make_float2(r, r);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -175,28 +283,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const _
                 z[2 * i + 1] = mul2(z[2 * i + 1], mul2(r2, make_float2(q.z, q.w)));
             }
         }
-        if (turned) {
-            if (P.interleaved) {
-                auto rotate = [](float2 &p, float cosine, float sine) {
-                    p = make_float2(p.x * cosine - p.y * sine, p.x * sine + p.y * cosine);
-                };
-                rotate(v[0], c[0].x, s[0].x), rotate(v[1], c[0].y, s[0].y), rotate(v[2], c[1].x, s[1].x), rotate(v[3], c[1].y, s[1].y);
-                rotate(z[0], c[2].x, s[2].x), rotate(z[1], c[2].y, s[2].y), rotate(z[2], c[3].x, s[3].x), rotate(z[3], c[3].y, s[3].y);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 v0 = v[i], z0 = z[i];
-                    v[i] = fma2(v0, c[i], mul2(z0, n[i]));
-                    z[i] = fma2(v0, s[i], mul2(z0, c[i]));
-                }
-            }
-        }
-        if (there) {
+        if (turned) turn(P, turns, v, z);
+        if (there && !odd) {
             E *p = static_cast<E *>(P.y[what]) + t * P.y_stride[what] + static_cast<int64_t>(head) * D;
             store8<E, kVec>(p + a, v);
             store8<E, kVec>(p + b, z);
         }
     }
+    if (__any_sync(0xFFFFFFFFu, odd_passes != 0)) odd_heads<E, D, kVec>(P, t, slice, odd_passes, weights);
 }
 
 template <class E, int D>
@@ -241,6 +335,8 @@ extern "C" int ssd_qk_rope(const void *q, const void *k, int dtype, int64_t q_st
     P.slices = 1;
     while (P.slices < passes && static_cast<int64_t>(T) * P.slices < 32 * 152) P.slices *= 2;
     if (P.slices > passes) P.slices = passes;
+    // (a warp has no more passes than it has marks for)
+    if (P.slices < (passes + kMostPasses - 1) / kMostPasses) P.slices = (passes + kMostPasses - 1) / kMostPasses;
     P.units = static_cast<int64_t>(T) * P.slices;
     const int es = dtype == SSD_F32 ? 4 : 2;
     const bool vec = aligned(q, 16) && aligned(k, 16) && aligned(q_out, 16) && aligned(k_out, 16) && q_stride * es % 16 == 0 &&

@@ -149,3 +149,45 @@ def test_in_a_graph_and_on_another_stream(ssd):
     graph.replay()
     torch.cuda.synchronize()
     c.near(out, c.want())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,Hkv", [(64, 2), (128, 3)])
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-30])
+def test_norms_of_heads_of_any_size(ssd, dtype, D, Hkv, eps):
+    """Squares that fp32 does not hold, large or small, in a head by itself or next to ordinary ones; one channel far above the
+    rest; and eps above, among or below the squares."""
+    c = Case(9, 9, 9, Hkv, D, D, dtype)
+    c.eps = eps
+    for h, size in enumerate((1e25, 1e-25, 1e-12, 1e19, 3e37, 1.0, 1e-38, 1e-21)):
+        c.q[:, h] *= size
+    c.q[:, 3, 5] = 1e30
+    c.k[1::2, 0] *= 1e22
+    c.k[2, 1:] *= 1e-30
+    assert not torch.isinf(c.q).any() and not torch.isinf(c.k).any()
+    got = ssd.ssd_qk_rope(c.q, c.k, c.positions, ssd.rope_turns(c.inv_freq.tolist()), **c.args(ssd))
+    # below the normal range, which the bound leaves out: half a step of the output's smallest, and the smallest step of fp32
+    # for each of a rotation's three roundings
+    tiny = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps / 2 + 3 * 2.0 ** -149
+    for g, (y, size) in zip(got, c.want()):
+        over = np.abs(g.double().cpu().numpy() - y) - ref.rope_bound(dtype, y, size, c.far) - tiny
+        assert over.max() <= 0, (over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+def test_many_heads(ssd):
+    """More heads than a warp has marks for those of odd size, with enough tokens that each has a warp: any token's results are those
+    that it has by itself, odd heads, in place and not."""
+    c = Case(10, 50, 300, 8, 64, 64, BF)
+    for h, size in ((0, 1e25), (7, 1e-30), (8, 1e22), (150, 1e25), (299, 1e30)):
+        c.q[:, h] *= size
+    c.k[:, 7] *= 1e25
+    c.eps = 0.0
+    turns = ssd.rope_turns(c.inv_freq.tolist())
+    want = ssd.ssd_qk_rope(c.q, c.k, c.positions, turns, **c.args(ssd))
+    c.near([x[:3] for x in want], [(y[:3], z[:3]) for y, z in c.want()])
+    q, k, positions = c.q.repeat(110, 1, 1), c.k.repeat(110, 1, 1), c.positions.repeat(110)
+    got = ssd.ssd_qk_rope(q, k, positions, turns, **c.args(ssd))
+    for g, w in zip(got, want):
+        assert torch.equal(g.view(110, *w.shape), w[None].expand(110, -1, -1, -1))
+    ssd.ssd_qk_rope(q, k, positions, turns, q_out=q, k_out=k, **c.args(ssd))
+    assert torch.equal(q, got[0]) and torch.equal(k, got[1])
