@@ -33,11 +33,16 @@ struct CompactParams {
     int32_t *dev_status;
 };
 
-// The smallest power of two 2^k, k >= -100, with amax <= 448 * 2^k (448 is 1.75 * 2^8).
+// A byte times a large scale may pass fp32 (a bf16 value next to its type's largest is held so): magnitudes are 2^-kDown of
+// theirs.  What that makes inexact is far below the smallest need.
+constexpr int kDown = 16;
+constexpr float kDownBy = 1.f / (1 << kDown);
+
+// The smallest power of two 2^k, -100 <= k <= 127, with amax <= 448 * 2^k (448 is 1.75 * 2^8), of 2^-kDown amax.
 __device__ __forceinline__ float needed_scale(float amax) {
     const uint32_t u = __float_as_uint(amax);
-    int k = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    k = k < -100 ? -100 : k;
+    int k = static_cast<int>(u >> 23) + kDown - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    k = min(max(k, -100), 127);
     return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
 
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_c
         const uint32_t got = __shfl_sync(kAll, m, (lane % kStep) * kLanes);
         if (lane / kStep == i) {
             const uint32_t two = halves_of_e4m3x2(got);
-            amax = __half22float2(*reinterpret_cast<const __half2 *>(&two)).x * fabsf(from_scale);
+            amax = __half22float2(*reinterpret_cast<const __half2 *>(&two)).x * (fabsf(from_scale) * kDownBy);
         }
     }
     if (!comes || !(amax <= kMost)) amax = 0.f;
@@ -180,7 +185,8 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_c
         if (k >= a) continue;
         uint4 *to_at = reinterpret_cast<uint4 *>(cache + row * D + part * 16);
         if (other)
-            *to_at = s == over ? held[i] : restored(held[i], s, over);
+            // (the quotient of both's 2^-kDown is the same)
+            *to_at = s == over ? held[i] : (s > 1.f ? restored(held[i], s * kDownBy, over * kDownBy) : restored(held[i], s, over));
         else if (r != 1.f)
             *to_at = restored(held[i], r, 0.f);
         else if (row != was)

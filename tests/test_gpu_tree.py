@@ -218,6 +218,33 @@ def test_compact_with_odd_values(ssd):
         c.run(ssd, paths(c.rng, accept, 60, 9), accept, c.rng.integers(0, 30, 12))
 
 
+@pytest.mark.parametrize("k", [100, 119, 120, 121, 123])
+def test_compact_of_values_next_to_the_largest(ssd, k):
+    """A byte times its page's scale may pass fp32: 3.3e38 in bf16 is stored as 256 * 2^120.  The scale
+    grows to hold the largest all the same, and powers of two leave the values exact."""
+    c = Cache(6, 3, 100, 2, 64, 16)
+    c.codes[0][:] = CODE[1.0]
+    c.scales[0][:], c.scales[1][:] = 1.0, 1.0
+    path, accept, keep = np.array([[0, 20, 37, 40]] * 3), np.full(3, 3), np.array([2, 3, 9])
+    byte = {100: 448.0, 119: 448.0, 120: 256.0, 121: 240.0, 123: 416.0}[k]
+    for b in range(3):
+        pages = c.table[b][[(int(keep[b]) + n) // 16 for n in (20, 37, 40)]]
+        c.scales[0][pages] = 2.0 ** k
+        for n, page in zip((20, 37, 40), pages):
+            c.codes[0][page, :, (keep[b] + n) % 16, 5] = CODE[byte]
+    got, status = c.run(ssd, path, accept, keep, check=False)
+    assert status == 0
+    need = 2.0 ** int(np.ceil(np.log2(byte / 448) + k))
+    for b in range(3):
+        page, at = c.table[b][int(keep[b]) // 16], (int(keep[b]) + np.arange(4)) % 16
+        assert (got[2][page] == need).all()
+        want = np.full((2, 3, 64), 2.0 ** k)
+        want[:, :, 5] = byte * 2.0 ** k
+        np.testing.assert_array_equal(VALUES[got[0][page][:, at[1:]]] * need, np.where(want / need < 2.0 ** -9, 0, want))
+        # rows that were there, of ones, are nothing under the new scale
+        assert not VALUES[got[0][page][:, :at[0] + 1]].any()
+
+
 def test_compact_leaves_a_sequence_that_it_cannot_move(ssd):
     path = np.array([[0, 2, 3, 7], [0, 1, 5, 6]])
 
