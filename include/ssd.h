@@ -641,6 +641,25 @@ int ssd_kv_attend_tree(const void *q, int dtype, int64_t q_stride, const void *k
                        void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
+ * Check of ssd_kv_attend_tree's bounded waits (no counterpart on the pages): the same call, in which each CTA of
+ * three steps of 128 keys or more leaves out one signal of its third, so that the waits for it run out (after some
+ * 20 ms; 4 s in ssd_kv_attend_tree), SSD_DEV_TIMEOUT is set and the launch ends normally.  What it leaves in out is not
+ * to be used, and the workspace is to be zeroed again.  withheld: one of SSD_CHECK_...; bf16, heads of 64, 256 rows (tokens of one sequence
+ * times Hq / Hkv) at most.
+ */
+#define SSD_CHECK_STEPS 1   /* a step */
+#define SSD_CHECK_WEIGHTS 2 /* a softmax warp's weights */
+#define SSD_CHECK_VALUES 3  /* values as halves */
+#define SSD_CHECK_COPIES 4  /* a copy of keys */
+#define SSD_CHECK_SCORES 5  /* the end of the scores' products */
+int ssd_check_tree_timeout(int withheld, const void *q, int dtype, int64_t q_stride, const void *k_cache,
+                           const void *v_cache, const float *k_scale, const float *v_scale, int num_pages,
+                           int page_size, int Hq, int Hkv, int D, const int32_t *block_table, int max_blocks,
+                           const int32_t *cu_new, const int32_t *kv_len, const int32_t *mask, int B, int T,
+                           int max_new, float sm_scale, int window, void *out, void *workspace,
+                           size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
  * ssd_tree_accept -- follows the target's own draws down each tree: from node 0 to the first
  * child whose token is the draw at the node, until no child is or the path has max_path nodes.
  * The tokens of the path and the draw at its end are then distributed as the target's, whatever

@@ -58,7 +58,7 @@ ABI_SYMBOLS = ("ssd_strerror", "ssd_version", "ssd_workspace_size", "ssd_verify"
                "ssd_host_staging_size", "ssd_round_host", "ssd_last_kernel", "ssd_workspace_size_v",
                "ssd_kv_plan", "ssd_kv_append", "ssd_kv_workspace_size", "ssd_kv_attend", "ssd_sample",
                "ssd_qk_rope", "ssd_tree_plan", "ssd_kv_tree_workspace_size", "ssd_kv_attend_tree", "ssd_tree_accept",
-               "ssd_kv_compact")
+               "ssd_kv_compact", "ssd_check_tree_timeout")
 
 
 class SSDError(RuntimeError):
@@ -153,6 +153,8 @@ def lib() -> ctypes.CDLL:
         L.ssd_kv_tree_workspace_size.restype = z
         L.ssd_kv_attend_tree.argtypes = [P, i, n, P, P, P, P, i, i, i, i, i, P, i, P, P, P, i, i, i, f, i, P, P, z, P, P]
         L.ssd_kv_attend_tree.restype = i
+        L.ssd_check_tree_timeout.argtypes = [i] + L.ssd_kv_attend_tree.argtypes
+        L.ssd_check_tree_timeout.restype = i
         L.ssd_tree_accept.argtypes = [P, P, P, P, i, i, i, i, P, P, P, P, P]
         L.ssd_tree_accept.restype = i
         L.ssd_kv_compact.argtypes = [P, P, P, i, i, P, i, i, i, P, P, P, P, i, i, P, P]

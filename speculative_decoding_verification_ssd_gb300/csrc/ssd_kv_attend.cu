@@ -361,10 +361,10 @@ struct Shared {
     int red[kAttendWarps];
 };
 
-// Waits are bounded by a number of polls (each may suspend the thread for a while: seconds in all, far
+// Waits are bounded by a number of polls (each suspends the thread for 4 us at most: 4 s in all, far
 // more than any step takes).  When one runs out, `gave_up` is set and every role leaves its loop without
 // waiting for the others; barriers that a whole group shares are met by all of it or by none.
-constexpr int kPolls = 1 << 22;
+constexpr int kPolls = 1 << 20;
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
     int polls = 0;
     while (!mbar_try_wait(bar, parity)) {
@@ -1188,11 +1188,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         }
     }
     __syncwarp();
-    if (tid == 0 && gave_up()) report(P.dev_status, SSD_DEV_TIMEOUT);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     if (gave_up()) {
+        if (tid == 0) report(P.dev_status, SSD_DEV_TIMEOUT);
         // Some role left early, perhaps after the ones that issue copies and products had left: what they issued still
         // has to end before the CTA does.
         if (warp == 12) {

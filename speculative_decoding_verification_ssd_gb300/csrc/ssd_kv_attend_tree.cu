@@ -112,6 +112,7 @@ struct TreeParams {
     int window;
     int inside;      // a sequence is a pair, and the schedule made by every CTA in shared memory
     int most_pairs;  // (sequence, row block) pairs that T tokens of B sequences can make
+    int withheld;    // SSD_CHECK_..., 0: none
     void *out;
     Workspace *ws;
     int32_t *dev_status;
@@ -420,13 +421,14 @@ struct Shared {
 
 // A whole warp waits, and its lanes get the same answer: loops and branches that the compiler takes for divergent cost
 // this kernel more than anything else in a wait (one lane that waits for all: 411 us in place of 288).  Waits are
-// bounded by a number of polls (each may suspend the warp for a while: seconds in all, far more than any step takes).
+// bounded by a number of polls (each suspends the warp for 4 us at most: 4 s in all, far more than any step takes).
 // When one runs out, `gave_up` is set and every role leaves its loop without waiting for the others; no role meets
 // another at a barrier that is not waited for in this way.
-constexpr int kPolls = 1 << 22;
+constexpr int kPolls = 1 << 20, kPollsChecked = 1 << 12;
+template <int kLimit>
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
     for (int polls = 0; !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)); ++polls) {
-        if (__any_sync(0xFFFFFFFFu, *gave_up) || polls == kPolls) {
+        if (__any_sync(0xFFFFFFFFu, *gave_up) || polls == kLimit) {
             *gave_up = 1;
             return false;
         }
@@ -434,8 +436,9 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volat
     return true;
 }
 // The same for what has to end whether or not a wait ran out.
+template <int kLimit>
 __device__ __forceinline__ void drain_phase(uint64_t *bar, uint32_t parity) {
-    for (int i = 0; i < kPolls && !mbar_try_wait(bar, parity); ++i) {
+    for (int i = 0; i < kLimit && !mbar_try_wait(bar, parity); ++i) {
     }
 }
 
@@ -496,7 +499,9 @@ __device__ __forceinline__ void row_keys(const TreeParams &P, const Row &r, int 
 }
 
 // kOwn: a schedule of several row blocks to a sequence is made by every CTA (as a branch it cost the others 1%).
-template <class F, bool kOwn>
+// kChecked: the form of ssd_check_tree_timeout: in each CTA the third step's signal of role P.withheld is left out, so that
+// the waits for it run out, after kPollsChecked polls.
+template <class F, bool kOwn, bool kChecked = false>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_kernel(const __grid_constant__ TreeParams P, const __grid_constant__ CUtensorMap k_map,
                 const __grid_constant__ CUtensorMap v_map) {
@@ -609,7 +614,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     else
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
 
-    auto wait = [&](uint64_t *bar, int parity) { return wait_phase(bar, static_cast<uint32_t>(parity), &S.gave_up); };
+    constexpr int kWait = kChecked ? kPollsChecked : kPolls;
+    auto wait = [&](uint64_t *bar, int parity) { return wait_phase<kWait>(bar, static_cast<uint32_t>(parity), &S.gave_up); };
+    auto withheld = [&](int role, int step) { return kChecked && P.withheld == role && step == 2; };
     auto gave_up = [&] { return *static_cast<volatile int *>(&S.gave_up) != 0; };
     // The flags of step s, for all lanes of a warp; 0 at the end, or where a wait ran out.
     auto open_step = [&](int s) {
@@ -820,7 +827,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     tc::tmem_wait_store();
                     tc::fence_before();
                 }
-                arrive(&S.p_full[group]);
+                if (withheld(SSD_CHECK_WEIGHTS, it) && quad == 0)
+                    __syncwarp();
+                else
+                    arrive(&S.p_full[group]);
             }
             if (flags & kEnds) {
                 // ---- the item's output, or this part's share of it ----
@@ -1113,7 +1123,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (met) atomicExch(&S.nan_met[st.item], 1);
             tc::fence_async_shared();
             __syncwarp();
-            tc::warp_arrive(&S.h_full[buf]);
+            if (!(withheld(SSD_CHECK_VALUES, it) && w4 == 0)) tc::warp_arrive(&S.h_full[buf]);
             tc::warp_arrive(&S.v_empty[slot]);
             tc::warp_arrive(&S.step_free[it % kSteps]);
         }
@@ -1129,9 +1139,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const int y = mine ? (st.page[lane] * P.Hkv + st.head) << P.page_shift : 0;
             const int k_slot = n % F::kKeys, v_slot = n % F::kValues;
             if (n >= F::kKeys && !wait(&S.k_empty[k_slot], (n / F::kKeys - 1) & 1)) break;
-            tc::warp_arrive_expect(&S.k_full[k_slot], static_cast<uint32_t>(bytes));
+            const bool copied = !withheld(SSD_CHECK_COPIES, n);
+            if (copied) tc::warp_arrive_expect(&S.k_full[k_slot], static_cast<uint32_t>(bytes));
             __syncwarp();
-            if (mine) tc::tma_load_2d(k_sh + k_slot * F::kSlot + lane * (16 * D), &k_map, 0, y, &S.k_full[k_slot]);
+            if (copied && mine) tc::tma_load_2d(k_sh + k_slot * F::kSlot + lane * (16 * D), &k_map, 0, y, &S.k_full[k_slot]);
             S.k_issued = n + 1;
             if (n >= F::kValues && !wait(&S.v_empty[v_slot], (n / F::kValues - 1) & 1)) break;
             tc::warp_arrive_expect(&S.v_full[v_slot], static_cast<uint32_t>(bytes));
@@ -1209,7 +1220,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)  // 32 channels further inside the swizzled rows
                     tc::warp_mma_e4m3(s_at, q + ((d * F::kSlot + k * 32) >> 4), k8 + (k * 32 >> 4), kScores, d + k > 0);
-            tc::warp_mma_commit(&S.s_full[e & 1]);
+            if (!withheld(SSD_CHECK_SCORES, n)) tc::warp_mma_commit(&S.s_full[e & 1]);
             if (last && (flags & kEnds)) tc::warp_mma_commit(&S.q_free);
             if (before) output_done();
             if (behind == 0)
@@ -1307,7 +1318,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         }
                     }
                     event += passes;
-                    arrive(&S.step_full[slot]);
+                    if (withheld(SSD_CHECK_STEPS, s))
+                        __syncwarp();
+                    else
+                        arrive(&S.step_full[slot]);
                 }
             }
             ++items;
@@ -1321,24 +1335,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
     }
     __syncwarp();
-    if (tid == 0 && gave_up()) report(P.dev_status, SSD_DEV_TIMEOUT);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     if (gave_up()) {
+        if (tid == 0) report(P.dev_status, SSD_DEV_TIMEOUT);
         // Some role left early, perhaps after the ones that issue copies and products had left: what they issued still
         // has to end before the CTA does.
         if (warp == 12) {
             const int k = S.k_issued, v = S.v_issued;
 #pragma unroll 1
-            for (int x = max(0, k - F::kKeys); x < k; ++x) drain_phase(&S.k_full[x % F::kKeys], (x / F::kKeys) & 1);
+            for (int x = max(0, k - F::kKeys); x < k; ++x) drain_phase<kWait>(&S.k_full[x % F::kKeys], (x / F::kKeys) & 1);
 #pragma unroll 1
-            for (int x = max(0, v - F::kValues); x < v; ++x) drain_phase(&S.v_full[x % F::kValues], (x / F::kValues) & 1);
+            for (int x = max(0, v - F::kValues); x < v; ++x) drain_phase<kWait>(&S.v_full[x % F::kValues], (x / F::kValues) & 1);
         }
         if (warp == 13) {
             if (lane == 0) tc::mma_commit(&S.drained);
             __syncwarp();
-            drain_phase(&S.drained, 0);
+            drain_phase<kWait>(&S.drained, 0);
         }
     }
     if (warp == 13) tc::tmem_free(tmem, 512);
@@ -1358,9 +1372,9 @@ int device_limits(Device *d) {
     return SSD_OK;
 }
 
-template <class F, bool kOwn>
+template <class F, bool kOwn, bool kChecked = false>
 int tree_run(const TreeParams &P, const CUtensorMap &k_map, const CUtensorMap &v_map, const Device &dev, int ctas, cudaStream_t stream) {
-    auto *kernel = tree_kernel<F, kOwn>;
+    auto *kernel = tree_kernel<F, kOwn, kChecked>;
     constexpr int dyn = F::kBytes + static_cast<int>(sizeof(Shared<F>)) + (kOwn ? 4 * kInside + 2 : kInside + 1) * 4;
     static_assert(dyn <= 227 * 1024);
     if (dyn > dev.smem_cta) return SSD_ERR_UNSUPPORTED;
@@ -1388,6 +1402,11 @@ int tree_launch(TreeParams P, const CUtensorMap &k_map, const CUtensorMap &v_map
     P.inside = P.B <= kInside && static_cast<int64_t>(P.max_new) * P.G <= kMaxRows;
     const int64_t most = static_cast<int64_t>(P.T) * P.G / kMaxRows + P.B;
     P.most_pairs = static_cast<int>(most < kMaxPairs ? most : kMaxPairs);
+    if (P.withheld) {
+        if constexpr (__is_same(typename F::E, __nv_bfloat16) && F::D == 64)
+            if (P.inside) return tree_run<F, false, true>(P, k_map, v_map, dev, ctas, stream);
+        return SSD_ERR_UNSUPPORTED;
+    }
     if (P.inside) return tree_run<F, false>(P, k_map, v_map, dev, ctas, stream);
     // A schedule in the workspace takes a launch of its own (6 sequences of up to 509 nodes: 58.5 us, and 62.6 with it).
     if (most <= kInside) return tree_run<F, true>(P, k_map, v_map, dev, ctas, stream);
@@ -1397,18 +1416,11 @@ int tree_launch(TreeParams P, const CUtensorMap &k_map, const CUtensorMap &v_map
     return tree_run<F, false>(P, k_map, v_map, dev, ctas, stream);
 }
 
-}  // namespace
-}  // namespace ssd
-
-extern "C" size_t ssd_kv_tree_workspace_size(void) { return (sizeof(ssd::Workspace) + 255) / 256 * 256; }
-
-extern "C" int ssd_kv_attend_tree(const void *q, int dtype, int64_t q_stride, const void *k_cache, const void *v_cache,
-                                  const float *k_scale, const float *v_scale, int num_pages, int page_size, int Hq,
-                                  int Hkv, int D, const int32_t *block_table, int max_blocks, const int32_t *cu_new,
-                                  const int32_t *kv_len, const int32_t *mask, int B, int T, int max_new, float sm_scale,
-                                  int window, void *out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
-                                  void *stream) {
-    using namespace ssd;
+int attend_tree(const void *q, int dtype, int64_t q_stride, const void *k_cache, const void *v_cache, const float *k_scale,
+                const float *v_scale, int num_pages, int page_size, int Hq, int Hkv, int D, const int32_t *block_table,
+                int max_blocks, const int32_t *cu_new, const int32_t *kv_len, const int32_t *mask, int B, int T, int max_new,
+                float sm_scale, int window, void *out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                void *stream, int withheld) {
     if (dtype != SSD_BF16 && dtype != SSD_F16) return SSD_ERR_DTYPE;
     if (B < 1 || T < 0 || max_new < 1 || num_pages < 1 || max_blocks < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 ||
         window < 0 || !kv_page_size_ok(page_size) || (D != 64 && D != 128))
@@ -1443,6 +1455,7 @@ extern "C" int ssd_kv_attend_tree(const void *q, int dtype, int64_t q_stride, co
     P.scale = scale, P.window = window, P.out = out;
     P.ws = static_cast<Workspace *>(workspace);
     P.dev_status = dev_status;
+    P.withheld = withheld;
     Device dev;
     if (device_limits(&dev) != SSD_OK) return SSD_ERR_CUDA;
     CUtensorMap k_map, v_map;
@@ -1454,4 +1467,32 @@ extern "C" int ssd_kv_attend_tree(const void *q, int dtype, int64_t q_stride, co
         return D == 64 ? tree_launch<Form<__nv_bfloat16, 64>>(P, k_map, v_map, dev, s)
                        : tree_launch<Form<__nv_bfloat16, 128>>(P, k_map, v_map, dev, s);
     return D == 64 ? tree_launch<Form<__half, 64>>(P, k_map, v_map, dev, s) : tree_launch<Form<__half, 128>>(P, k_map, v_map, dev, s);
+}
+
+}  // namespace
+}  // namespace ssd
+
+extern "C" size_t ssd_kv_tree_workspace_size(void) { return (sizeof(ssd::Workspace) + 255) / 256 * 256; }
+
+extern "C" int ssd_kv_attend_tree(const void *q, int dtype, int64_t q_stride, const void *k_cache, const void *v_cache,
+                                  const float *k_scale, const float *v_scale, int num_pages, int page_size, int Hq,
+                                  int Hkv, int D, const int32_t *block_table, int max_blocks, const int32_t *cu_new,
+                                  const int32_t *kv_len, const int32_t *mask, int B, int T, int max_new, float sm_scale,
+                                  int window, void *out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                  void *stream) {
+    return ssd::attend_tree(q, dtype, q_stride, k_cache, v_cache, k_scale, v_scale, num_pages, page_size, Hq, Hkv,
+                            D, block_table, max_blocks, cu_new, kv_len, mask, B, T, max_new, sm_scale, window,
+                            out, workspace, workspace_bytes, dev_status, stream, 0);
+}
+
+extern "C" int ssd_check_tree_timeout(int withheld, const void *q, int dtype, int64_t q_stride, const void *k_cache,
+                                      const void *v_cache, const float *k_scale, const float *v_scale, int num_pages,
+                                      int page_size, int Hq, int Hkv, int D, const int32_t *block_table, int max_blocks,
+                                      const int32_t *cu_new, const int32_t *kv_len, const int32_t *mask, int B, int T,
+                                      int max_new, float sm_scale, int window, void *out, void *workspace,
+                                      size_t workspace_bytes, int32_t *dev_status, void *stream) {
+    if (withheld < SSD_CHECK_STEPS || withheld > SSD_CHECK_SCORES) return SSD_ERR_INVALID_ARG;
+    return ssd::attend_tree(q, dtype, q_stride, k_cache, v_cache, k_scale, v_scale, num_pages, page_size, Hq, Hkv,
+                            D, block_table, max_blocks, cu_new, kv_len, mask, B, T, max_new, sm_scale, window,
+                            out, workspace, workspace_bytes, dev_status, stream, withheld);
 }

@@ -558,3 +558,27 @@ def test_a_batch_ends_where_its_token_counts_fall(ssd, n, rest):
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         assert torch.equal(c.run(ssd, dev_status=status), want)
         assert int(status) == ssd.SSD_DEV_BAD_LENGTH
+
+
+@pytest.mark.parametrize("withheld", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("n", [20, 50])
+def test_waits_that_run_out_end_the_launch(ssd, n, withheld):
+    """One signal left out in every CTA: each role leaves by itself, the status says so, and the next call is as ever."""
+    import ctypes
+    c = Case(42, [(40000, n), (300, 3), (129, 4)], 4, 1, 64, 64, BF)
+    want = c.run(ssd)
+    q, out, status = c.q.cuda(), torch.empty_like(want), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = ssd.kv_tree_workspace()
+    held = [dev(a) for a in (c.k, c.v, c.ks, c.vs, c.table, c.cu, c.kv, ref.words(c.sees, -(-c.max_new // 32)))]
+    k, v, ks, vs, table, cu, kv, mask = (t.data_ptr() for t in held)
+    T, Hq, D = q.shape
+    call = (q.data_ptr(), ssd.SSD_BF16, Hq * D, k, v, ks, vs, len(c.k), c.P, Hq, 1, D, table, c.table.shape[1], cu, kv, mask, 3, T, c.max_new,
+            ctypes.c_float(c.scale), 0, out.data_ptr(), ws.data_ptr(), ws.numel(), status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert ssd.lib().ssd_check_tree_timeout(withheld, *call) == ssd.SSD_OK
+    torch.cuda.synchronize()
+    assert int(status) == ssd.SSD_DEV_TIMEOUT
+    ws.zero_()
+    status.zero_()
+    out.zero_()
+    assert ssd.lib().ssd_kv_attend_tree(*call) == ssd.SSD_OK
+    assert torch.equal(out, want) and int(status) == 0

@@ -88,6 +88,18 @@ def test_attend_tree_refuses(ssd):
     assert call(T=0, q=None, out=None, mask=None) == ssd.SSD_OK
 
 
+def test_timeout_check_refuses(ssd):
+    n = ssd.lib().ssd_kv_tree_workspace_size()
+
+    def call(withheld, dtype=ssd.SSD_BF16, D=128, q=P):
+        return ssd.lib().ssd_check_tree_timeout(withheld, q, dtype, 4096, P, P, P, P, 10, 16, 32, 8, D, P, 4, P, P, P, 2, 3, 2,
+                                                ctypes.c_float(0.1), 0, P, P, n, None, None)
+    for withheld in (-1, 0, 6):
+        assert call(withheld) == ssd.SSD_ERR_INVALID_ARG
+    assert call(1, q=None) == ssd.SSD_ERR_INVALID_ARG
+    assert call(1, dtype=ssd.SSD_F32) == ssd.SSD_ERR_DTYPE
+
+
 def test_turns_hold_the_frequencies(ssd):
     f = [0.0, 1.0, 1e-4, 2 * math.pi * 0.75, -1.0, 10.0, 2 * math.pi * 5e-20]
     got = ssd.rope_turns(f, device="cpu")
