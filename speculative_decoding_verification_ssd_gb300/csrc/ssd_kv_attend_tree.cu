@@ -1350,8 +1350,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             for (int x = max(0, v - F::kValues); x < v; ++x) drain_phase<kWait>(&S.v_full[x % F::kValues], (x / F::kValues) & 1);
         }
         if (warp == 13) {
-            if (lane == 0) tc::mma_commit(&S.drained);
-            __syncwarp();
+            // (of the thread that issued them: a commit is of its own thread's products)
+            tc::warp_mma_commit(&S.drained);
             drain_phase<kWait>(&S.drained, 0);
         }
     }
