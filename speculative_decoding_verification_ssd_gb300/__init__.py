@@ -797,6 +797,13 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale, dev):
                    _at(k_scale, "k_scale", torch.float32, blocks, dev), _at(v_scale, "v_scale", torch.float32, blocks, dev))
 
 
+def _int32(x, name) -> int:
+    x = int(x)
+    if not -1 << 31 <= x < 1 << 31:     # ctypes would drop the upper bits
+        raise ValueError(f"{name} does not fit in 32 bits")
+    return x
+
+
 def _tokens(t, name, H, D, dev):
     """(T, heads, token stride) of a [T, H, D] tensor whose heads and channels are contiguous."""
     T, heads, width = _cuda(t, name, 3, dev)
@@ -857,7 +864,7 @@ def ssd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, kv
     _check(lib().ssd_kv_attend(
         q.data_ptr(), _KV_DTYPES[q.dtype], ld, *cache, N, P, Hq, Hkv, D,
         _at(block_table, "block_table", i32, (B, max_blocks), dev), max_blocks, _at(cu_new, "cu_new", i32, (B + 1,), dev),
-        _at(kv_len, "kv_len", i32, (B,), dev), B, T, int(max_new), float(sm_scale), int(window),
+        _at(kv_len, "kv_len", i32, (B,), dev), B, T, _int32(max_new, "max_new"), float(sm_scale), _int32(window, "window"),
         _at(out, "out", q.dtype, (T, Hq, D), dev), _at(workspace, "workspace", torch.uint8, workspace.shape, dev),
         workspace.numel(), _status_at(dev_status, dev), _stream_at(stream, q)), "ssd_kv_attend")
     if stream is not None:
@@ -976,9 +983,11 @@ def ssd_tree_plan(parent, cu_new, seq_len, max_new: int, *, out=None, dev_status
     i32, dev = torch.int32, _device_of(parent, "parent")
     T, = _cuda(parent, "parent", 1, dev)
     B, = _cuda(seq_len, "seq_len", 1, dev)
-    W = (int(max_new) + 31) // 32
+    max_new = int(max_new)
+    W = (max_new + 31) // 32
     if W < 1:
         raise ValueError("max_new must be positive")
+    _check(SSD_OK if max_new <= SSD_TREE_MAX else SSD_ERR_UNSUPPORTED, "ssd_tree_plan")      # (before a mask of that size is made)
     o, made = ({} if out is None else dict(out)), []
     for name, shape in (("positions", (T,)), ("mask", (T, W))):
         if o.get(name) is None:
@@ -986,7 +995,7 @@ def ssd_tree_plan(parent, cu_new, seq_len, max_new: int, *, out=None, dev_status
             made.append(o[name])
     _check(lib().ssd_tree_plan(
         _at(parent, "parent", i32, (T,), dev), _at(cu_new, "cu_new", i32, (B + 1,), dev), _at(seq_len, "seq_len", i32, (B,), dev), B, T,
-        int(max_new), _at(o["positions"], "positions", i32, (T,), dev), _at(o["mask"], "mask", i32, (T, W), dev),
+        max_new, _at(o["positions"], "positions", i32, (T,), dev), _at(o["mask"], "mask", i32, (T, W), dev),
         _status_at(dev_status, dev), _stream_at(stream, parent)), "ssd_tree_plan")
     if stream is not None:
         _on(stream, *made)
@@ -1024,8 +1033,8 @@ def ssd_kv_attend_tree(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_ne
     _check(lib().ssd_kv_attend_tree(
         q.data_ptr(), _KV_DTYPES[q.dtype], ld, *cache, N, P, Hq, Hkv, D,
         _at(block_table, "block_table", i32, (B, max_blocks), dev), max_blocks, _at(cu_new, "cu_new", i32, (B + 1,), dev),
-        _at(kv_len, "kv_len", i32, (B,), dev), _at(mask, "mask", i32, (T, (int(max_new) + 31) // 32), dev), B, T, int(max_new),
-        float(sm_scale), int(window), _at(out, "out", q.dtype, (T, Hq, D), dev),
+        _at(kv_len, "kv_len", i32, (B,), dev), _at(mask, "mask", i32, (T, (int(max_new) + 31) // 32), dev), B, T,
+        _int32(max_new, "max_new"), float(sm_scale), _int32(window, "window"), _at(out, "out", q.dtype, (T, Hq, D), dev),
         _at(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(), _status_at(dev_status, dev),
         _stream_at(stream, q)), "ssd_kv_attend_tree")
     if stream is not None:
@@ -1042,6 +1051,7 @@ def ssd_tree_accept(parent, tokens, sampled, cu_new, max_new: int, max_path: int
     J, of_t, of_b = int(max_path), (T,), (B,)
     if B < 0 or J < 0:
         raise ValueError("cu_new must be [B+1] and max_path positive")
+    _check(SSD_OK if J <= SSD_MAX_K + 1 else SSD_ERR_INVALID_ARG, "ssd_tree_accept")         # (before a path of that size is made)
     o, made = ({} if out is None else dict(out)), []
     for name, shape in (("accept_len", of_b), ("bonus", of_b), ("path", (B, J))):
         if o.get(name) is None:
@@ -1049,7 +1059,7 @@ def ssd_tree_accept(parent, tokens, sampled, cu_new, max_new: int, max_path: int
             made.append(o[name])
     _check(lib().ssd_tree_accept(
         _at(parent, "parent", i32, of_t, dev), _at(tokens, "tokens", i32, of_t, dev), _at(sampled, "sampled", i32, of_t, dev),
-        _at(cu_new, "cu_new", i32, (B + 1,), dev), B, T, int(max_new), J, _at(o["accept_len"], "accept_len", i32, of_b, dev),
+        _at(cu_new, "cu_new", i32, (B + 1,), dev), B, T, _int32(max_new, "max_new"), J, _at(o["accept_len"], "accept_len", i32, of_b, dev),
         _at(o["bonus"], "bonus", i32, of_b, dev), _at(o["path"], "path", i32, (B, J), dev), _status_at(dev_status, dev),
         _stream_at(stream, parent)), "ssd_tree_accept")
     if stream is not None:

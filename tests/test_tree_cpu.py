@@ -198,6 +198,35 @@ def test_binding_refuses_host_tensors_and_shapes(ssd, monkeypatch):
             call()
 
 
+@pytest.mark.parametrize("size", [1 << 31, 1 << 32, (1 << 32) + 5, 1 << 40, -(1 << 32) + 5])
+def test_binding_refuses_sizes_beyond_32_bits(ssd, monkeypatch, size):
+    """Not their lower bits in their place, and not a tensor of that size on the way."""
+    class Lib:
+        def __getattr__(self, name):
+            def launch(*a):
+                raise AssertionError(f"{name} was called")
+            return launch
+
+    monkeypatch.setattr(ssd, "lib", Lib)
+    monkeypatch.setattr(ssd, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(ssd, "_current_stream", lambda device: 0)
+    monkeypatch.setattr(ssd, "strerror", str)
+
+    def t(shape, dtype=torch.int32):
+        return torch.zeros(shape, dtype=dtype).as_subclass(Somewhere)
+    f32, b16, u8 = torch.float32, torch.bfloat16, torch.uint8
+    cache = (t((3, 2, 16, 64), u8), t((3, 2, 16, 64), u8), t((3, 2), f32), t((3, 2), f32))
+    q, lens = t((5, 4, 64), b16), (t((2, 4)), t(3), t(2))
+    kw = dict(out=t((5, 4, 64), b16), workspace=t(256, u8))
+    for call in (lambda: ssd.ssd_kv_attend(q, *cache, *lens, 4, 1.0, window=size, **kw), lambda: ssd.ssd_kv_attend(q, *cache, *lens, size, 1.0, **kw),
+                 lambda: ssd.ssd_kv_attend_tree(q, *cache, *lens, t((5, 1)), 4, 1.0, window=size, **kw),
+                 lambda: ssd.ssd_kv_attend_tree(q, *cache, *lens, t((5, 1)), size, 1.0, **kw),
+                 lambda: ssd.ssd_tree_plan(t(5), t(3), t(2), size), lambda: ssd.ssd_tree_accept(t(5), t(5), t(5), t(3), size, 3),
+                 lambda: ssd.ssd_tree_accept(t(5), t(5), t(5), t(3), 4, size)):
+        with pytest.raises((ValueError, ssd.SSDError)):
+            call()
+
+
 def test_plain_forms_of_a_small_tree():
     """     0 -> 1 -> 3 -> 5,  0 -> 2 -> 4"""
     parent = [-1, 0, 0, 1, 2, 3]
