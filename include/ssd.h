@@ -533,7 +533,9 @@ int ssd_kv_append(const void *k, const void *v, int dtype, int64_t k_stride, int
  * unchanged; a query enters as the sum of two (bf16) or three (fp16) e4m3 digits,
  * exact down to 2^-9 (2^-6) of its row's largest channel and to 2^-17 of that below;
  * a softmax weight is rounded to two or three digits (2^-8 or 2^-12 of itself, 2^-18
- * or 2^-23 of the largest weight near it).
+ * or 2^-23 of the largest weight near it; the value scales of its step's pages, at most
+ * 256 keys, count for that, seen or not).  Scores times log2(e) are to stay below 2^20:
+ * their differences are taken in fp32.
  * workspace: ssd_kv_workspace_size() bytes, 256-byte aligned, zero-filled before
  *   its first use and left ready by each call (not by one that reported
  *   SSD_DEV_TIMEOUT: zero it again); calls that share one must not overlap on the
@@ -630,7 +632,10 @@ int ssd_tree_plan(const int32_t *parent, const int32_t *cu_new, const int32_t *s
  * 32) (ssd_tree_plan, or any mask); with window > 0 only to the last `window` of those.
  * A mask whose bits j <= i are all set gives ssd_kv_attend's function.
  * Everything else (layouts, scales, lengths, reports) as ssd_kv_attend, with max_new <=
- * SSD_TREE_MAX.
+ * SSD_TREE_MAX, but for the weights: a softmax weight times its value scale is held as one half
+ * for both types, 2^-11 of itself, and off by 2^-30 of the largest of those products that its
+ * token attends to below 2^-19 of it.  Scores of any size that fp32 holds, and pages of any value
+ * scale next to others.
  * workspace: ssd_kv_tree_workspace_size() bytes, used as ssd_kv_attend's.
  */
 size_t ssd_kv_tree_workspace_size(void);

@@ -29,19 +29,21 @@
 // the CTA that brings an item's last part joins them all.
 //
 // What bounds it (32/8 heads of 128, bf16, cold caches): 64 sequences of 37 nodes and 40 to 8191 keys
-// 267 us, 578 MB of cache (85 us at the copy's rate) and two tiles for 148 rows; 4 of 9 nodes and 90001
-// to 131072 keys 222 us (134 us of bytes); one of 37 nodes over 1074 keys 44 us.  DRAM is at 29% and
-// 52%, the tensor pipe at 43%, issue at 39% and 44%: a step of two tiles would take the tensor cores
+// 273 us, 578 MB of cache (85 us at the copy's rate) and two tiles for 148 rows; 4 of 9 nodes and 90001
+// to 131072 keys 226 us (134 us of bytes); one of 37 nodes over 1074 keys 46 us.  DRAM is at 28% and
+// 52%, the tensor pipe at 42%, issue at 38% and 44%: a step of two tiles would take the tensor cores
 // 2144 clocks and takes some 3700, in which a stream's scores, weights and output follow one another
-// through four softmax warps, and of an item's time as much as five steps is its start.  The form that
-// ssd_kv_attend has (keys as the long side) takes 167, 425 and 833 us for 64 sequences of 9, 32 and 64
-// tokens over these lengths, this one 163, 177 and 286; over the second case's very long sequences
-// that form is the faster one with its 9 tokens (202 us).
+// through four softmax warps, and of an item's time as much as five steps is its start.  What binds the
+// second case is not known: half the softmax chain (rows in two lanes, below) took 4 us off it.  The form
+// that ssd_kv_attend has (keys as the long side) takes 180, 439 and 861 us for 64 sequences of 9, 32 and
+// 64 tokens over these lengths, this one 167, 181 and 290; over the second case's very long sequences
+// that form is the faster one with its 9 tokens (200 us).
 //
-// Clocks of one of a stream's passes, two tiles: 750 from the last weights to the next wait, 800 in it,
-// 600 for the maximum, 1650 for the weights, 165 to store them; the MMA warp needs 1300 for its part.
+// Clocks of one of a stream's passes, two tiles, when weights were relative to their step's value scales
+// (which took 2% less): 750 from the last weights to the next wait, 800 in it, 600 for the maximum, 1650
+// for the weights, 165 to store them; the MMA warp needs 1300 for its part.
 //
-// Tried and not faster: scores of 64 keys in two buffers a stream, so that a product runs beside the
+// Tried and not faster (267, 222 and 44 us then): scores of 64 keys in two buffers a stream, so that a product runs beside the
 // next pass's weights (323 us for the first case; 276 and 234 for the first two with both streams'
 // products issued together, when the softmax warps bound every pass: a pass's fixed work comes twice);
 // the next item's queries made during this one's steps (275; the same warps make V's halves); weights
@@ -49,8 +51,10 @@
 // instruction group (267); another slot for values in place of one for keys (269, and 349 in place of
 // 302 in fp16); boxes fetched into L2 ahead of their copies (272); steps handed over two at a time
 // (284); items of up to 64 rows with each row in two lanes, which take half the keys each (218 for
-// the second case's 222, but 284 for the first, whose items are larger, by code alone); whole rows
-// in straight-line code, slower by the instruction caches.
+// the second case's 222, but 284 for the first, whose items are larger, by code alone, and 190 to 214
+// for 165 with 64 trees of 9); whole rows in straight-line code, slower by the instruction caches.  A sum
+// of the weights as rounded would cancel their common rounding, and lose keys of small value scales whose
+// weights are none as halves.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -7,8 +7,9 @@
 // another bring its scale along, and where that asks for a larger one the page's earlier rows are
 // stored again under it, as the append does.
 //
-// Bound by latency: the path, the table, the scales and the rows are read one after another, each a
-// miss when the caches are cold.  256 sequences of 8 heads of 128, paths of up to 9, move 4.7 MB at
+// Bound by latency: the accepted length, the path, the table, the sources' scales and rows, and the
+// destination's scale are read one after another, each a miss when the caches are cold (the path need
+// not wait for the length, nor the last scale for the rows).  256 sequences of 8 heads of 128, paths of up to 9, move 4.7 MB at
 // most (0.7 us at the copy's rate): 11.4 us with cold caches, of which an almost empty kernel makes 7,
 // and one sequence of 4 heads 9.3.  The steps of 4 or 8 tokens end with the path: a form that went
 // over all SSD_MAX_K took 15.5 us.  72 or 64 registers, with which every warp is resident at once, and

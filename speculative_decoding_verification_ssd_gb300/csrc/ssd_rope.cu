@@ -9,7 +9,8 @@
 //
 // A lane holds 16 channels of a head in two runs of 8: of halves the runs that are turned with each
 // other, of neighbours runs that hold their own pairs, so that no value crosses lanes but the sum of
-// squares.  Sums and the rotation are fp32, two to an instruction, rounded once at the store.
+// squares.  Sums and the rotation are fp32, two to an instruction, rounded once at the store; a head
+// whose squares fp32 does not hold is done over at the end.
 //
 // A warp takes a token, D/16 lanes a head, and goes over the heads with the next pass's on their way:
 // the angles (8 sincospi per lane) serve all of a token's heads.  Only while tokens alone would leave
@@ -18,8 +19,8 @@
 // were most of its loads (44 us, 40 with them here and 48 with both heads' held in registers).
 //
 // Bound by bytes: 9472 tokens of 32 + 8 heads of 128 in bf16 read and write 194 MB, 29 us at the
-// copy's rate; 38 us, 5.1 TB/s, with the launch and a last wave that is not full (3040 to 3648 warps
-// are resident).  In fp32, half as many tokens, 34 to 38 us.  Tried: runs of 4 channels, half the
+// copy's rate; 39 us, 5.0 TB/s, with the launch and a last wave that is not full (3648 warps are
+// resident).  In fp32, half as many tokens, 34 to 38 us.  Tried: runs of 4 channels, half the
 // registers (46 us); two and four passes on their way (42 and 69); 1, 5 and 8 blocks per SM asked
 // for (40, 40, 44).  One token 7 to 9 us, a launch's own time.
 #include <cuda_bf16.h>
