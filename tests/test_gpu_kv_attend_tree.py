@@ -513,7 +513,7 @@ def test_value_scales_of_all_sizes(ssd):
             check_seen(c, c.run(ssd, window=window), window)
 
 
-@pytest.mark.parametrize("size", [64.0, 2.0 ** 13, 2.0 ** 20, 2.0 ** 27, 1e15, 1e28, 1e31])
+@pytest.mark.parametrize("size", [40.0, 64.0, 2.0 ** 13, 2.0 ** 20, 2.0 ** 27, 1e15, 1e28, 1e31])
 @pytest.mark.parametrize("sign", [1, -1])
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_scores_of_any_size(ssd, dtype, size, sign):
@@ -582,3 +582,19 @@ def test_waits_that_run_out_end_the_launch(ssd, n, withheld):
     out.zero_()
     assert ssd.lib().ssd_kv_attend_tree(*call) == ssd.SSD_OK
     assert torch.equal(out, want) and int(status) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("times", [0.12, 0.49, 0.51, 2.0, 100.0])
+def test_scores_as_large_as_their_digits_can_make_them(ssd, dtype, D, times):
+    """Every channel of queries and keys at the end of its range, alike or opposite: no weight leaves fp16's."""
+    c = Case(43, [(700, 30), (90, 5)], 4, 2, D, 64, dtype)
+    c.q = torch.where(c.q > 0, 255.0, -255.0).to(dtype)
+    sign = np.where(np.asarray(c.q[0, ::2].double()) > 0, 0, 0x80).astype(np.uint8)             # of each cache head's first query
+    level = c.rng.choice([0x7E, 0x7D, 0x70], c.k.shape[:3] + (1,)) | (c.rng.random(c.k.shape[:3] + (1,)) < 0.5) * 0x80
+    c.k[:] = (level.astype(np.uint8) ^ sign[None, :, None, :])
+    c.q[:, ::2] = c.q[0, ::2]
+    c.ks[:] = 1.0
+    c.scale = times / float(np.log2(np.e))
+    c.check(ssd)
