@@ -84,7 +84,8 @@ constexpr float kLag = 10.f, kUp = 15.f - kLag, kUnit = 32.f;  // (2^kUp)
 // 2^-kMostUnit to 2^kMostUnit, so that the sum's terms down to 2^-(2 kMostUnit) are normal in fp32, and no score can
 // be above 2^22.8: three roundings of 1/4 leave a weight below the largest half.  (A product of digits is at most 2^8 448
 // kMostHead = 2^23.8, and mostly 2^8 less, which makes those roundings 2^-10.)  The long form's exponents are differences of
-// scores, exact whatever their size, and a warp goes back to the short one while that is so to 2^-12.
+// scores, exact whatever their size, and a warp goes back to the short one while that is so to 2^-12.  It takes twice as long
+// (the cases above 583, 464 and 63 us in place of 273, 226 and 46).
 constexpr float kMostUnit = 50.f, kMostFactor = 0.5f, kMostScore = 8192.f;
 // In the long form the sum is relative to the scores' maximum, and what the weights are relative to is not below 2^kLow
 // (and kLag less) of that, so that it stays a normal number whatever the value scales.
