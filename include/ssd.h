@@ -533,8 +533,8 @@ int ssd_kv_append(const void *k, const void *v, int dtype, int64_t k_stride, int
  * unchanged; a query enters as the sum of two (bf16) or three (fp16) e4m3 digits,
  * exact down to 2^-9 (2^-6) of its row's largest channel and to 2^-17 of that below;
  * a softmax weight is rounded to two or three digits (2^-8 or 2^-12 of itself, 2^-18
- * or 2^-23 of the largest weight near it; the value scales of its step's pages, at most
- * 256 keys, count for that, seen or not).  Scores times log2(e) are to stay below 2^20:
+ * or 2^-23 of the largest weight times value scale near it, among pages whose value
+ * scales are within 2^4 of each other).  Scores times log2(e) are to stay below 2^20:
  * their differences are taken in fp32.
  * workspace: ssd_kv_workspace_size() bytes, 256-byte aligned, zero-filled before
  *   its first use and left ready by each call (not by one that reported

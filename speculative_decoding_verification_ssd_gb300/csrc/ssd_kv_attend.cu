@@ -64,6 +64,7 @@ constexpr int kMaxHead = 128;
 constexpr int kSeqsInside = 256;   // sequences whose prefix sums every CTA makes itself
 constexpr int kMaxPairs = 1 << 18;  // (sequence, row block) pairs of a call with longer items
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNear = 1.f / 16;  // value scales of one step are from the largest down to this of it
 
 struct Workspace {
     float o[2 * kMaxCtas][kMaxRows][kMaxHead];
@@ -409,6 +410,70 @@ __device__ __forceinline__ void reduce_lanes(float (&v)[kN], int lane, Op op) {
             v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], o));
         }
     }
+}
+
+// What the scout makes of steps whose pages' value scales are far apart: a step each for those near the largest, then for
+// those near the largest of the rest, and so on, in which the others are not there: a row may attend to them alone, or give
+// them its largest weights.  (One that is not finite goes first, one of 0 by itself.)  Steps from s on; returns the next.  Rare,
+// and apart from the scout's loop, as a part of which it slowed every step (64 sequences of 5 tokens over 3 to 8191 keys 124
+// us a call, 108 so and without it; 111 with its arguments by reference).
+struct Far {
+    int key0, t0, n, items, page, pages, common_from, common_to;
+    float ks, vs;
+    bool there;
+};
+template <class F>
+__device__ __noinline__ int parts_of_steps(const AttendParams &P, Shared<F::R> &S, Part part, Far v, int s) {
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31, my_step = lane / v.pages, my_page = lane % v.pages;
+    const uint32_t of_step = v.pages == 32 ? kAll : (1u << v.pages) - 1u;
+    const bool finite = fabsf(v.vs) <= 3.402823466e38f;
+    const uint32_t odd_all = __ballot_sync(kAll, !finite);
+#pragma unroll 1
+    for (int i = 0; i < v.n; ++i) {
+        bool left = my_step == i && v.there;  // the lane's page is still to come
+#pragma unroll 1
+        for (bool begins = true, ends = false; !ends; begins = false, ++s) {
+            float unit = left && finite ? fabsf(v.vs) : 0.f;
+            for (int o = 1; o < v.pages; o <<= 1) unit = fmaxf(unit, __shfl_xor_sync(kAll, unit, o));
+            const bool now = left && !(fabsf(v.vs) < unit * kNear);
+            left &= !now;
+            ends = !__any_sync(kAll, left);
+            const uint32_t mask = (__ballot_sync(kAll, now) >> (i * v.pages)) & of_step;
+            const uint32_t e = min(max(__float_as_uint(unit) >> 23, 8u), 254u);
+            const float f = finite ? v.vs * __uint_as_float((261u - e) << 23) : __int_as_float(0x7FC00000);
+            const int slot = s % kSteps;
+            if (s >= kSteps) wait_phase(&S.step_free[slot], static_cast<uint32_t>((s / kSteps - 1) & 1), &S.gave_up);
+            if (__any_sync(kAll, *static_cast<volatile int *>(&S.gave_up))) return s;
+            Step &st = S.step[slot];
+            if (my_step == i) {
+                st.page[my_page] = v.page;
+                st.scale[my_page] = now ? make_float2(v.ks, f) : make_float2(0.f, 0.f);
+                if (my_page == 0) {
+                    const int k0 = v.key0 + (v.t0 + i) * F::kStep;
+                    st.live = 1;
+                    st.first = begins && v.t0 + i == 0;
+                    st.last = ends && v.t0 + i == part.steps - 1;
+                    st.plain = mask == of_step && k0 >= v.common_from && k0 + F::kStep - 1 <= v.common_to;
+                    st.odd = ((odd_all >> (i * v.pages)) & of_step) != 0;
+                    st.key0 = k0;
+                    st.subs = k0 + kTile < part.stop ? F::kSub : 1;
+                    st.start = part.start, st.stop = part.stop;
+                    st.common_from = v.common_from, st.common_to = v.common_to;
+                    st.there = static_cast<int32_t>(mask);
+                    st.item = v.items % kItems;
+                    st.first_cta = part.first_cta, st.parts = part.parts;
+                    st.seq = part.b, st.head = part.head, st.row0 = part.row0, st.rows = part.rows;
+                    st.token0 = part.first, st.pos0 = part.pos0;
+                    st.part_key0 = v.key0;
+                    st.v_unit = __uint_as_float((e - 7u) << 23);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.step_full[slot]);
+        }
+    }
+    return s;
 }
 
 // Shared memory besides the ring of K and V slots, which gets the rest.
@@ -1139,7 +1204,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 const float f = finite ? vs * __uint_as_float((261u - e) << 23) : __int_as_float(0x7FC00000);
                 const uint32_t there_all = __ballot_sync(kAll, there), odd_all = __ballot_sync(kAll, !finite);
                 const uint32_t of_step = pages == 32 ? kAll : (1u << pages) - 1u;
-                const int n = min(at_once, part.steps - t0);
+                int n = min(at_once, part.steps - t0);
+                if (__any_sync(kAll, there && fabsf(vs) < top * kNear)) {
+                    s = parts_of_steps<F>(P, S, part, {key0, t0, n, items, page, pages, common_from, common_to, ks, vs, there}, s);
+                    n = 0;
+                }
                 for (int i = 0; i < n; ++i, ++s) {
                     const int slot = s % kSteps;
                     if (s >= kSteps) wait(&S.step_free[slot], (s / kSteps - 1) & 1);

@@ -35,7 +35,7 @@
 // 2144 clocks and takes some 3700, in which a stream's scores, weights and output follow one another
 // through four softmax warps, and of an item's time as much as five steps is its start.  What binds the
 // second case is not known: half the softmax chain (rows in two lanes, below) took 4 us off it.  The form
-// that ssd_kv_attend has (keys as the long side) takes 180, 439 and 861 us for 64 sequences of 9, 32 and
+// that ssd_kv_attend has (keys as the long side) takes 170, 427 and 836 us for 64 sequences of 9, 32 and
 // 64 tokens over these lengths, this one 167, 181 and 290; over the second case's very long sequences
 // that form is the faster one with its 9 tokens (200 us).
 //

@@ -381,3 +381,83 @@ def test_a_batch_ends_where_its_token_counts_fall(ssd, n, rest):
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         assert torch.equal(c.run(ssd, dev_status=status), want)
         assert int(status) == ssd.SSD_DEV_BAD_LENGTH
+
+
+def seen_parts(c, window=0):
+    """ref.attend's arrays, and the largest value that a token attends to times its weight: 448 times the largest of those products
+    with the scale alone."""
+    ks, vs = c.ks.astype(np.float64), c.vs.astype(np.float64)
+    want = ref.attend(c.q.double().numpy(), VALUES[c.k], VALUES[c.v], ks, vs, c.table, c.cu, c.kv, c.P, c.scale, window)
+    T, Hq, _ = c.q.shape
+    G, most = Hq // c.k.shape[1], np.zeros((T, Hq, 1))
+    for b in range(len(c.kv)):
+        n = c.cu[b + 1] - c.cu[b]
+        for i in range(n):
+            last = c.kv[b] - n + i
+            js = np.arange(max(0, last + 1 - window) if window else 0, last + 1)
+            pages, rows = c.table[b][js // c.P], js % c.P
+            for h in range(Hq):
+                s = c.scale * ((VALUES[c.k[pages, h // G, rows]] * ks[pages, h // G][:, None]) @ c.q[c.cu[b] + i, h].double().numpy())
+                p = np.exp(s - s.max())
+                most[c.cu[b] + i, h] = 448 * np.max(p / p.sum() * np.abs(vs[pages, h // G]))
+    return want, most
+
+
+def check_seen(c, got, window=0, rows=slice(None)):
+    """As ref.attend_bound, with what the digits' end is relative to taken from the token's own keys: digits end at 2^-18 or 2^-23 of the
+    largest weight times value scale of a step, whose scales are within 2^4 of each other, or at 2^-14 and 2^-19 of the largest
+    that the token gives in that step, once for each of its keys."""
+    (out, weight, score, largest), most = seen_parts(c, window)
+    half = torch.finfo(c.dtype).eps / 2
+    end = 2.0 ** -14 if c.dtype is BF else 2.0 ** -19
+    keys = 256 * -(-c.kv.max() // 256)
+    bound = ref.attend_bound(c.dtype, c.D, out, weight, score, 0 * largest) + (1 + half) * end * keys * most
+    held = np.abs(out) + bound <= torch.finfo(c.dtype).max          # (beyond that the type has an infinity)
+    with np.errstate(invalid="ignore"):
+        over = np.where(held, np.abs(got.double().cpu().numpy() - out) - bound, -1.0)[rows]
+    assert over.max() <= 0, (over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("times", [12, 30, 60, 100])
+@pytest.mark.parametrize("n,window", [(40, 0), (40, 9), (5, 0)])
+def test_a_large_value_scale_concerns_those_alone_that_see_it(ssd, dtype, times, n, window):
+    """The last tokens' page is of far larger scale, and the others do not attend to it: what those get does not depend on it."""
+    c = Case(51, [(290, n), (300, 3)], 4, 2, 64, 16, dtype)         # (288 on is page 18)
+    want = c.run(ssd, window=window)
+    c.vs[c.table[0, 18]] *= np.float32(2.0 ** times)
+    got = c.run(ssd, window=window)
+    others = slice(0, n - 2)
+    check_seen(c, got, window, others if dtype == FP else slice(None))
+    off = (got[others].double() - want[others].double()).abs()
+    # both are within the weights' digits of the same values, and half a step of the type
+    assert bool((off <= 2 * 2.0 ** -8 * want[others].double().abs().amax(dim=2, keepdim=True)).all())
+    assert torch.equal(got[n:], want[n:])
+
+
+@pytest.mark.parametrize("times", [12, 30, 60])
+@pytest.mark.parametrize("page", [0, 5, 17])
+def test_the_largest_score_next_to_the_largest_value_scale(ssd, times, page):
+    """A page of far larger value scale, whose keys all score 2^-(times + 20) of the others: the others' weights keep their bits."""
+    for dtype in (BF, FP):
+        c = Case(52, [(300, 20), (77, 7)], 4, 2, 64, 16, dtype)
+        p = c.table[0, page]
+        c.q[:, :, 5] = 4.0
+        c.k[..., 5] = 0
+        c.k[p, ..., 5] = 0xFE                                    # -448
+        c.ks[p] = 0.02
+        c.scale = (times + 20) * float(np.log(2.0)) / (4 * 448 * 0.02)
+        c.vs[p] = 0.02 * 2.0 ** times
+        check_seen(c, c.run(ssd))
+
+
+@pytest.mark.parametrize("P", [16, 64, 128])
+def test_value_scales_of_all_sizes(ssd, P):
+    """From 2^-100 to 2^100 in one step, none and negative ones among them, in items of several row blocks and of one token."""
+    for n in (1, 40):
+        c = Case(53, [(1000, n), (200, 9)], 8, 2, 64, P, BF, spread=4.0)
+        c.vs *= (2.0 ** np.random.default_rng(P).uniform(-100, 100, c.vs.shape)).astype(np.float32)
+        c.vs[c.table[0, 1]] = 0.0
+        c.vs[c.table[0, 2]] *= -1
+        for window in (0, 130):
+            check_seen(c, c.run(ssd, window=window), window)
