@@ -29,19 +29,19 @@
 // the CTA that brings an item's last part joins them all.
 //
 // What bounds it (32/8 heads of 128, bf16, cold caches): 64 sequences of 37 nodes and 40 to 8191 keys
-// 273 us, 578 MB of cache (85 us at the copy's rate) and two tiles for 148 rows; 4 of 9 nodes and 90001
-// to 131072 keys 226 us (134 us of bytes); one of 37 nodes over 1074 keys 46 us.  DRAM is at 28% and
-// 52%, the tensor pipe at 42%, issue at 38% and 44%: a step of two tiles would take the tensor cores
+// 269 us, 578 MB of cache (85 us at the copy's rate) and two tiles for 148 rows; 4 of 9 nodes and 90001
+// to 131072 keys 228 us (134 us of bytes); one of 37 nodes over 1074 keys 44 us.  DRAM is at 29% and
+// 51%, the tensor pipe at 43%, issue at 40% and 45%: a step of two tiles would take the tensor cores
 // 2144 clocks and takes some 3700, in which a stream's scores, weights and output follow one another
 // through four softmax warps, and of an item's time as much as five steps is its start.  What binds the
 // second case is not known: half the softmax chain (rows in two lanes, below) took 4 us off it.  The form
 // that ssd_kv_attend has (keys as the long side) takes 170, 427 and 836 us for 64 sequences of 9, 32 and
-// 64 tokens over these lengths, this one 167, 181 and 290; over the second case's very long sequences
+// 64 tokens over these lengths, this one 163, 177 and 286; over the second case's very long sequences
 // that form is the faster one with its 9 tokens (200 us).
 //
 // Clocks of one of a stream's passes, two tiles, when weights were relative to their step's value scales
-// (which took 2% less): 750 from the last weights to the next wait, 800 in it, 600 for the maximum, 1650
-// for the weights, 165 to store them; the MMA warp needs 1300 for its part.
+// (267 us): 750 from the last weights to the next wait, 800 in it, 600 for the maximum, 1650 for the
+// weights, 165 to store them; the MMA warp needs 1300 for its part.
 //
 // Tried and not faster (267, 222 and 44 us then): scores of 64 keys in two buffers a stream, so that a product runs beside the
 // next pass's weights (323 us for the first case; 276 and 234 for the first two with both streams'
@@ -85,7 +85,7 @@ constexpr float kLag = 10.f, kUp = 15.f - kLag, kUnit = 32.f;  // (2^kUp)
 // be above 2^22.8: three roundings of 1/4 leave a weight below the largest half.  (A product of digits is at most 2^8 448
 // kMostHead = 2^23.8, and mostly 2^8 less, which makes those roundings 2^-10.)  The long form's exponents are differences of
 // scores, exact whatever their size, and a warp goes back to the short one while that is so to 2^-12.  It takes twice as long
-// (the cases above 583, 464 and 63 us in place of 273, 226 and 46).
+// (the cases above 587, 472 and 63 us in place of 269, 228 and 44).
 constexpr float kMostUnit = 50.f, kMostFactor = 0.5f, kMostScore = 8192.f;
 // In the long form the sum is relative to the scores' maximum, and what the weights are relative to is not below 2^kLow
 // (and kLag less) of that, so that it stays a normal number whatever the value scales.
@@ -503,6 +503,83 @@ __device__ __forceinline__ void row_keys(const TreeParams &P, const Row &r, int 
     }
 }
 
+// A row of O times f.
+template <class F>
+__device__ __forceinline__ void scale_output(uint32_t o_at, float f) {
+#pragma unroll 1
+    for (int c = 0; c < F::D; c += 16) {
+        uint32_t o[16];
+        tc::tmem_load(o, o_at + c);
+        tc::tmem_wait_load(o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tc::tmem_store(o_at + c, o);
+    }
+}
+
+// The long form of a step's weights; out of the kernel's loop, whose code it would lengthen (273, 226 and 46 us for the cases
+// above).
+struct State {
+    float m, l, u;
+};
+template <class F>
+__device__ __noinline__ State long_weights(const Step &st, State row, float qf, bool first, uint32_t sees_0, uint32_t sees_1, uint32_t sees_2,
+                                           uint32_t sees_3, uint32_t s_at, uint32_t o_at) {
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    const uint32_t sees[4] = {sees_0, sees_1, sees_2, sees_3};
+    float m = row.m, l = row.l, u = row.u;
+    float x[16], to = m, largest = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 2 * kGroups; ++c) {  // the largest score and weight, then the weights
+        const int g = c & (kGroups - 1);
+        const float4 sc = st.scale[g];
+        const uint32_t bits = (g < 4 ? (g < 2 ? sees[0] : sees[1]) : (g < 6 ? sees[2] : sees[3])) >> (16 * (g & 1));
+        const float f = sc.x * qf;
+        if (c == kGroups) {
+            largest = fmaxf(largest, kLow);
+            if (first) {
+                m = to, u = largest;
+            } else {
+                const float up = to - m;
+                l *= ex2(-up);
+                m = to, u -= up;
+                const bool move = largest > u + kLag;
+                if (__any_sync(kAll, move)) {
+                    scale_output<F>(o_at, move ? ex2(u - largest) : 1.f);
+                    if (move) u = largest;
+                }
+            }
+        }
+        tc::tmem_load(x, s_at + 16 * g);
+        tc::tmem_wait_load(x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = (bits >> i) & 1 ? x[i] * f : -INFINITY;
+        if (c < kGroups) {
+            float top = x[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+            const float before = to;
+            to = fmaxf(to, top);
+            largest = fmaxf(largest - (to - before), (top - to) + sc.z);
+            continue;
+        }
+        const float e = sc.z + (kUp - u);
+        uint32_t w[8];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            float y = x[i] - m, z = x[i + 1] - m;
+            sum += ex2(y) + ex2(z);
+            // (not 0 times a scale that is not finite, of keys that the row does not attend to)
+            y = (bits >> i) & 1 ? copysignf(ex2(y + e), sc.y) : 0.f, z = (bits >> i) & 2 ? copysignf(ex2(z + e), sc.y) : 0.f;
+            w[i / 2] = two_of(__half(), y, z);
+        }
+        l += sum;
+        tc::tmem_store(s_at + 8 * g, w);
+    }
+    return {m, l, u};
+}
+
 // kOwn: a schedule of several row blocks to a sequence is made by every CTA (as a branch it cost the others 1%).
 // kChecked: the form of ssd_check_tree_timeout: in each CTA the third step's signal of role P.withheld is left out, so that
 // the waits for it run out, after kPollsChecked polls.
@@ -683,17 +760,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         return f <= 1.2e-38f ? 1.2e-38f : f;
                     };
                     some |= (sees[0] | sees[1] | sees[2] | sees[3]) != 0;
-                    auto scale_output = [&](float f) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t o[16];
-                            tc::tmem_load(o, o_at + c);
-                            tc::tmem_wait_load(o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tc::tmem_store(o_at + c, o);
-                        }
-                    };
                     // Loops of few instructions: straight-line code for a whole row of scores passes through the instruction
                     // caches each time, and the other roles' code with it.
                     if (ordinary) {
@@ -738,7 +804,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             const float to = move ? top : m, by = ex2(m - to);
                             l *= by;
                             m = to;
-                            scale_output(by);
+                            scale_output<F>(o_at, by);
                         }
                         // 2^s vs / 2^m is one power here, and the sum over 16 keys is divided by vs.
                         const float unit = kUp - m;
@@ -772,55 +838,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         }
                         l = fmaf(sums, 1.f / kUnit, l);
                     } else {
-                        float x[16], to = m, largest = -INFINITY;
-#pragma unroll 1
-                        for (int c = 0; c < 2 * kGroups; ++c) {  // the largest score and weight, then the weights
-                            const int g = c & (kGroups - 1);
-                            const float4 sc = st.scale[g];
-                            const uint32_t bits = (g < 4 ? (g < 2 ? sees[0] : sees[1]) : (g < 6 ? sees[2] : sees[3])) >> (16 * (g & 1));
-                            const float f = sc.x * qf;
-                            if (c == kGroups) {
-                                largest = fmaxf(largest, kLow);
-                                if (first) {
-                                    m = to, u = largest;
-                                } else {
-                                    const float up = to - m;
-                                    l *= ex2(-up);
-                                    m = to, u -= up;
-                                    const bool move = largest > u + kLag;
-                                    if (__any_sync(kAll, move)) {
-                                        scale_output(move ? ex2(u - largest) : 1.f);
-                                        if (move) u = largest;
-                                    }
-                                }
-                            }
-                            tc::tmem_load(x, s_at + 16 * g);
-                            tc::tmem_wait_load(x);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) x[i] = (bits >> i) & 1 ? x[i] * f : -INFINITY;
-                            if (c < kGroups) {
-                                float top = x[0];
-#pragma unroll
-                                for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
-                                const float before = to;
-                                to = fmaxf(to, top);
-                                largest = fmaxf(largest - (to - before), (top - to) + sc.z);
-                                continue;
-                            }
-                            const float e = sc.z + (kUp - u);
-                            uint32_t w[8];
-                            float sum = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                float y = x[i] - m, z = x[i + 1] - m;
-                                sum += ex2(y) + ex2(z);
-                                // (not 0 times a scale that is not finite, of keys that the row does not attend to)
-                                y = (bits >> i) & 1 ? copysignf(ex2(y + e), sc.y) : 0.f, z = (bits >> i) & 2 ? copysignf(ex2(z + e), sc.y) : 0.f;
-                                w[i / 2] = two_of(__half(), y, z);
-                            }
-                            l += sum;
-                            tc::tmem_store(s_at + 8 * g, w);
-                        }
+                        const State now = long_weights<F>(st, {m, l, u}, qf, first, sees[0], sees[1], sees[2], sees[3], s_at, o_at);
+                        m = now.m, l = now.l, u = now.u;
                         // back to one number for both, where that is in range
                         const bool none = m == kNothing;
                         far = __any_sync(kAll, !none && (fabsf(u) > kMostUnit || fabsf(m) > kMostScore));
